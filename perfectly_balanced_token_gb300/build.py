@@ -16,7 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libmoonep.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
-SOURCES = ["moonep.cu", "plan.cu", "move.cu", "gemm.cu"]
+SOURCES = ["moonep.cu", "plan.cu", "move.cu", "gemm.cu", "ops.cu", "router.cu", "mxfp4.cu",
+           "mxfp4_gemm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE,
          "--expt-relaxed-constexpr"]
@@ -38,7 +39,7 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
     os.makedirs(OUT_DIR, exist_ok=True)
     nvcc = _nvcc()
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
-    headers.append(os.path.join(INCLUDE, "moonep.h"))
+    headers += [os.path.join(INCLUDE, h) for h in ("moonep.h", "moonep_ops.h")]
     jobs = []
     objs = []
     for src in SOURCES:

@@ -1,0 +1,267 @@
+"""The router on the GPU against its 64-bit definition: ids, counts and token
+numbers exactly; gates, sums, loss and gradient within bounds derived below.
+
+Rounding: an exponential of x is off by at most (3 + 1.2 |x|) 2^-23 of itself
+(|x| <= 40 here where it counts: 51 ulp = 6.1e-6), a sum of n terms by n 2^-24
+of the sum of magnitudes in the worst order (a lane adds at most 128 of them and
+5 levels across the warp: 8e-6).  A gate takes an exponential, a sum and a
+division: RTOL = 2e-5 covers 6.1e-6 twice and 8e-6.  The balance sums also
+round each warp's part to 2^-shift, shift = 46 at these lengths: nothing beside
+ATOL = 1e-10.  A bf16 gradient adds 2^-9 of its value.
+"""
+import numpy as np
+import pytest
+import torch
+
+import perfectly_balanced_token_gb300 as mx
+from oracle import ops
+from tests.gpu_harness import ensure_library
+
+pytestmark = pytest.mark.gpu
+RTOL, ATOL = 2e-5, 1e-10
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    ensure_library()
+
+
+def draw(T, E, seed, dtype=torch.float32, ties=False, off=0, spread=2.0):
+    rng = np.random.default_rng(seed)
+    l = rng.standard_normal((T, E)) * spread
+    if ties:  # many equal logits, zeros of both signs among them
+        l = np.round(l)
+        l[l == 0] = np.where(rng.random((l == 0).sum()) < 0.5, -0.0, 0.0)
+    if off:
+        l[:, rng.permutation(E)[:off]] = -np.inf
+    return torch.from_numpy(l.astype(np.float32)).to(dtype)
+
+
+def forward(rd, logits, mask=None, loss=True, stream=None):
+    dev = "cuda"
+    out = dict(topk_idx=torch.full((rd.T, rd.K), -7, dtype=torch.int32, device=dev),
+               gates=torch.full((rd.T, rd.K), 7e7, dtype=torch.float32, device=dev))
+    if loss:
+        out.update(counts=torch.full((rd.G, rd.E), -7, dtype=torch.int32, device=dev),
+                   prob_sum=torch.full((rd.G, rd.E), 7e7, dtype=torch.float32, device=dev),
+                   seg_tokens=torch.full((rd.G,), -7, dtype=torch.int32, device=dev),
+                   loss=torch.full((1,), 7e7, dtype=torch.float32, device=dev))
+        ws = torch.full((mx.moonep_router_workspace_bytes(rd),), 0xA5, dtype=torch.uint8, device=dev)
+        mx.moonep_router_forward(rd, logits, out["topk_idx"], out["gates"], token_mask=mask, ws=ws,
+                                 stream=stream, **{k: out[k] for k in ("counts", "prob_sum",
+                                                                       "seg_tokens", "loss")})
+    else:
+        mx.moonep_router_forward(rd, logits, out["topk_idx"], out["gates"], token_mask=mask,
+                                 stream=stream)
+    return out
+
+
+def close(got, want, what, rtol=RTOL, atol=ATOL):
+    got, want = np.asarray(got, np.float64), np.asarray(want, np.float64)
+    nan = np.isnan(want)
+    assert np.array_equal(np.isnan(got), nan), what
+    err = np.abs(got - want)[~nan]
+    bad = err > (atol + rtol * np.abs(want))[~nan]
+    assert not bad.any(), (what, int(bad.sum()), err.max())
+
+
+def check(rd, logits, mask_np=None, score="softmax", loss=True):
+    x = logits.double().numpy()
+    live = None if mask_np is None else mask_np != 0
+    mask = None if mask_np is None else torch.from_numpy(mask_np).cuda()
+    out = {k: v.cpu().numpy() for k, v in forward(rd, logits.cuda(), mask, loss).items()}
+    scale = float(np.float32(rd.scale))
+    ids, gates, counts, sums, tokens, value = ops.router(
+        x, rd.K, rd.segment or rd.T, score, bool(rd.normalise), scale, live)
+    assert np.array_equal(out["topk_idx"], ids)
+    close(out["gates"], gates, "gates")
+    if loss:
+        assert np.array_equal(out["counts"], counts)
+        assert np.array_equal(out["seg_tokens"], tokens)
+        close(out["prob_sum"], sums, "prob_sum")
+        close(out["loss"][0], value, "loss")
+    return out
+
+
+# T, E, K, segment: one token to several blocks a segment, experts from fewer than
+# lanes to 4096 and off every vector width, K from 1 to E and beyond 32, ragged segments
+SHAPES = [(1, 1, 1, 0), (1, 8, 8, 0), (7, 20, 3, 3), (33, 31, 31, 32), (64, 33, 2, 1),
+          (130, 71, 5, 50), (257, 127, 7, 0), (64, 128, 8, 16), (300, 132, 4, 7),
+          (1000, 257, 6, 999), (513, 384, 8, 128), (100, 384, 40, 0), (77, 640, 9, 20),
+          (1300, 896, 16, 600), (64, 1023, 12, 0), (40, 1024, 128, 9), (19, 1500, 10, 0),
+          (21, 2048, 33, 5), (23, 4096, 16, 11), (9, 4093, 100, 4), (5000, 64, 6, 5000),
+          (20000, 96, 4, 9000)]
+
+
+@pytest.mark.parametrize("T,E,K,segment", SHAPES)
+@pytest.mark.parametrize("score,normalise,dtype", [("softmax", True, torch.float32),
+                                                   ("sigmoid", False, torch.bfloat16),
+                                                   ("softmax", False, torch.bfloat16),
+                                                   ("sigmoid", True, torch.float32)])
+def test_forward(T, E, K, segment, score, normalise, dtype):
+    rd = mx.router_dims(T, E, K, segment, score, normalise, 2.5, dtype)
+    logits = draw(T, E, T + E + K, dtype)
+    mask = (np.random.default_rng(T).random(T) > 0.2).astype(np.uint8)
+    with_loss = check(rd, logits, mask, score)
+    # the form without the loss gives the same ids and gates
+    bare = forward(rd, logits.cuda(), torch.from_numpy(mask).cuda(), loss=False)
+    assert np.array_equal(bare["topk_idx"].cpu().numpy(), with_loss["topk_idx"])
+    assert np.array_equal(bare["gates"].cpu().numpy(), with_loss["gates"])
+
+
+@pytest.mark.parametrize("T,E,K", [(50, 384, 8), (50, 71, 16), (20, 1500, 8), (20, 32, 32)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_ties_and_experts_switched_off(T, E, K, score):
+    rd = mx.router_dims(T, E, K, 0, score, True, 1.0)
+    check(rd, draw(T, E, 1, ties=True), score=score)
+    check(rd, torch.zeros(T, E), score=score)  # every logit equal
+    check(rd, draw(T, E, 2, off=E // 2), score=score)
+    check(rd, draw(T, E, 3, off=E - 3), score=score)  # fewer than K left
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [24, 384])
+def test_rows_of_infinities_and_nan(score, E):
+    T, K = 12, 6
+    l = draw(T, E, 5)
+    l[1] = -np.inf
+    l[3, 4] = np.nan
+    l[4] = np.nan
+    l[5] = -np.inf
+    l[5, 7] = np.nan
+    l[6] = torch.finfo(torch.float32).min
+    l[7] = torch.finfo(torch.float32).max
+    l[8, 2] = torch.finfo(torch.float32).max
+    if score == "sigmoid":
+        l[9, 3] = np.inf
+    rd = mx.router_dims(T, E, K, 4, score, True, 1.0)
+    check(rd, l, score=score)
+    # a masked token's NaN reaches no sum
+    mask = np.ones(T, np.uint8)
+    mask[[3, 4, 5]] = 0
+    out = check(rd, l, mask, score)
+    assert np.isfinite(out["loss"]).all()
+
+
+def test_segments_without_tokens():
+    rd = mx.router_dims(40, 64, 4, 8, "softmax", True, 1.0)
+    mask = np.ones(40, np.uint8)
+    mask[8:24] = 0
+    check(rd, draw(40, 64, 0), mask)
+    check(rd, draw(40, 64, 0), np.zeros(40, np.uint8))
+    big = mx.router_dims(4000, 64, 4, 2000, "softmax", True, 1.0)
+    mask = np.ones(4000, np.uint8)
+    mask[:2000] = 0
+    check(big, draw(4000, 64, 0), mask)
+
+
+def test_same_bits_in_every_run_and_on_another_stream():
+    rd = mx.router_dims(30000, 384, 8, 10000, "softmax", True, 1.0)
+    l = draw(30000, 384, 9).cuda()
+    first = forward(rd, l)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        second = forward(rd, l)
+    third = forward(rd, l, stream=side)
+    torch.cuda.synchronize()
+    for k in first:
+        assert torch.equal(first[k], second[k]) and torch.equal(first[k], third[k]), k
+
+
+def test_ids_feed_the_plan():
+    d = mx.dims(4, 64, 16, 4, 100, 64, 64)
+    rd = mx.router_dims(400, 64, 4, 100)
+    out = forward(rd, draw(400, 64, 3).cuda())
+    ws = mx.PlanWorkspace(d)
+    mx.moonep_plan(d, out["topk_idx"], ws.buf)
+    tabs = ws.tables()
+    assert tabs["status"][0] == 0
+    assert np.array_equal(tabs["T"], out["counts"].sum(0).cpu().numpy())
+
+
+# ------------------------------------------------------------------------- gradient
+# Each factor of the gradient (a score, a gate's share, the sums over the row) is
+# within RTOL of its own, so the element is within 3 RTOL of the sum of magnitudes
+# that make it up; bf16 results are rounded once more.
+@pytest.mark.parametrize("T,E,K,segment", [(1, 1, 1, 0), (7, 20, 3, 3), (33, 31, 31, 32),
+                                           (64, 33, 2, 1), (130, 71, 5, 50), (64, 128, 8, 16),
+                                           (60, 384, 8, 25), (40, 384, 40, 0), (30, 896, 16, 30),
+                                           (9, 1023, 12, 0), (9, 1024, 128, 4), (5, 2047, 9, 2),
+                                           (3, 4096, 16, 0)])
+@pytest.mark.parametrize("score,normalise,dtype", [("softmax", True, torch.float32),
+                                                   ("sigmoid", False, torch.bfloat16),
+                                                   ("softmax", False, torch.float32),
+                                                   ("sigmoid", True, torch.bfloat16)])
+@pytest.mark.parametrize("parts", ["both", "gates", "loss"])
+def test_backward(T, E, K, segment, score, normalise, dtype, parts):
+    rd = mx.router_dims(T, E, K, segment, score, normalise, 1.5, dtype)
+    off = E // 3 if E > 3 * K else 0
+    logits = draw(T, E, T + E, dtype, off=off)
+    rng = np.random.default_rng(E)
+    live = rng.random(T) > 0.2
+    mask = torch.from_numpy(live.astype(np.uint8)).cuda()
+    fwd = forward(rd, logits.cuda(), mask)
+    dg = rng.standard_normal((T, K)).astype(np.float32) if parts != "loss" else None
+    dl = float(np.float32(rng.random() * T + 1)) if parts != "gates" else 0.0
+    got = torch.full((T, E), 7.0, dtype=dtype, device="cuda")
+    extra = {}
+    if dg is not None:
+        extra["d_gates"] = torch.from_numpy(dg).cuda()
+    if dl:
+        extra.update(counts=fwd["counts"], seg_tokens=fwd["seg_tokens"],
+                     d_loss=torch.tensor([dl], device="cuda"))
+    mx.moonep_router_backward(rd, logits.cuda(), fwd["topk_idx"], got, token_mask=mask, **extra)
+    want, size = ops.router_backward(logits.double().numpy(), fwd["topk_idx"].cpu().numpy(),
+                                     segment or T, score, normalise, 1.5, live, dg, dl)
+    tol = 3 * RTOL * size + 1e-12 + (2.0 ** -8 * np.abs(want) if dtype == torch.bfloat16 else 0)
+    err = np.abs(got.double().cpu().numpy() - want)
+    assert (err <= tol).all(), (err.max(), (err / tol).max())
+    assert not got[torch.from_numpy(~live).cuda()].any()
+
+
+def test_backward_of_rows_without_weight():
+    T, E, K = 6, 40, 3
+    for score in ("softmax", "sigmoid"):
+        rd = mx.router_dims(T, E, K, 3, score, True, 1.0)
+        l = draw(T, E, 8)
+        l[2] = -np.inf
+        fwd = forward(rd, l.cuda())
+        got = torch.full((T, E), 7.0, device="cuda")
+        mx.moonep_router_backward(rd, l.cuda(), fwd["topk_idx"], got,
+                                  d_gates=torch.ones(T, K, device="cuda"), counts=fwd["counts"],
+                                  seg_tokens=fwd["seg_tokens"], d_loss=torch.ones(1, device="cuda"))
+        assert torch.isfinite(got).all() and not got[2].any()
+
+
+def test_gradient_against_differences_on_the_gpu():
+    """d_logits against differences of the forward pass's own fp32 gates and loss.  Their
+    rounding is RTOL of values below 3, so a difference over 2 h is off by 6 RTOL / (2 h),
+    and the formula's third derivative adds at most h^2 (all terms below 10)."""
+    T, E, K, h = 4, 24, 4, 0.05
+    rd = mx.router_dims(T, E, K, 2, "softmax", True, 1.0)
+    l = draw(T, E, 21, spread=1.0)
+    dg = torch.randn(T, K, generator=torch.Generator().manual_seed(1)).cuda()
+    fwd = forward(rd, l.cuda())
+    got = torch.empty(T, E, device="cuda")
+    mx.moonep_router_backward(rd, l.cuda(), fwd["topk_idx"], got, d_gates=dg, counts=fwd["counts"],
+                              seg_tokens=fwd["seg_tokens"], d_loss=torch.ones(1, device="cuda"))
+
+    def value(x):
+        out = forward(rd, x.cuda())
+        if not torch.equal(out["topk_idx"], fwd["topk_idx"]):
+            return None
+        return float((out["gates"] * dg).double().sum()) + float(out["loss"])
+
+    seen = 0
+    for t in range(T):
+        for e in range(E):
+            up, down = l.clone(), l.clone()
+            up[t, e] += h
+            down[t, e] -= h
+            a, b = value(up), value(down)
+            if a is None or b is None:
+                continue  # the step changed the choice of experts
+            seen += 1
+            assert abs((a - b) / (2 * h) - float(got[t, e])) <= 6 * RTOL / (2 * h) + 10 * h * h
+    assert seen > T * E // 2
