@@ -13,12 +13,16 @@
 // brings in are the same and the MMA work is four times as much in the same time.
 //
 // Scales: the instruction reads them from TMEM, where lane l of column j holds the
-// four scale bytes (128 values of K) of row 32 j + l, once for each of the four
-// lane groups.  A warp for each 128 rows loads 16 scale bytes a row (512 of K) one
-// load ahead, writes them to the stage in that order (one 16-byte store a lane
-// and 128 of K) and arrives on the stage's barrier next to the TMA copies; the
-// MMA thread moves them to TMEM with tcgen05.cp, which the tensor core runs in
-// order with the products.
+// four scale bytes (128 values of K) of row 32 j + l, repeated for the four lane
+// groups.  One thread has TMA bring 16 scale bytes (512 of K) of every row into a
+// ring of its own; four warps, one for each lane group, read them as 16 bytes a
+// row, which the order of registers turns around, and store them to TMEM.  (The
+// other way into TMEM, tcgen05.cp, measured 100 clocks for each 512 bytes, 600 for
+// a stage's six, where the stage's products take 512.)
+//
+// TMEM: two accumulators of 256 columns that share 128, and 2 x 48 columns of
+// scales.  The epilogue takes the shared columns first, so the next tile's
+// products start when half of a tile is in registers.
 #include <algorithm>
 
 #include "ops.h"
@@ -29,6 +33,14 @@ namespace moonep {
 constexpr int kMxK = 256;     // K per stage: 128 bytes of codes a row
 constexpr int kMxUmmaK = 64;  // K of one MMA
 constexpr int kMxBN = 256;    // columns of a work tile
+constexpr int kMxGroup = 2;   // stages that a slot of scales lasts: 512 values of K
+
+constexpr uint32_t kMxTmemCols = 512;
+constexpr uint32_t kMxAccStep = 128;   // the second accumulator starts here: 128 columns shared
+constexpr uint32_t kMxScaleCol = 384;  // slots of scales: A 4 x 4 columns, then B 4 x 8
+constexpr int kMxTmemSlots = 2, kMxSlotCols = 48;
+static_assert(kMxAccStep + kMxBN <= kMxScaleCol &&
+              kMxScaleCol + kMxTmemSlots * kMxSlotCols <= kMxTmemCols, "TMEM columns");
 
 // Per CTA: 128 rows of A, kMxBN / CG of the weights' rows, and the scales of its
 // rows and of all kMxBN columns.
@@ -37,24 +49,18 @@ struct MxCfg {
   static constexpr int kABytes = kMmaM * kMxK / 2;
   static constexpr int kBRows = kMxBN / CG;
   static constexpr int kBBytes = kBRows * kMxK / 2;
-  static constexpr int kAtoms = 1 + kMxBN / 128;  // 128-row scale blocks: A, then B
-  static constexpr int kScaleBytes = (kMxK / 128) * kAtoms * 512;
-  static constexpr int kStageBytes = kABytes + kBBytes + kScaleBytes;
-  static constexpr int kStages = CG == 2 ? 5 : 4;
-  static constexpr int kOutBufs = CG == 2 ? 2 : 1;  // 32 x 64 bf16 staging buffers a warp
-  static constexpr int kOutWarpBytes = kOutBufs * 4096;
-  static constexpr int kOutBytes = 4 * kOutWarpBytes;
-  static constexpr int kThreads = 192 + 32 * kAtoms;
-  static constexpr int kConsumers = CG == 2 ? 2 * (5 + kAtoms) : 5 + kAtoms;
-  static constexpr int kNumBars = 2 * kStages + 3 + 2 * kQueue;
-  static constexpr int kSmem =
-      kStages * kStageBytes + kOutBytes + 1024 + kNumBars * 8 + 16 + 4 * kQueue;
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr int kStages = CG == 2 ? 6 : 4;
+  static constexpr int kScaleBytes = (kMmaM + kMxBN) * 16;  // a slot: A's rows, then B's
+  static constexpr int kScaleSlots = 2;
+  static constexpr int kOutBytes = 4 * 4096;  // a 32 x 64 bf16 staging buffer a warp
+  static constexpr int kThreads = 32 * 11;
+  static constexpr int kConsumers = CG == 2 ? 20 : 10;  // every role but the claiming producer
+  static constexpr int kNumBars = 2 * kStages + 2 * kScaleSlots + 2 * kMxTmemSlots + 4 + 2 * kQueue;
+  static constexpr int kSmem = kStages * kStageBytes + kOutBytes + kScaleSlots * kScaleBytes + 1024 +
+                               kNumBars * 8 + 16 + 4 * kQueue;
 };
 static_assert(MxCfg<1>::kSmem <= 232448 && MxCfg<2>::kSmem <= 232448, "shared memory of a CTA");
-static_assert(MxCfg<1>::kScaleBytes % 1024 == 0, "stages stay 1024-byte aligned");
-
-constexpr uint32_t kMxTmemCols = 512;
-constexpr uint32_t kMxScaleCol = kMxBN;  // A: 2 x 4 columns, then B: 2 x 8
 
 // Instruction descriptor, kind::mxf4: A and B E2M1 (bits 7-9 and 10-11 = 1), both
 // K-major, N >> 3 in bits 17-22, E8M0 scales (bit 23), M >> 7 in bits 27-28; the
@@ -84,48 +90,46 @@ __device__ __forceinline__ void mx_mma(uint32_t d, uint64_t a, uint64_t b, uint3
   }
 }
 
-// 512 bytes of scales (32 rows of 16) from shared memory to four TMEM columns,
-// repeated for the four lane groups; in both CTAs of a pair, each from its own.
-template <int CG>
-__device__ __forceinline__ void mx_copy_scales(uint32_t tmem, uint32_t saddr) {
-  // no swizzle: 8-row groups of 16-byte rows 128 bytes apart
-  const uint64_t desc = (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) |
-                        ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
-  if constexpr (CG == 2)
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
-                 : "memory");
-  else
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
-                 : "memory");
+// 16 columns of this warp's 32 TMEM lanes
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+      : "memory");
 }
-
-struct MxScales {
-  const uint8_t *a, *home, *slot;
-  int pitch;                  // bytes a row
-  int a_rows, home_rows, slot_rows;
-};
 
 template <int CG>
 __global__ void __launch_bounds__(MxCfg<CG>::kThreads, 1)
 k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_wh,
-             const __grid_constant__ CUtensorMap tm_ws, const __grid_constant__ CUtensorMap tm_y,
-             MxScales sc, int K, int N, PlanPtrs p, uint16_t* __restrict__ y) {
+             const __grid_constant__ CUtensorMap tm_ws, const __grid_constant__ CUtensorMap tm_sa,
+             const __grid_constant__ CUtensorMap tm_sh, const __grid_constant__ CUtensorMap tm_ss,
+             const __grid_constant__ CUtensorMap tm_y, int K, int N, PlanPtrs p,
+             uint16_t* __restrict__ y) {
   using Cfg = MxCfg<CG>;
-  constexpr int STAGES = Cfg::kStages;
+  constexpr int STAGES = Cfg::kStages, SLOTS = Cfg::kScaleSlots;
   constexpr bool kPair = CG == 2;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* out_stage = smem + STAGES * Cfg::kStageBytes;
-  uint64_t* bars = (uint64_t*)(out_stage + Cfg::kOutBytes);
+  uint8_t* scale_ring = out_stage + Cfg::kOutBytes;
+  uint64_t* bars = (uint64_t*)(scale_ring + SLOTS * Cfg::kScaleBytes);
   uint32_t* tmem_slot = (uint32_t*)(bars + Cfg::kNumBars);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   const uint32_t bar0 = smem_u32(bars);
   auto full = [&](int s) { return bar0 + 8u * s; };
   auto empty = [&](int s) { return bar0 + 8u * (STAGES + s); };
-  const uint32_t tfull = bar0 + 8u * (2 * STAGES);
-  const uint32_t tempty = tfull + 8u;
-  const uint32_t drain = tfull + 16u;
-  const PairQueue q{tfull + 24u, tfull + 24u + 8u * kQueue, (int32_t*)(tmem_slot + 2)};
+  const uint32_t bar1 = bar0 + 16u * STAGES;
+  auto raw_full = [&](int s) { return bar1 + 8u * s; };  // a ring slot holds its scales
+  auto raw_empty = [&](int s) { return bar1 + 8u * (SLOTS + s); };
+  const uint32_t bar2 = bar1 + 16u * SLOTS;
+  auto sf_full = [&](int s) { return bar2 + 8u * s; };  // a TMEM slot holds its scales (leader's)
+  auto sf_empty = [&](int s) { return bar2 + 8u * (kMxTmemSlots + s); };
+  const uint32_t bar3 = bar2 + 16u * kMxTmemSlots;
+  auto tfull = [&](int b) { return bar3 + 8u * b; };
+  const uint32_t tempty = bar3 + 16u, drain = bar3 + 24u;
+  const PairQueue q{bar3 + 32u, bar3 + 32u + 8u * kQueue, (int32_t*)(tmem_slot + 2)};
   constexpr uint64_t kDrainNs = 200000000ull;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -136,14 +140,23 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
   const int NT = (N + kMxBN - 1) / kMxBN;
   const int total = p.counters[MOONEP_CNT_MTILES] * NT;
   const int KB = (K + kMxK - 1) / kMxK;
+  const int KG = (KB + kMxGroup - 1) / kMxGroup;
   int32_t* sched = p.sched + (kPair ? 0 : 4);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(full(s), 1 + CG * Cfg::kAtoms);  // the TMA bytes and every scale warp
+      mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
     }
-    mbar_init(tfull, 1);
+    for (int s = 0; s < SLOTS; ++s) {
+      mbar_init(raw_full(s), 1);
+      mbar_init(raw_empty(s), 4);  // the four scale warps
+    }
+    for (int s = 0; s < kMxTmemSlots; ++s) {
+      mbar_init(sf_full(s), 4 * CG);
+      mbar_init(sf_empty(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) mbar_init(tfull(b), 1);
     mbar_init(tempty, 4 * CG);
     mbar_init(drain, 1);
     queue_init(q, Cfg::kConsumers);
@@ -174,6 +187,9 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     *abort_flag = 1;
     set_error(p.status, MOONEP_ERR_TIMEOUT);
   };
+  auto weight_row = [&](const MTile& mt, int t) {  // first weight row of item t
+    return (mt.wsel >= 0 ? mt.wsel : (-1 - mt.wsel)) * N + (t % NT) * kMxBN;
+  };
 
   if (warp == 0) {
     // ---------------- TMA producer ----------------
@@ -194,14 +210,13 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         }
         if (t < 0) break;
         const MTile mt = p.mtiles[t / NT];
-        const int n0 = (t % NT) * kMxBN + (int)crank * Cfg::kBRows;
         const CUtensorMap* wmap = mt.wsel >= 0 ? &tm_wh : &tm_ws;
-        const int wrow = (mt.wsel >= 0 ? mt.wsel : (-1 - mt.wsel)) * N + n0;
+        const int wrow = weight_row(mt, t) + (int)crank * Cfg::kBRows;
         const int row0 = mt.row0 + (int)crank * kMmaM;
         for (int kb = 0; kb < KB; ++kb) {
           if (!mbar_wait(empty(stage), phase ^ 1u, abort_flag)) { ok = false; break; }
           const uint32_t sa = smem_u32(smem + stage * Cfg::kStageBytes);
-          if (leader) mbar_expect_tx(full(stage), CG * (Cfg::kABytes + Cfg::kBBytes));
+          if (leader) mbar_expect_tx(full(stage), CG * Cfg::kStageBytes);
           if constexpr (kPair) {
             const uint32_t fb = pair_map(full(stage), 0);
             tma_load_2d_pair(sa, &tm_a, fb, kb * (kMxK / 2), row0);
@@ -235,44 +250,47 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     // ---------------- MMA issuer (leader only) ----------------
     if (leader && lane == 0) {
       constexpr uint32_t idesc[2] = {mx_idesc(CG * kMmaM, kMxBN, 0), mx_idesc(CG * kMmaM, kMxBN, 2)};
-      const uint32_t sfa = tmem_base + kMxScaleCol, sfb = sfa + 8;
-      int stage = 0;
-      uint32_t phase = 0, acc_phase = 0;
+      int stage = 0, slot = 0;
+      uint32_t phase = 0, slot_phase = 0;
       bool ok = true;
       for (int i = 0; ok; ++i) {
         int t;
         if (!queue_take(q, i, true, true, t, abort_flag)) { ok = false; break; }
         if (t < 0) break;
-        if (!mbar_wait_cluster(tempty, acc_phase ^ 1u, abort_flag)) { ok = false; break; }
+        // the shared columns of the tile before are drained
+        if (!mbar_wait(tempty, (i & 1) ^ 1u, abort_flag)) { ok = false; break; }
         tc_fence_after();
-        for (int kb = 0; kb < KB; ++kb) {
-          if (!mbar_wait_cluster(full(stage), phase, abort_flag)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t sa = smem_u32(smem + stage * Cfg::kStageBytes);
-          const uint32_t sb = sa + Cfg::kABytes;
-          const uint32_t ss = sb + Cfg::kBBytes;
+        const uint32_t dtm = tmem_base + (uint32_t)(i & 1) * kMxAccStep;
+        for (int kb = 0; ok && kb < KB;) {
+          if (!mbar_wait(sf_full(slot), slot_phase, abort_flag)) { ok = false; break; }
+          const uint32_t sfa = tmem_base + kMxScaleCol + (uint32_t)slot * kMxSlotCols, sfb = sfa + 16;
 #pragma unroll
-          for (int c = 0; c < kMxK / 128; ++c) {
-            const uint32_t src = ss + c * Cfg::kAtoms * 512;
-            mx_copy_scales<CG>(sfa + c * 4, src);
-            mx_copy_scales<CG>(sfb + c * 8, src + 512);
-            mx_copy_scales<CG>(sfb + c * 8 + 4, src + 1024);
+          for (int h = 0; h < kMxGroup; ++h) {
+            if (kb == KB) break;
+            if (!mbar_wait(full(stage), phase, abort_flag)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t sa = smem_u32(smem + stage * Cfg::kStageBytes);
+            const uint32_t sb = sa + Cfg::kABytes;
+            const int steps = min(kMxK, K - kb * kMxK) / kMxUmmaK;
+#pragma unroll
+            for (int k = 0; k < kMxK / kMxUmmaK; ++k)
+              if (k < steps)
+                mx_mma<CG>(dtm, sw128_desc(sa + k * (kMxUmmaK / 2), 16, 1024),
+                           sw128_desc(sb + k * (kMxUmmaK / 2), 16, 1024), idesc[k & 1],
+                           sfa + (2 * h + (k >> 1)) * 4, sfb + (2 * h + (k >> 1)) * 8, (kb | k) != 0);
+            if constexpr (kPair) umma_commit_pair_both(empty(stage));
+            else umma_commit(empty(stage));
+            ++kb;
+            if (++stage == STAGES) { stage = 0; phase ^= 1u; }
           }
-          const int steps = min(kMxK, K - kb * kMxK) / kMxUmmaK;
-#pragma unroll
-          for (int k = 0; k < kMxK / kMxUmmaK; ++k)
-            if (k < steps)
-              mx_mma<CG>(tmem_base, sw128_desc(sa + k * (kMxUmmaK / 2), 16, 1024),
-                         sw128_desc(sb + k * (kMxUmmaK / 2), 16, 1024), idesc[k & 1],
-                         sfa + (k >> 1) * 4, sfb + (k >> 1) * 8, (kb | k) != 0);
-          if constexpr (kPair) umma_commit_pair_both(empty(stage));
-          else umma_commit(empty(stage));
-          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+          if (!ok) break;
+          if constexpr (kPair) umma_commit_pair_both(sf_empty(slot));
+          else umma_commit(sf_empty(slot));
+          if (++slot == kMxTmemSlots) { slot = 0; slot_phase ^= 1u; }
         }
         if (!ok) break;
-        if constexpr (kPair) umma_commit_pair_both(tfull);
-        else umma_commit(tfull);
-        acc_phase ^= 1u;
+        if constexpr (kPair) umma_commit_pair_both(tfull(i & 1));
+        else umma_commit(tfull(i & 1));
       }
       if (!ok) {
         fail();
@@ -284,8 +302,7 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
   } else if (warp < 6) {
     // ---------------- epilogue ----------------
     const int qw = warp & 3;
-    int nstore = 0;
-    uint32_t acc_phase = 0;
+    uint8_t* buf = out_stage + qw * 4096;
     for (int i = 0;; ++i) {
       int t;
       if (!queue_take_warp(q, i, leader, t, abort_flag)) {
@@ -295,133 +312,164 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
       if (t < 0) break;
       const MTile mt = p.mtiles[t / NT];
       const int n0 = (t % NT) * kMxBN;
-      if (!__all_sync(0xffffffffu, mbar_wait(tfull, acc_phase, abort_flag))) {
+      const int acc = i & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait(tfull(acc), (i >> 1) & 1, abort_flag))) {
         if (lane == 0) fail();
         break;
       }
       tc_fence_after();
       const int wrow0 = (int)crank * kMmaM + qw * 32;  // this warp's first row of the tile
-      const uint32_t tbase = tmem_base + ((uint32_t)(qw * 32) << 16);
+      const uint32_t tbase = tmem_base + ((uint32_t)(qw * 32) << 16) + (uint32_t)acc * kMxAccStep;
       const bool whole = wrow0 + 32 <= mt.rows;  // all 32 rows inside the group
       const bool valid = wrow0 + lane < mt.rows;
       uint16_t* yrow = y + (size_t)(mt.row0 + wrow0 + lane) * N + n0;
 #pragma unroll 1
-      for (int c = 0; c < kMxBN / 64 && n0 + c * 64 < N; ++c) {  // N is a multiple of 64
-        uint32_t lo[32], hi[32];
-        tmem_ld_x32(tbase + c * 64, lo);
-        tmem_ld_x32(tbase + c * 64 + 32, hi);
+      for (int half = 0; half < 2; ++half) {
+        // the columns that both accumulators use come first: the last 128 of the
+        // first accumulator, the first 128 of the second
+        const int c0 = (half ^ acc ^ 1) * 128;
+        uint32_t r[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_x32(tbase + c0 + c * 32, r[c]);
         tmem_ld_wait();
-        uint4 o[8];
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          o[v] = make_uint4(pack_bf16x2(lo[8 * v], lo[8 * v + 1]), pack_bf16x2(lo[8 * v + 2], lo[8 * v + 3]),
-                            pack_bf16x2(lo[8 * v + 4], lo[8 * v + 5]), pack_bf16x2(lo[8 * v + 6], lo[8 * v + 7]));
-          o[4 + v] = make_uint4(pack_bf16x2(hi[8 * v], hi[8 * v + 1]), pack_bf16x2(hi[8 * v + 2], hi[8 * v + 3]),
-                                pack_bf16x2(hi[8 * v + 4], hi[8 * v + 5]), pack_bf16x2(hi[8 * v + 6], hi[8 * v + 7]));
-        }
-        if (whole) {
-          // staged with the 128-byte swizzle, so that the lanes of a store phase hit
-          // distinct bank groups, and written by one TMA store
-          uint8_t* buf = out_stage + qw * Cfg::kOutWarpBytes + (nstore % Cfg::kOutBufs) * 4096;
-          if (lane == 0)
-            asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(Cfg::kOutBufs - 1) : "memory");
-          __syncwarp();
-          uint4* rowp = reinterpret_cast<uint4*>(buf + lane * 128);
-#pragma unroll
-          for (int v = 0; v < 8; ++v) rowp[v ^ (lane & 7)] = o[v];
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        if (half == 0) {
+          tc_fence_before();
           __syncwarp();
           if (lane == 0) {
-            asm volatile(
-                "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-                    (uint64_t)&tm_y),
-                "r"(n0 + c * 64), "r"(mt.row0 + wrow0), "r"(smem_u32(buf))
-                : "memory");
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            if constexpr (kPair) mbar_arrive_remote(pair_map(tempty, 0));
+            else mbar_arrive(tempty);
           }
-          ++nstore;
-        } else if (valid) {  // rows past the group's end are the next group's
+        }
 #pragma unroll
-          for (int v = 0; v < 8; ++v) reinterpret_cast<uint4*>(yrow + c * 64)[v] = o[v];
+        for (int c = 0; c < 2; ++c) {
+          const int n = c0 + c * 64;
+          if (n0 + n >= N) break;  // N is a multiple of 64
+          uint4 o[8];
+#pragma unroll
+          for (int v = 0; v < 8; ++v) {
+            const uint32_t* f = &r[2 * c + v / 4][8 * (v % 4)];
+            o[v] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                              pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+          }
+          if (whole) {
+            // staged with the 128-byte swizzle, so that the lanes of a store phase hit
+            // distinct bank groups, and written by one TMA store
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            __syncwarp();
+            uint4* rowp = reinterpret_cast<uint4*>(buf + lane * 128);
+#pragma unroll
+            for (int v = 0; v < 8; ++v) rowp[v ^ (lane & 7)] = o[v];
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+              asm volatile(
+                  "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                      (uint64_t)&tm_y),
+                  "r"(n0 + n), "r"(mt.row0 + wrow0), "r"(smem_u32(buf))
+                  : "memory");
+              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+          } else if (valid) {  // rows past the group's end are the next group's
+#pragma unroll
+            for (int v = 0; v < 8; ++v) reinterpret_cast<uint4*>(yrow + n)[v] = o[v];
+          }
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if constexpr (kPair) mbar_arrive_remote(pair_map(tempty, 0));
-        else mbar_arrive(tempty);
-      }
-      acc_phase ^= 1u;
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     __syncwarp();
-  } else {
-    // ---------------- scales: 128 rows of A or 128 columns of B each ----------------
-    const int atom = warp - 6;
-    const int KG = sc.pitch / 16;  // loads a row: 16 scale bytes, two stages
-    int stage = 0;
-    uint32_t phase = 0;
+  } else if (warp < 10) {
+    // ---------------- scales to TMEM: one warp for each lane group ----------------
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    int slot = 0, tslot = 0;
+    uint32_t phase = 0, tphase = 0;
     bool ok = true;
     for (int i = 0; ok; ++i) {
       int t;
       if (!queue_take_warp(q, i, leader, t, abort_flag)) { ok = false; break; }
       if (t < 0) break;
-      const MTile mt = p.mtiles[t / NT];
-      const uint8_t* src;
-      int first, rows;
-      if (atom == 0) {
-        src = sc.a, rows = sc.a_rows;
-        first = mt.row0 + (int)crank * kMmaM;
-      } else {
-        const bool home = mt.wsel >= 0;
-        src = home ? sc.home : sc.slot, rows = home ? sc.home_rows : sc.slot_rows;
-        first = (home ? mt.wsel : -1 - mt.wsel) * N + (t % NT) * kMxBN + (atom - 1) * 128;
+      for (int g = 0; g < KG; ++g) {
+        if (!__all_sync(0xffffffffu, mbar_wait(raw_full(slot), phase, abort_flag))) {
+          ok = false;
+          break;
+        }
+        const uint4* rows = reinterpret_cast<const uint4*>(scale_ring + slot * Cfg::kScaleBytes);
+        uint4 v[3][4];
+#pragma unroll
+        for (int a = 0; a < 3; ++a)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[a][j] = rows[a * 128 + 32 * j + lane];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(raw_empty(slot));
+        if (++slot == SLOTS) { slot = 0; phase ^= 1u; }
+        if (!__all_sync(0xffffffffu, mbar_wait(sf_empty(tslot), tphase ^ 1u, abort_flag))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t dst = tmem_base + lanes + kMxScaleCol + (uint32_t)tslot * kMxSlotCols;
+        // column 4 w + j of A and 8 w + 4 a + j of B: word w of row 32 j + lane
+        uint32_t r[48];
+#pragma unroll
+        for (int a = 0; a < 3; ++a)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int at = a == 0 ? j : 16 + 4 * (a - 1) + j, step = a == 0 ? 4 : 8;
+            r[at] = v[a][j].x;
+            r[at + step] = v[a][j].y;
+            r[at + 2 * step] = v[a][j].z;
+            r[at + 3 * step] = v[a][j].w;
+          }
+#pragma unroll
+        for (int c = 0; c < 3; ++c)
+          tmem_st_x16(dst + 16 * c, *reinterpret_cast<const uint32_t(*)[16]>(&r[16 * c]));
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (kPair) mbar_arrive_remote(pair_map(sf_full(tslot), 0));
+          else mbar_arrive(sf_full(tslot));
+        }
+        if (++tslot == kMxTmemSlots) { tslot = 0; tphase ^= 1u; }
       }
-      // rows past the group, the matrix or the tensor feed results that are not
-      // stored: any scale in range will do
-      const uint4* row[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        row[j] = reinterpret_cast<const uint4*>(
-            src + (size_t)min(first + 32 * j + lane, rows - 1) * sc.pitch);
-      uint4 now[4], then[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) now[j] = __ldg(row[j]);
-      for (int g = 0; ok && g < KG; ++g) {
-        if (g + 1 < KG) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) then[j] = __ldg(row[j] + g + 1);
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (2 * g + h >= KB) break;
-          if (!__all_sync(0xffffffffu, mbar_wait(empty(stage), phase ^ 1u, abort_flag))) {
-            ok = false;
-            break;
-          }
-          uint4* dst = reinterpret_cast<uint4*>(smem + stage * Cfg::kStageBytes + Cfg::kABytes +
-                                                Cfg::kBBytes + atom * 512) + lane;
-          if (h == 0) {
-            dst[0] = make_uint4(now[0].x, now[1].x, now[2].x, now[3].x);
-            dst[Cfg::kAtoms * 32] = make_uint4(now[0].y, now[1].y, now[2].y, now[3].y);
-          } else {
-            dst[0] = make_uint4(now[0].z, now[1].z, now[2].z, now[3].z);
-            dst[Cfg::kAtoms * 32] = make_uint4(now[0].w, now[1].w, now[2].w, now[3].w);
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if (lane == 0) {
-            if constexpr (kPair) mbar_arrive_remote(pair_map(full(stage), 0));
-            else mbar_arrive(full(stage));
-          }
-          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) now[j] = then[j];
+    }
+    if (ok) {  // every slot released: no commit still in flight
+      for (int i = 0; ok && i < kMxTmemSlots; ++i) {
+        ok = __all_sync(0xffffffffu, mbar_wait(sf_empty(tslot), tphase ^ 1u, abort_flag));
+        if (++tslot == kMxTmemSlots) { tslot = 0; tphase ^= 1u; }
       }
     }
     if (!ok && lane == 0) fail();
     __syncwarp();
+  } else if (lane == 0) {
+    // ---------------- scales to shared memory ----------------
+    int slot = 0, issued = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+      int t;
+      if (!queue_take(q, i, leader, true, t, abort_flag)) { ok = false; break; }
+      if (t < 0) break;
+      const MTile mt = p.mtiles[t / NT];
+      const CUtensorMap* smap = mt.wsel >= 0 ? &tm_sh : &tm_ss;
+      const int wrow = weight_row(mt, t), row0 = mt.row0 + (int)crank * kMmaM;
+      for (int g = 0; g < KG; ++g) {
+        if (!mbar_wait(raw_empty(slot), phase ^ 1u, abort_flag)) { ok = false; break; }
+        mbar_expect_tx(raw_full(slot), Cfg::kScaleBytes);
+        const uint32_t dst = smem_u32(scale_ring + slot * Cfg::kScaleBytes);
+        tma_load_2d(dst, &tm_sa, raw_full(slot), g * 16, row0);
+        tma_load_2d(dst + kMmaM * 16, smap, raw_full(slot), g * 16, wrow);
+        ++issued;
+        if (++slot == SLOTS) { slot = 0; phase ^= 1u; }
+      }
+    }
+    if (!ok) {
+      fail();
+      for (int i = 0; i < min(issued, SLOTS); ++i) {  // the copies this thread started
+        if (slot == 0) { slot = SLOTS - 1; phase ^= 1u; } else { --slot; }
+        mbar_wait(raw_full(slot), phase, nullptr, kDrainNs);
+      }
+    }
   }
 
   tc_fence_before();
@@ -437,18 +485,19 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-// Codes [rows][bytes], box of box_rows rows of 128 bytes, 128-byte swizzle; what
-// lies past a row's or the tensor's end reads as zeros.
-static bool encode_codes(CUtensorMap* m, const void* base, uint64_t bytes, uint64_t rows,
-                         uint32_t box_rows) {
+// A byte matrix [rows][bytes], box of box_rows rows of box_bytes (128: swizzled over
+// 128 bytes); what lies past a row's or the tensor's end reads as zeros.
+static bool encode_bytes(CUtensorMap* m, const void* base, uint64_t bytes, uint64_t rows,
+                         uint32_t box_bytes, uint32_t box_rows) {
   EncodeTiledFn enc = get_encode();
   if (!enc) return false;
   cuuint64_t gdim[2] = {bytes, rows};
   cuuint64_t gstride[1] = {bytes};
-  cuuint32_t box[2] = {128, box_rows};
+  cuuint32_t box[2] = {box_bytes, box_rows};
   cuuint32_t estr[2] = {1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), gdim, gstride, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_INTERLEAVE_NONE,
+             box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -465,14 +514,24 @@ static bool encode_out(CUtensorMap* m, const void* base, uint64_t N, uint64_t ro
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+struct MxOperands {
+  const uint8_t *a, *a_scales, *home, *home_scales, *slot, *slot_scales;
+  uint64_t a_rows, home_rows, slot_rows;
+};
+
 template <int CG>
-static cudaError_t launch_mx(const Dims& d, const PlanPtrs& p, const CUtensorMap& ta,
-                             const uint8_t* home, const uint8_t* slot, const CUtensorMap& ty,
-                             const MxScales& sc, uint16_t* y, cudaStream_t st) {
+static cudaError_t launch_mx(const Dims& d, const PlanPtrs& p, const MxOperands& m, uint16_t* y,
+                             cudaStream_t st) {
   using Cfg = MxCfg<CG>;
-  CUtensorMap twh, tws;
-  if (!encode_codes(&twh, home, d.H / 2, (uint64_t)sc.home_rows, Cfg::kBRows) ||
-      !encode_codes(&tws, slot, d.H / 2, (uint64_t)sc.slot_rows, Cfg::kBRows))
+  const uint64_t bytes = d.H / 2, pitch = MOONEP_MXFP4_SCALE_PITCH(d.H);
+  CUtensorMap ta, twh, tws, tsa, tsh, tss, ty;
+  if (!encode_bytes(&ta, m.a, bytes, m.a_rows, 128, kMmaM) ||
+      !encode_bytes(&twh, m.home, bytes, m.home_rows, 128, Cfg::kBRows) ||
+      !encode_bytes(&tws, m.slot, bytes, m.slot_rows, 128, Cfg::kBRows) ||
+      !encode_bytes(&tsa, m.a_scales, pitch, m.a_rows, 16, kMmaM) ||
+      !encode_bytes(&tsh, m.home_scales, pitch, m.home_rows, 16, kMxBN) ||
+      !encode_bytes(&tss, m.slot_scales, pitch, m.slot_rows, 16, kMxBN) ||
+      !encode_out(&ty, y, (uint64_t)d.Hp, m.a_rows))
     return cudaErrorInvalidValue;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -499,7 +558,7 @@ static cudaError_t launch_mx(const Dims& d, const PlanPtrs& p, const CUtensorMap
   }
   const long long items = (long long)d.max_mtiles * ((d.Hp + kMxBN - 1) / kMxBN);
   cfg.gridDim = dim3((unsigned)std::min<long long>(grid, CG * items));
-  return cudaLaunchKernelEx(&cfg, k_mxfp4_gemm<CG>, ta, twh, tws, ty, sc, d.H, d.Hp, p, y);
+  return cudaLaunchKernelEx(&cfg, k_mxfp4_gemm<CG>, ta, twh, tws, tsa, tsh, tss, ty, d.H, d.Hp, p, y);
 }
 
 cudaError_t launch_mxfp4_grouped_gemm(const Dims& d, const PlanPtrs& p, const uint8_t* a,
@@ -508,23 +567,19 @@ cudaError_t launch_mxfp4_grouped_gemm(const Dims& d, const PlanPtrs& p, const ui
                                       const uint8_t* slot_scales, void* y, cudaStream_t st,
                                       int* launches) {
   const bool slots = slot != nullptr && d.B > 0;
-  const MxScales sc{a_scales, home_scales, slots ? slot_scales : home_scales,
-                    MOONEP_MXFP4_SCALE_PITCH(d.H), d.R * d.C, d.E * d.Hp,
-                    slots ? d.R * d.B * d.Hp : d.E * d.Hp};
-  const uint8_t* sl = slots ? slot : home;
-  CUtensorMap ta, ty;
-  if (!encode_codes(&ta, a, d.H / 2, (uint64_t)d.R * d.C, kMmaM) ||
-      !encode_out(&ty, y, (uint64_t)d.Hp, (uint64_t)d.R * d.C))
-    return cudaErrorInvalidValue;
+  const uint64_t home_rows = (uint64_t)d.E * d.Hp;
+  const MxOperands m{a, a_scales, home, home_scales, slots ? slot : home,
+                     slots ? slot_scales : home_scales, (uint64_t)d.R * d.C, home_rows,
+                     slots ? (uint64_t)d.R * d.B * d.Hp : home_rows};
   // the plan's tile height is on the device: the variant it did not choose
   // returns at once (as in the bf16 product)
   if (d.tile_m != 2 * kMmaM) {
-    const cudaError_t e = launch_mx<1>(d, p, ta, home, sl, ty, sc, (uint16_t*)y, st);
+    const cudaError_t e = launch_mx<1>(d, p, m, (uint16_t*)y, st);
     if (e != cudaSuccess) return e;
     *launches += 1;
   }
   if (d.tile_m != kMmaM) {
-    const cudaError_t e = launch_mx<2>(d, p, ta, home, sl, ty, sc, (uint16_t*)y, st);
+    const cudaError_t e = launch_mx<2>(d, p, m, (uint16_t*)y, st);
     if (e != cudaSuccess) return e;
     *launches += 1;
   }
