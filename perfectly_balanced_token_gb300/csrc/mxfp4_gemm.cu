@@ -20,7 +20,7 @@
 // other way into TMEM, tcgen05.cp, measured 100 clocks for each 512 bytes, 600 for
 // a stage's six, where the stage's products take 512.)
 //
-// TMEM: two accumulators of 256 columns that share 128, and 2 x 48 columns of
+// TMEM: two accumulators of 256 columns that share 128, and 5 x 24 columns of
 // scales.  The epilogue takes the shared columns first, so the next tile's
 // products start when half of a tile is in registers.
 #include <algorithm>
@@ -33,12 +33,12 @@ namespace moonep {
 constexpr int kMxK = 256;     // K per stage: 128 bytes of codes a row
 constexpr int kMxUmmaK = 64;  // K of one MMA
 constexpr int kMxBN = 256;    // columns of a work tile
-constexpr int kMxGroup = 2;   // stages that a slot of scales lasts: 512 values of K
+constexpr int kMxGroup = 2;   // stages that one load of scales lasts: 512 values of K
 
 constexpr uint32_t kMxTmemCols = 512;
 constexpr uint32_t kMxAccStep = 128;   // the second accumulator starts here: 128 columns shared
-constexpr uint32_t kMxScaleCol = 384;  // slots of scales: A 4 x 4 columns, then B 4 x 8
-constexpr int kMxTmemSlots = 2, kMxSlotCols = 48;
+constexpr uint32_t kMxScaleCol = 384;  // a slot for a stage's scales: A 2 x 4 columns, B 2 x 8
+constexpr int kMxSlotCols = 24, kMxTmemSlots = 5;
 static_assert(kMxAccStep + kMxBN <= kMxScaleCol &&
               kMxScaleCol + kMxTmemSlots * kMxSlotCols <= kMxTmemCols, "TMEM columns");
 
@@ -53,10 +53,11 @@ struct MxCfg {
   static constexpr int kStages = CG == 2 ? 6 : 4;
   static constexpr int kScaleBytes = (kMmaM + kMxBN) * 16;  // a slot: A's rows, then B's
   static constexpr int kScaleSlots = 2;
+  static constexpr int kTmemSlots = kMxTmemSlots < kStages ? kMxTmemSlots : kStages;
   static constexpr int kOutBytes = 4 * 4096;  // a 32 x 64 bf16 staging buffer a warp
   static constexpr int kThreads = 32 * 11;
   static constexpr int kConsumers = CG == 2 ? 20 : 10;  // every role but the claiming producer
-  static constexpr int kNumBars = 2 * kStages + 2 * kScaleSlots + 2 * kMxTmemSlots + 4 + 2 * kQueue;
+  static constexpr int kNumBars = 2 * kStages + 2 * kScaleSlots + 4 + 2 * kQueue;
   static constexpr int kSmem = kStages * kStageBytes + kOutBytes + kScaleSlots * kScaleBytes + 1024 +
                                kNumBars * 8 + 16 + 4 * kQueue;
 };
@@ -90,7 +91,13 @@ __device__ __forceinline__ void mx_mma(uint32_t d, uint64_t a, uint64_t b, uint3
   }
 }
 
-// 16 columns of this warp's 32 TMEM lanes
+// 8 or 16 columns of this warp's 32 TMEM lanes
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
@@ -124,12 +131,9 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
   auto raw_full = [&](int s) { return bar1 + 8u * s; };  // a ring slot holds its scales
   auto raw_empty = [&](int s) { return bar1 + 8u * (SLOTS + s); };
   const uint32_t bar2 = bar1 + 16u * SLOTS;
-  auto sf_full = [&](int s) { return bar2 + 8u * s; };  // a TMEM slot holds its scales (leader's)
-  auto sf_empty = [&](int s) { return bar2 + 8u * (kMxTmemSlots + s); };
-  const uint32_t bar3 = bar2 + 16u * kMxTmemSlots;
-  auto tfull = [&](int b) { return bar3 + 8u * b; };
-  const uint32_t tempty = bar3 + 16u, drain = bar3 + 24u;
-  const PairQueue q{bar3 + 32u, bar3 + 32u + 8u * kQueue, (int32_t*)(tmem_slot + 2)};
+  auto tfull = [&](int b) { return bar2 + 8u * b; };
+  const uint32_t tempty = bar2 + 16u, drain = bar2 + 24u;
+  const PairQueue q{bar2 + 32u, bar2 + 32u + 8u * kQueue, (int32_t*)(tmem_slot + 2)};
   constexpr uint64_t kDrainNs = 200000000ull;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -145,16 +149,12 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(full(s), 1);
+      mbar_init(full(s), 1 + 4 * CG);  // the codes' bytes and the scale warps (leader's)
       mbar_init(empty(s), 1);
     }
     for (int s = 0; s < SLOTS; ++s) {
       mbar_init(raw_full(s), 1);
       mbar_init(raw_empty(s), 4);  // the four scale warps
-    }
-    for (int s = 0; s < kMxTmemSlots; ++s) {
-      mbar_init(sf_full(s), 4 * CG);
-      mbar_init(sf_empty(s), 1);
     }
     for (int b = 0; b < 2; ++b) mbar_init(tfull(b), 1);
     mbar_init(tempty, 4 * CG);
@@ -251,42 +251,35 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     if (leader && lane == 0) {
       constexpr uint32_t idesc[2] = {mx_idesc(CG * kMmaM, kMxBN, 0), mx_idesc(CG * kMmaM, kMxBN, 2)};
       int stage = 0, slot = 0;
-      uint32_t phase = 0, slot_phase = 0;
+      uint32_t phase = 0;
       bool ok = true;
       for (int i = 0; ok; ++i) {
-        int t;
-        if (!queue_take(q, i, true, true, t, abort_flag)) { ok = false; break; }
+        // the leader's own slot, written by its own producer: no cluster-scope order
+        if (!mbar_wait(q.full(i % kQueue), (i / kQueue) & 1, abort_flag)) { ok = false; break; }
+        const int t = *reinterpret_cast<volatile int32_t*>(q.items + i % kQueue);
+        mbar_arrive(q.empty(i % kQueue));
         if (t < 0) break;
         // the shared columns of the tile before are drained
         if (!mbar_wait(tempty, (i & 1) ^ 1u, abort_flag)) { ok = false; break; }
         tc_fence_after();
         const uint32_t dtm = tmem_base + (uint32_t)(i & 1) * kMxAccStep;
-        for (int kb = 0; ok && kb < KB;) {
-          if (!mbar_wait(sf_full(slot), slot_phase, abort_flag)) { ok = false; break; }
-          const uint32_t sfa = tmem_base + kMxScaleCol + (uint32_t)slot * kMxSlotCols, sfb = sfa + 16;
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!mbar_wait(full(stage), phase, abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(smem + stage * Cfg::kStageBytes);
+          const uint32_t sb = sa + Cfg::kABytes;
+          const uint32_t sfa = tmem_base + kMxScaleCol + (uint32_t)slot * kMxSlotCols, sfb = sfa + 8;
+          const int steps = min(kMxK, K - kb * kMxK) / kMxUmmaK;
 #pragma unroll
-          for (int h = 0; h < kMxGroup; ++h) {
-            if (kb == KB) break;
-            if (!mbar_wait(full(stage), phase, abort_flag)) { ok = false; break; }
-            tc_fence_after();
-            const uint32_t sa = smem_u32(smem + stage * Cfg::kStageBytes);
-            const uint32_t sb = sa + Cfg::kABytes;
-            const int steps = min(kMxK, K - kb * kMxK) / kMxUmmaK;
-#pragma unroll
-            for (int k = 0; k < kMxK / kMxUmmaK; ++k)
-              if (k < steps)
-                mx_mma<CG>(dtm, sw128_desc(sa + k * (kMxUmmaK / 2), 16, 1024),
-                           sw128_desc(sb + k * (kMxUmmaK / 2), 16, 1024), idesc[k & 1],
-                           sfa + (2 * h + (k >> 1)) * 4, sfb + (2 * h + (k >> 1)) * 8, (kb | k) != 0);
-            if constexpr (kPair) umma_commit_pair_both(empty(stage));
-            else umma_commit(empty(stage));
-            ++kb;
-            if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-          }
-          if (!ok) break;
-          if constexpr (kPair) umma_commit_pair_both(sf_empty(slot));
-          else umma_commit(sf_empty(slot));
-          if (++slot == kMxTmemSlots) { slot = 0; slot_phase ^= 1u; }
+          for (int k = 0; k < kMxK / kMxUmmaK; ++k)
+            if (k < steps)
+              mx_mma<CG>(dtm, sw128_desc(sa + k * (kMxUmmaK / 2), 16, 1024),
+                         sw128_desc(sb + k * (kMxUmmaK / 2), 16, 1024), idesc[k & 1],
+                         sfa + (k >> 1) * 4, sfb + (k >> 1) * 8, (kb | k) != 0);
+          if constexpr (kPair) umma_commit_pair_both(empty(stage));
+          else umma_commit(empty(stage));
+          if (++slot == Cfg::kTmemSlots) slot = 0;
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
         if (!ok) break;
         if constexpr (kPair) umma_commit_pair_both(tfull(i & 1));
@@ -336,7 +329,7 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
-            if constexpr (kPair) mbar_arrive_remote(pair_map(tempty, 0));
+            if constexpr (kPair) mbar_arrive_remote_relaxed(pair_map(tempty, 0));
             else mbar_arrive(tempty);
           }
         }
@@ -381,14 +374,18 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
   } else if (warp < 10) {
     // ---------------- scales to TMEM: one warp for each lane group ----------------
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    int slot = 0, tslot = 0;
-    uint32_t phase = 0, tphase = 0;
+    // Stage n's scales take TMEM slot n % kTmemSlots, free once the products of stage
+    // n - kTmemSlots are done: the `empty` barrier of that stage (which cannot be a
+    // phase further, as the stage STAGES later waits for these scales).
+    int slot = 0, tslot = 0, stage = 0, old = 0;
+    uint32_t phase = 0, old_phase = 0;
+    int before = Cfg::kTmemSlots;  // stages still without an earlier one
     bool ok = true;
     for (int i = 0; ok; ++i) {
       int t;
       if (!queue_take_warp(q, i, leader, t, abort_flag)) { ok = false; break; }
       if (t < 0) break;
-      for (int g = 0; g < KG; ++g) {
+      for (int kb = 0; ok && kb < KB;) {
         if (!__all_sync(0xffffffffu, mbar_wait(raw_full(slot), phase, abort_flag))) {
           ok = false;
           break;
@@ -402,41 +399,45 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         __syncwarp();
         if (lane == 0) mbar_arrive(raw_empty(slot));
         if (++slot == SLOTS) { slot = 0; phase ^= 1u; }
-        if (!__all_sync(0xffffffffu, mbar_wait(sf_empty(tslot), tphase ^ 1u, abort_flag))) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t dst = tmem_base + lanes + kMxScaleCol + (uint32_t)tslot * kMxSlotCols;
-        // column 4 w + j of A and 8 w + 4 a + j of B: word w of row 32 j + lane
-        uint32_t r[48];
 #pragma unroll
-        for (int a = 0; a < 3; ++a)
+        for (int h = 0; h < kMxGroup; ++h) {
+          if (kb == KB) break;
+          if (before > 0) {
+            --before;
+          } else {
+            if (!__all_sync(0xffffffffu, mbar_wait(empty(old), old_phase, abort_flag))) {
+              ok = false;
+              break;
+            }
+            if (++old == STAGES) { old = 0; old_phase ^= 1u; }
+            tc_fence_after();
+          }
+          const uint32_t dst = tmem_base + lanes + kMxScaleCol + (uint32_t)tslot * kMxSlotCols;
+          // columns 4 w + j of A, then 8 w + 4 a + j of B: word w of row 32 j + lane
+          uint32_t ra[8], rb[16];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const int at = a == 0 ? j : 16 + 4 * (a - 1) + j, step = a == 0 ? 4 : 8;
-            r[at] = v[a][j].x;
-            r[at + step] = v[a][j].y;
-            r[at + 2 * step] = v[a][j].z;
-            r[at + 3 * step] = v[a][j].w;
-          }
+            ra[j] = h == 0 ? v[0][j].x : v[0][j].z;
+            ra[4 + j] = h == 0 ? v[0][j].y : v[0][j].w;
 #pragma unroll
-        for (int c = 0; c < 3; ++c)
-          tmem_st_x16(dst + 16 * c, *reinterpret_cast<const uint32_t(*)[16]>(&r[16 * c]));
-        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if constexpr (kPair) mbar_arrive_remote(pair_map(sf_full(tslot), 0));
-          else mbar_arrive(sf_full(tslot));
+            for (int a = 0; a < 2; ++a) {
+              rb[4 * a + j] = h == 0 ? v[1 + a][j].x : v[1 + a][j].z;
+              rb[8 + 4 * a + j] = h == 0 ? v[1 + a][j].y : v[1 + a][j].w;
+            }
+          }
+          tmem_st_x8(dst, ra);
+          tmem_st_x16(dst + 8, rb);
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (kPair) mbar_arrive_remote_relaxed(pair_map(full(stage), 0));
+            else mbar_arrive(full(stage));
+          }
+          ++kb;
+          if (++tslot == Cfg::kTmemSlots) tslot = 0;
+          if (++stage == STAGES) stage = 0;
         }
-        if (++tslot == kMxTmemSlots) { tslot = 0; tphase ^= 1u; }
-      }
-    }
-    if (ok) {  // every slot released: no commit still in flight
-      for (int i = 0; ok && i < kMxTmemSlots; ++i) {
-        ok = __all_sync(0xffffffffu, mbar_wait(sf_empty(tslot), tphase ^ 1u, abort_flag));
-        if (++tslot == kMxTmemSlots) { tslot = 0; tphase ^= 1u; }
       }
     }
     if (!ok && lane == 0) fail();
