@@ -193,7 +193,7 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
 
   if (warp == 0) {
     // ---------------- TMA producer ----------------
-    if (lane == 0) {
+    if (elect_one()) {
       int stage = 0, issued = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -248,7 +248,8 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     }
   } else if (warp == 1) {
     // ---------------- MMA issuer (leader only) ----------------
-    if (leader && lane == 0) {
+    // (elect_one instead of lane 0: 1355 -> 1229 us at 262144 rows x 7168 x 2048)
+    if (leader && elect_one()) {
       constexpr uint32_t idesc[2] = {mx_idesc(CG * kMmaM, kMxBN, 0), mx_idesc(CG * kMmaM, kMxBN, 2)};
       int stage = 0, slot = 0;
       uint32_t phase = 0;
@@ -442,7 +443,7 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     }
     if (!ok && lane == 0) fail();
     __syncwarp();
-  } else if (lane == 0) {
+  } else if (elect_one()) {
     // ---------------- scales to shared memory ----------------
     int slot = 0, issued = 0;
     uint32_t phase = 0;
