@@ -34,8 +34,7 @@ extern "C" {
  * l [T][E] logits.  Per token: s = softmax(l) or sigmoid(l); the K experts with
  * the largest logits, largest first, equal logits in ascending expert id (-0 and
  * +0 are equal; a NaN ranks below -inf); gate k = scale * s[id_k], divided by
- * the sum of the K chosen s when `normalise` is set (gates are 0 where that sum
- * is 0).  A token whose token_mask is 0 still gets K distinct ids, as the plan
+ * the sum of the K chosen s when `normalise` is set.  A token whose token_mask is 0 still gets K distinct ids, as the plan
  * needs them, but its gates are 0, it is not counted and its gradient is 0.
  *
  * Balance loss over segments of `segment` consecutive tokens (the last may be
@@ -46,11 +45,10 @@ extern "C" {
  *   loss = 1/G sum_g E / (K n_g^2) sum_e counts[g][e] prob_sum[g][e]
  * (1 when counts and probabilities are even; a segment with n_g = 0 adds 0).
  *
- * A softmax row that holds only -inf has s = 0, q = 0 and gates 0; so has a
- * sigmoid row whose s are all 0.  Other rows with NaN (softmax: or +inf) give NaN where the
- * formulas do.  Gates, sums and the loss are computed in fp32 or wider; the
- * result is the same in every run (sums across blocks are integer sums of
- * fixed-point values). */
+ * A row that holds only -inf has q = 0 and gates 0.  Other rows with NaN (softmax:
+ * or +inf) give NaN where the formulas do.  Gates, sums and the loss are computed
+ * in fp32 or wider; the result is the same in every run (sums across blocks are
+ * integer sums of fixed-point values). */
 typedef struct moonep_router_dims {
   int32_t T, E, K;
   int32_t segment;    /* tokens per segment of the balance loss, 1 .. T (0: T) */
@@ -67,7 +65,8 @@ int moonep_router_workspace_bytes(const moonep_router_dims* dims, size_t* bytes)
  * fp32 [T][K] (written).  The balance outputs are all given or all NULL: ws
  * (overwritten), counts int32 [G][E], prob_sum fp32 [G][E], seg_tokens int32
  * [G] (n_g), loss fp32 [1] (4-byte aligned).
- * MOONEP_ERR_SHAPE: K > E, K > 128, E > 4096, T*K reaches 2^31, or segment > T.  Two calls that overlap on the GPU need two workspaces. */
+ * MOONEP_ERR_SHAPE: K > E, K > 128, E > 4096, T*K or G*E reaches 2^31, or
+ * segment > T.  Two calls that overlap on the GPU need two workspaces. */
 int moonep_router_forward(const moonep_router_dims* dims, const void* logits,
                           const uint8_t* token_mask, int32_t* topk_idx, float* gates, void* ws,
                           int32_t* counts, float* prob_sum, int32_t* seg_tokens, float* loss,

@@ -29,16 +29,32 @@ def scores(logits: np.ndarray, kind: str):
             s = np.where(total == 0, 0.0, s / total)
             return s, s
         s = 1.0 / (1.0 + np.exp(-logits))
-        total = s.sum(-1, keepdims=True)
-        return s, np.where(total == 0, 0.0, s / total)
+        return s, _share(_log_sigmoid(logits))
 
 
-def gates_of(s: np.ndarray, ids: np.ndarray, normalise: bool, scale: float, live: np.ndarray):
-    g = np.take_along_axis(s, ids.astype(np.int64), 1)
-    with np.errstate(invalid="ignore", divide="ignore"):
-        if normalise:
-            total = g.sum(-1, keepdims=True)
-            g = np.where(total == 0, 0.0, g / total)
+def _log_sigmoid(x):
+    return -np.logaddexp(0.0, -x)
+
+
+def _share(logs: np.ndarray) -> np.ndarray:
+    """e^logs over its sum along the row, whatever the size of logs; 0 for a row of -inf."""
+    m = np.fmax.reduce(logs, axis=-1, keepdims=True)
+    e = np.exp(logs - np.where(np.isneginf(m), 0.0, m))
+    total = e.sum(-1, keepdims=True)
+    return np.where(total == 0, 0.0, e / total)
+
+
+def gates_of(logits, kind: str, ids: np.ndarray, normalise: bool, scale: float, live: np.ndarray):
+    at = ids.astype(np.int64)
+    with np.errstate(invalid="ignore", over="ignore", divide="ignore"):
+        if not normalise:
+            g = np.take_along_axis(scores(logits, kind)[0], at, 1)
+        else:
+            chosen = np.take_along_axis(logits, at, 1)
+            g = _share(chosen if kind == "softmax" else _log_sigmoid(chosen))
+            if kind == "softmax":  # a NaN or an infinity in the row is in every score
+                bad = np.isnan(scores(logits, kind)[0]).any(-1, keepdims=True)
+                g = np.where(bad, np.nan, g)
     return np.where(live[:, None], scale * g, 0.0)
 
 
@@ -67,7 +83,7 @@ def router(logits, K, segment, kind, normalise, scale, live=None):
     live = np.ones(T, bool) if live is None else live
     ids = top_k(logits, K)
     s, q = scores(logits, kind)
-    gates = gates_of(s, ids, normalise, scale, live)
+    gates = gates_of(logits, kind, ids, normalise, scale, live)
     return ids, gates, *balance(q, ids, live, segment)
 
 

@@ -7,18 +7,6 @@
 
 namespace moonep {
 
-// The multiprocessors of the current device (host only: 152 where there is none,
-// so that sizes can be asked for without a GPU).
-static int router_sms() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) {
-    (void)cudaGetLastError();
-    return 152;
-  }
-  return sms;
-}
-
 static int check_router(const moonep_router_dims* in, RouterDims* d) {
   if (in == nullptr) return MOONEP_ERR_ARG;
   const moonep_router_dims& x = *in;
@@ -38,13 +26,8 @@ static int check_router(const moonep_router_dims* in, RouterDims* d) {
   d->bf16 = x.dtype;
   d->scale = x.scale;
   d->G = (int)(((int64_t)x.T + d->segment - 1) / d->segment);
-  // Tokens per block: four blocks a multiprocessor where there are enough, whole
-  // rounds of eight warps, and at most 32 tokens a warp, so that a warp's fp32
-  // sums stay short.
-  const int64_t each = ((int64_t)x.T + 4 * router_sms() - 1) / (4 * router_sms());
-  d->chunk = (int)std::min<int64_t>(256, std::max<int64_t>(8, (each + 7) / 8 * 8));
-  d->cps = (d->segment + d->chunk - 1) / d->chunk;
-  if ((int64_t)d->G * d->cps >= (int64_t(1) << 31)) return MOONEP_ERR_SHAPE;
+  d->chunk = d->cps = 0;  // set where the kernel's occupancy is known
+  if ((int64_t)d->G * d->E >= (int64_t(1) << 31)) return MOONEP_ERR_SHAPE;
   int bits = 0;  // a sum of `segment` probabilities fits 62 bits
   while ((int64_t(1) << bits) < d->segment) ++bits;
   d->shift = std::min(46, 62 - bits);

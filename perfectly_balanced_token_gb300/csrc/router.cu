@@ -81,78 +81,133 @@ __device__ __forceinline__ float warp_sort_down(float v, int lane) {
   return v;
 }
 
-// Rank of a logit as an integer: larger logits first, equal ones (-0 and +0
-// too) by ascending expert; a NaN below -inf.
+// Rank of a logit (not NaN) as an integer: larger logits first, equal ones (-0 and
+// +0 too) by ascending expert.
 __device__ __forceinline__ unsigned long long rank_key(float v, int e) {
   const uint32_t u = __float_as_uint(v + 0.0f);
-  const uint32_t k = v != v ? 1u : u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+  const uint32_t k = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
   return ((unsigned long long)k << 32) | (uint32_t)~e;
 }
-__device__ __forceinline__ int key_expert(unsigned long long k) { return (int)~(uint32_t)k; }
-__device__ __forceinline__ float key_logit(unsigned long long key) {
-  const uint32_t k = (uint32_t)(key >> 32);
-  if (k == 1u) return __uint_as_float(0x7fffffffu);
-  return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
+
+// e^x in one multiplication and the hardware's power of two (off by 2 ulp and by
+// what rounding x log2(e) leaves: |x| 2^-24); results below 2^-126 are 0.
+__device__ __forceinline__ float fast_exp(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+  return r;
+}
+__device__ __forceinline__ float fast_rcp(float x) {  // 1 ulp
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
-__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
-
-// The K best keys of a token, by rank, into top[0..K): at most 128.
-//
-// With K <= 32 the K-th largest of the 32 lanes' maxima is a bound that at least
-// K values reach, and few more (K = 8 of 384 normal logits: 11 on average), so
-// the values that reach it are gathered and each finds its rank by counting the
-// larger ones.  More than 32 of them (ties), a bound of -inf and K > 32 take the K
-// largest one after the other.
-template <int N, bool VEC>
-__device__ __forceinline__ void select_top(const float (&l)[N], int E, int K, int lane,
-                                           float sorted, unsigned long long* cand,
-                                           unsigned long long* top) {
-  const float bound = __shfl_sync(kAll, sorted, min(K, 32) - 1);
-  // a bound of -inf would let in the places past the row's end
-  if (K <= 32 && bound > -INFINITY) {
-    int mine = 0;
-#pragma unroll
-    for (int j = 0; j < N; ++j) mine += l[j] >= bound;
-    int before = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(kAll, before, o);
-      if (lane >= o) before += v;
-    }
-    const int total = __shfl_sync(kAll, before, 31);
-    if (total <= 32) {
-      int at = before - mine;
-#pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (l[j] >= bound) cand[at++] = rank_key(l[j], place<N, VEC>(j, lane));
-      __syncwarp();
-      const unsigned long long key = lane < total ? cand[lane] : 0;
-      int rank = 0;
-      for (int i = 0; i < total; ++i) rank += cand[i] > key;
-      if (lane < total && rank < K) top[rank] = key;
-      __syncwarp();
-      return;
-    }
+// A row's scores up to a common factor, from its largest logit m:
+//   softmax: e^(l - m);  the factor is 1 / their sum
+//   sigmoid: 1 / (e^(b - l) + e^b) with b = min(m, 0), which is sigmoid(l) e^-b: at
+//   least 1/2 for l = m, so a sum of them never vanishes, however low the row's logits
+// (a row of nothing but -inf takes m = 0, and all its scores are 0).
+struct Scores {
+  int kind;
+  float shift, one;  // m; or b and e^b
+  __device__ __forceinline__ Scores(int kind_, float m) : kind(kind_) {
+    if (m == -INFINITY) m = 0.f;
+    shift = kind == 0 ? m : fminf(m, 0.f);
+    one = fast_exp(shift);
   }
-  unsigned long long last = ~0ull;
-  for (int k = 0; k < K; ++k) {
-    unsigned long long best = 0;
+  __device__ __forceinline__ float operator()(float l) const {
+    return kind == 0 ? fast_exp(l - shift) : fast_rcp(fast_exp(shift - l) + one);
+  }
+};
+
+// The K largest of a token, one after the other; f(k, logit, expert) for each.
+// (Compared as logits and experts, not as keys: keys of a whole row would be kept
+// in registers through the kernel.)
+template <int N, bool VEC, typename F>
+__device__ __forceinline__ void select_in_turn(const float (&l)[N], int E, int K, int lane, F&& f) {
+  float last = INFINITY;
+  int last_e = -1;
+  bool nans = false;  // all that is left is NaN
+#pragma unroll 1
+  for (int k = 0; k < K;) {
+    float best = -INFINITY;
+    int best_e = 0x7fffffff;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       const int e = place<N, VEC>(j, lane);
-      const unsigned long long key = e < E ? rank_key(l[j], e) : 0;
-      if (key < last && key > best) best = key;
+      const bool later = e > last_e;
+      const bool left = nans ? (l[j] != l[j] && later) : (l[j] < last || (l[j] == last && later));
+      if (left && e < E && (best_e == 0x7fffffff || l[j] > best)) best = l[j], best_e = e;
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
-      const unsigned long long v = __shfl_xor_sync(kAll, best, o);
-      best = v > best ? v : best;
+      const float v = __shfl_xor_sync(kAll, best, o);
+      const int e = __shfl_xor_sync(kAll, best_e, o);
+      if (e != 0x7fffffff && (best_e == 0x7fffffff || v > best || (!(v < best) && e < best_e)))
+        best = v, best_e = e;
     }
-    if (lane == 0) top[k] = best;
-    last = best;
+    if (best_e == 0x7fffffff) {  // (only once, as K <= E)
+      nans = true;
+      last_e = -1;
+      continue;
+    }
+    f(k++, best, best_e);
+    last = best, last_e = best_e;
+  }
+}
+
+// The K <= 32 largest of a token: lanes with 0 <= rank < K hold one each.
+//
+// The K-th largest of the 32 lanes' maxima is a bound that at least K values reach,
+// and few more (K = 8 of 384 normal logits: 9 on average), so the values that reach
+// it are gathered, and each finds its rank by counting the larger ones.  More than
+// 32 of them (ties) and a bound of -inf (which the places past the row's end reach
+// too) take the K largest one after the other.
+template <int N, bool VEC>
+__device__ __forceinline__ void select_top(const float (&l)[N], int E, int K, int lane,
+                                           float bound, unsigned long long* cand, int& rank,
+                                           float& value, int& expert) {
+  rank = 32;
+  value = 0.f, expert = 0;
+  if (bound > -INFINITY) {
+    int total = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const unsigned who = __ballot_sync(kAll, l[j] >= bound);
+      if (who) {
+        const int at = total + __popc(who & ((1u << lane) - 1u));
+        if ((who >> lane & 1u) && at < 32)
+          cand[at] = ((unsigned long long)__float_as_uint(l[j]) << 32) | (uint32_t)place<N, VEC>(j, lane);
+        total += __popc(who);
+      }
+    }
+    if (total <= 32) {
+      __syncwarp();
+      unsigned long long key = 0;
+      if (lane < total) {
+        const unsigned long long c = cand[lane];
+        value = __uint_as_float((uint32_t)(c >> 32)), expert = (int)(uint32_t)c;
+        key = rank_key(value, expert);
+      }
+      __syncwarp();
+      cand[lane] = key;  // 0 past the last: counts for nobody
+      __syncwarp();
+      int r = 0;
+#pragma unroll 1
+      for (int i = 0; i < total; i += 4) {
+        const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(cand + i);
+        const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(cand + i + 2);
+        r += (a.x > key) + (a.y > key) + (b.x > key) + (b.y > key);
+      }
+      __syncwarp();
+      if (lane < total) rank = r;
+      return;
+    }
   }
   __syncwarp();
+  select_in_turn<N, VEC>(l, E, K, lane, [&](int k, float v, int e) {
+    if (lane == k) value = v, expert = e, rank = k;
+  });
 }
 
 constexpr int kRouterMaxK = 128;
@@ -160,6 +215,11 @@ constexpr int kRouterMaxK = 128;
 template <int N>
 constexpr int router_warps() {
   return N > 32 ? 4 : 8;
+}
+// Blocks a multiprocessor has to hold, which caps the registers
+template <int N>
+constexpr int router_blocks() {
+  return N <= 8 ? 5 : N <= 16 ? 4 : N <= 32 ? 2 : 1;
 }
 
 // Sum over the block in a fixed order (every thread gets it).
@@ -175,132 +235,34 @@ __device__ __forceinline__ double block_sum(double v, double* s) {
   return r;
 }
 
-template <typename T, int N, bool VEC, bool LOSS>
-__global__ void __launch_bounds__(router_warps<N>() * 32)
-k_router(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__ mask,
-         RouterOut out, RouterScratch ws) {
-  constexpr int W = router_warps<N>();
-  __shared__ unsigned long long s_cand[W][32];
-  __shared__ unsigned long long s_top[W][kRouterMaxK];
-  extern __shared__ unsigned long long s_dyn[];  // LOSS: q sums [E], then counts [E]
-  __shared__ int s_tokens, s_bad, s_last;
-  unsigned long long* s_q = s_dyn;
-  int32_t* s_cnt = reinterpret_cast<int32_t*>(s_dyn + d.E);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-  const int g = LOSS ? blockIdx.x / d.cps : 0;
-  const int base = LOSS ? g * d.segment : 0;  // first token of the segment
-  const int t0 = base + (LOSS ? blockIdx.x % d.cps : blockIdx.x) * d.chunk;
-  const int t1 = min(min(t0 + d.chunk, LOSS ? base + d.segment : d.T), d.T);
-  if (LOSS) {
-    for (int e = threadIdx.x; e < d.E; e += blockDim.x) {
-      s_q[e] = 0;
-      s_cnt[e] = 0;
-    }
-    if (threadIdx.x == 0) s_tokens = s_bad = 0;
-    __syncthreads();
-  }
-
-  float acc[LOSS ? N : 1];
-#pragma unroll
-  for (int j = 0; j < (LOSS ? N : 1); ++j) acc[j] = 0.f;
-  int live_tokens = 0;
-
-  for (int t = t0 + warp; t < t1; t += W) {
-    float l[N];
-    load_row<T, N, VEC>(logits + (size_t)t * d.E, d.E, lane, l);
-    const bool live = mask == nullptr || mask[t] != 0;
-    float most = -INFINITY;
-    bool nan = false;
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      most = fmaxf(most, l[j]);  // passes NaN over
-      nan |= l[j] != l[j];
-    }
-    const float sorted = warp_sort_down(most, lane);
-    float m = __shfl_sync(kAll, sorted, 0);
-    if (m == -INFINITY) m = 0.f;  // nothing but -inf (and NaN): exponentials of 0
-    select_top<N, VEC>(l, d.E, d.K, lane, sorted, s_cand[warp], s_top[warp]);
-
-    // 1 / sum of the row's s (softmax: of the exponentials before they are divided)
-    float inv = 1.f;
-    if (LOSS || (d.score == 0 && !d.normalise)) {
-      float sum = 0.f;
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        l[j] = d.score == 0 ? __expf(l[j] - m) : sigmoid(l[j]);
-        sum += l[j];
-      }
-      sum = warp_sum(sum);
-      inv = sum == 0.f ? 0.f : 1.f / sum;
-    }
-    if (LOSS && live) {
-#pragma unroll
-      for (int j = 0; j < N; ++j) acc[j] = fmaf(l[j], inv, acc[j]);
-      ++live_tokens;
-    }
-
-    float gate[kRouterMaxK / 32], total = 0.f;
-#pragma unroll
-    for (int i = 0; i < kRouterMaxK / 32; ++i) {
-      const int k = i * 32 + lane;
-      gate[i] = 0.f;
-      if (k < d.K) {
-        const float v = key_logit(s_top[warp][k]);
-        gate[i] = d.score == 0 ? __expf(v - m) : sigmoid(v);
-        total += gate[i];
-      }
-    }
-    float factor = d.score == 0 ? inv : 1.f;
-    if (d.normalise) {
-      total = warp_sum(total);
-      factor = total == 0.f ? 0.f : 1.f / total;
-    }
-    factor *= d.scale;
-    // a NaN anywhere in the row is in every softmax score, so in every gate
-    if (d.score == 0 && __any_sync(kAll, nan)) factor = NAN;
-#pragma unroll
-    for (int i = 0; i < kRouterMaxK / 32; ++i) {
-      const int k = i * 32 + lane;
-      if (k < d.K) {
-        const int e = key_expert(s_top[warp][k]);
-        out.topk_idx[(size_t)t * d.K + k] = e;
-        out.gates[(size_t)t * d.K + k] = live ? gate[i] * factor : 0.f;
-        if (LOSS && live) atomicAdd(&s_cnt[e], 1);
-      }
-    }
-    __syncwarp();  // the next token reuses the lists
-  }
-  if (!LOSS) return;
-
-  // The warps' sums as integers: a step of 2^-shift, so the order of the
-  // additions changes nothing; what is not finite is only noted (q of such a
-  // token is NaN for every expert).
-  const float one = ldexpf(1.f, d.shift);
-#pragma unroll
-  for (int j = 0; j < N; ++j) {
-    const int e = place<N, VEC>(j, lane);
-    if (e < d.E) {
-      if (!isfinite(acc[j])) s_bad = 1;
-      else if (acc[j] != 0.f) atomicAdd(&s_q[e], __float2ull_rn(acc[j] * one));
-    }
-  }
-  if (lane == 0) atomicAdd(&s_tokens, live_tokens);
-  __syncthreads();
-
+// The end of a block with the loss: its warps' probability sums s_q [W][E], counts
+// s_cnt [E] and tokens go to its segment's, and the last block of a segment writes
+// the segment's outputs, the last segment the loss.
+template <int W>
+__device__ __forceinline__ void join_blocks(const RouterDims& d, const RouterOut& out,
+                                            const RouterScratch& ws, int g, const float* s_q,
+                                            const int32_t* s_cnt, int& s_tokens, int& s_bad) {
+  __shared__ int s_last;
   const bool alone = d.cps == 1;  // the segment's only block
   if (!alone) {
+    // Joined across blocks as integers (steps of 2^-shift), so the order of the
+    // atomics changes nothing; what is not finite is only noted (q of such a token is
+    // NaN for every expert).
+    const float one = ldexpf(1.f, d.shift);
     for (int e = threadIdx.x; e < d.E; e += blockDim.x) {
-      if (s_q[e]) atomicAdd(&ws.q[(size_t)g * d.E + e], s_q[e]);
+      float q = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) q += s_q[(size_t)w * d.E + e];
+      if (!isfinite(q)) s_bad = 1;
+      else if (q != 0.f) atomicAdd(&ws.q[(size_t)g * d.E + e], __float2ull_rn(q * one));
       if (s_cnt[e]) atomicAdd(&ws.counts[(size_t)g * d.E + e], s_cnt[e]);
-    }
-    if (threadIdx.x == 0) {
-      atomicAdd(&ws.tokens[g], s_tokens);
-      if (s_bad) atomicOr(&ws.bad[g], 1);
     }
     __threadfence();
     __syncthreads();
     if (threadIdx.x == 0) {
+      atomicAdd(&ws.tokens[g], s_tokens);
+      if (s_bad) atomicOr(&ws.bad[g], 1);
+      __threadfence();
       s_last = atomicAdd(&ws.seg_done[g], 1) == d.cps - 1;
       __threadfence();
       if (s_last) {
@@ -318,8 +280,17 @@ k_router(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__
   double part = 0.0;
   for (int e = threadIdx.x; e < d.E; e += blockDim.x) {
     const size_t at = (size_t)g * d.E + e;
-    const int32_t c = alone ? s_cnt[e] : __ldcg(&ws.counts[at]);
-    const double q = s_bad ? (double)NAN : (double)(alone ? s_q[e] : __ldcg(&ws.q[at])) * step;
+    int32_t c;
+    double q;
+    if (alone) {
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) v += s_q[(size_t)w * d.E + e];
+      c = s_cnt[e], q = v;
+    } else {
+      c = __ldcg(&ws.counts[at]);
+      q = s_bad ? (double)NAN : (double)__ldcg(&ws.q[at]) * step;
+    }
     out.counts[at] = c;
     out.prob_sum[at] = (float)q;
     part += (double)c * q;
@@ -345,6 +316,128 @@ k_router(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__
   for (int i = threadIdx.x; i < d.G; i += blockDim.x) mean += __ldcg(&ws.seg_loss[i]);
   mean = block_sum(mean, s_red);
   if (threadIdx.x == 0) *out.loss = (float)(mean / d.G);
+}
+
+// A block takes `chunk` tokens of one segment, a warp every W-th of them.
+// SHORT: K <= 32.
+template <typename T, int N, bool VEC, bool LOSS, bool SHORT>
+__global__ void __launch_bounds__(router_warps<N>() * 32, router_blocks<N>())
+k_router(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__ mask,
+         RouterOut out, RouterScratch ws) {
+  constexpr int W = router_warps<N>();
+  constexpr int KI = SHORT ? 1 : kRouterMaxK / 32;
+  __shared__ __align__(16) unsigned long long s_list[W][SHORT ? 32 : kRouterMaxK];  // candidates
+  extern __shared__ float s_dyn[];  // LOSS: the warps' sums [W][E], then counts [E]
+  __shared__ int s_tokens, s_bad;
+  int32_t* s_cnt = reinterpret_cast<int32_t*>(s_dyn + (size_t)W * d.E);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  const int g = LOSS ? blockIdx.x / d.cps : 0;
+  const int base = LOSS ? g * d.segment : 0;  // first token of the segment
+  const int t0 = base + (LOSS ? blockIdx.x % d.cps : blockIdx.x) * d.chunk;
+  const int t1 = min(min(t0 + d.chunk, LOSS ? base + d.segment : d.T), d.T);
+  if (LOSS) {
+    for (int e = threadIdx.x; e < d.E; e += blockDim.x) s_cnt[e] = 0;
+    if (threadIdx.x == 0) s_tokens = s_bad = 0;
+    __syncthreads();
+  }
+
+  float acc[LOSS ? N : 1];
+#pragma unroll
+  for (int j = 0; j < (LOSS ? N : 1); ++j) acc[j] = 0.f;
+  int live_tokens = 0;
+
+  for (int t = t0 + warp; t < t1; t += W) {
+    float l[N];
+    load_row<T, N, VEC>(logits + (size_t)t * d.E, d.E, lane, l);
+    const bool live = mask == nullptr || mask[t] != 0;
+    float most = l[0];
+#pragma unroll
+    for (int j = 1; j < N; ++j) most = fmaxf(most, l[j]);  // passes NaN over
+    if (N == 1) most = fmaxf(most, -INFINITY);
+    const float sorted = warp_sort_down(most, lane);
+    const Scores score(d.score, __shfl_sync(kAll, sorted, 0));
+
+    // the chosen ones of this lane: SHORT, the one with rank `rank`; else those with
+    // rank i * 32 + lane
+    float value[KI];
+    int expert[KI], rank = 0;
+    if constexpr (SHORT) {
+      select_top<N, VEC>(l, d.E, d.K, lane, __shfl_sync(kAll, sorted, d.K - 1), s_list[warp], rank,
+                         value[0], expert[0]);
+    } else {
+      select_in_turn<N, VEC>(l, d.E, d.K, lane, [&](int k, float v, int e) {
+        if (lane == 0)
+          s_list[warp][k] = ((unsigned long long)__float_as_uint(v) << 32) | (uint32_t)e;
+      });
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < KI; ++i) {
+        const unsigned long long c = i * 32 + lane < d.K ? s_list[warp][i * 32 + lane] : 0;
+        value[i] = __uint_as_float((uint32_t)(c >> 32)), expert[i] = (int)(uint32_t)c;
+      }
+      __syncwarp();
+    }
+
+    // 1 / sum of the row's scores, where it is needed; a NaN in the row, which is in
+    // every softmax score, shows in it
+    float inv = 1.f;
+    bool nan = false;
+    if (LOSS || (d.score == 0 && !d.normalise)) {
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        l[j] = score(l[j]);
+        sum += l[j];
+      }
+      sum = warp_sum(sum);
+      inv = sum == 0.f ? 0.f : fast_rcp(sum);
+      nan = sum != sum;
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j) nan |= l[j] != l[j];
+      nan = __any_sync(kAll, nan);
+    }
+    if (LOSS && live) {
+#pragma unroll
+      for (int j = 0; j < (LOSS ? N : 1); ++j) acc[j] = fmaf(l[j], inv, acc[j]);
+      ++live_tokens;
+    }
+
+    float gate[KI], total = 0.f;
+#pragma unroll
+    for (int i = 0; i < KI; ++i) {
+      const bool mine = SHORT ? rank < d.K : i * 32 + lane < d.K;
+      gate[i] = mine ? score(value[i]) : 0.f;
+      total += gate[i];
+    }
+    float factor = d.score == 0 ? inv : score.one;
+    if (d.normalise) {
+      total = warp_sum(total);
+      factor = total == 0.f ? 0.f : fast_rcp(total);
+    }
+    factor *= d.scale;
+    if (d.score == 0 && nan) factor = NAN;
+#pragma unroll
+    for (int i = 0; i < KI; ++i) {
+      const int k = SHORT ? rank : i * 32 + lane;
+      if (k < d.K) {
+        out.topk_idx[(size_t)t * d.K + k] = expert[i];
+        out.gates[(size_t)t * d.K + k] = live ? gate[i] * factor : 0.f;
+        if (LOSS && live) atomicAdd(&s_cnt[expert[i]], 1);
+      }
+    }
+  }
+  if constexpr (LOSS) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int e = place<N, VEC>(j, lane);
+      if (e < d.E) s_dyn[(size_t)warp * d.E + e] = acc[j];
+    }
+    if (lane == 0) atomicAdd(&s_tokens, live_tokens);
+    __syncthreads();
+    join_blocks<W>(d, out, ws, g, s_dyn, s_cnt, s_tokens, s_bad);
+  }
 }
 
 // The gradient.  With w_e = d_loss E counts_e / (G K n^2), a_k what the gate k
@@ -411,32 +504,29 @@ k_router_backward(RouterDims d, const T* __restrict__ logits, const uint8_t* __r
           }
         }
       }
-      float m = 0.f;
-      if (d.score == 0) {
-        m = -INFINITY;
+      float m = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < N; ++j) m = fmaxf(m, l[j]);
-        m = warp_max(m);
-        if (m == -INFINITY) m = 0.f;
-      }
-      // s, the sum of s and of s w
+      for (int j = 0; j < N; ++j) m = fmaxf(m, l[j]);
+      const Scores score(d.score, warp_max(m));
+      // the scores (up to their common factor), their sum and that with w
       float sum = 0.f, dot = 0.f;
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         if (d.score == 0) {
-          l[j] = __expf(l[j] - m);
+          l[j] = score(l[j]);
           dl[j] = 1.f;
         } else {
-          const float x = __expf(-l[j]);
-          const float v = __fdividef(1.f, 1.f + x);
-          dl[j] = l[j] > 0.f ? x * v : 1.f - v;  // 1 - s, near s = 1 without cancellation
+          const float x = fast_exp(score.shift - l[j]);
+          const float v = fast_rcp(x + score.one);
+          // 1 - s; near s = 1 (then the shift is 0) without cancellation
+          dl[j] = l[j] > 0.f ? x * v : fmaf(-v, score.one, 1.f);
           l[j] = v;
         }
         sum += l[j];
         dot = fmaf(l[j], w[j], dot);
       }
       sum = warp_sum(sum);
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const float inv = sum == 0.f ? 0.f : fast_rcp(sum);
       dot = warp_sum(dot) * inv;
 
       if (d_gates != nullptr) {
@@ -444,14 +534,14 @@ k_router_backward(RouterDims d, const T* __restrict__ logits, const uint8_t* __r
 #pragma unroll
         for (int i = 0; i < kRouterMaxK / 32; ++i)
           if (id[i] >= 0) {
-            s[i] = d.score == 0 ? __expf(s[i] - m) : sigmoid(s[i]);
+            s[i] = score(s[i]);
             total += s[i];
             with = fmaf(s[i], dg[i], with);
           }
-        float factor = d.score == 0 ? inv : 1.f, mean = 0.f;
+        float factor = d.score == 0 ? inv : score.one, mean = 0.f;
         if (d.normalise) {
           total = warp_sum(total);
-          factor = total == 0.f ? 0.f : 1.f / total;
+          factor = total == 0.f ? 0.f : fast_rcp(total);
           mean = warp_sum(with) * factor;
         } else if (d.score == 0) {
           dot = fmaf(warp_sum(with), d.scale * inv, dot);
@@ -522,50 +612,63 @@ RouterScratch router_scratch(const RouterDims& d, void* ws) {
   r.bad = (int32_t*)take(4 * G);
   r.counts = (int32_t*)take(4 * GE);
   r.q = (unsigned long long*)take(8 * GE);
-  // one block a segment: only the count of finished segments is kept here
-  r.zero_bytes = d.cps > 1 ? off : (d.G > 1 ? 4 : 0);
+  r.zero_bytes = off;
   r.seg_loss = (double*)take(8 * G);
   r.total_bytes = off;
   return r;
 }
 
+// Launch shape of a router kernel: blocks for one round of what fits the GPU at
+// once, so that all warps take equally many tokens; whole rounds of the block's
+// warps, and at most 64 tokens a warp, so that a warp's fp32 sums stay short.
 template <typename Kernel>
-static cudaError_t with_smem(Kernel* k, size_t bytes) {
-  return bytes > (32u << 10)
-             ? cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes)
-             : cudaSuccess;
+static cudaError_t plan_blocks(Kernel* k, int warps, size_t smem, RouterDims& d) {
+  if (smem > (32u << 10)) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  int dev = 0, sms = 0, per_sm = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, warps * 32, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t blocks = std::max(1, sms * per_sm);
+  // blocks a segment in that round, or one where there are more segments than blocks
+  const int64_t each = std::max<int64_t>(1, blocks / d.G);
+  int64_t chunk = (d.segment + each - 1) / each;
+  chunk = (chunk + warps - 1) / warps * warps;
+  d.chunk = (int)std::min<int64_t>(chunk, 64 * warps);
+  d.cps = (d.segment + d.chunk - 1) / d.chunk;
+  return cudaSuccess;
 }
 
-template <typename T, int N, bool VEC>
+template <typename T, int N, bool VEC, bool LOSS, bool SHORT>
 static cudaError_t forward(RouterDims d, const void* logits, const uint8_t* mask,
                            const RouterOut& out, const RouterScratch& ws, cudaStream_t st) {
   constexpr int W = router_warps<N>();
-  if (out.loss == nullptr) {
-    d.chunk = W;
-    k_router<T, N, VEC, false>
-        <<<(d.T + W - 1) / W, W * 32, 0, st>>>(d, (const T*)logits, mask, out, ws);
-    return cudaGetLastError();
-  }
-  if (ws.zero_bytes) {
-    const cudaError_t e = cudaMemsetAsync(ws.done, 0, ws.zero_bytes, st);
+  auto* kernel = k_router<T, N, VEC, LOSS, SHORT>;
+  const size_t smem = LOSS ? (size_t)d.E * 4 * (W + 1) : 0;
+  if (!LOSS) d.G = 1, d.segment = d.T;
+  cudaError_t e = plan_blocks(kernel, W, smem, d);
+  if (e != cudaSuccess) return e;
+  if (LOSS) {  // one block a segment: only the count of finished segments is used
+    const size_t zero = d.cps > 1 ? ws.zero_bytes : (d.G > 1 ? 4 : 0);
+    if (zero) e = cudaMemsetAsync(ws.done, 0, zero, st);
     if (e != cudaSuccess) return e;
   }
-  const size_t smem = (size_t)d.E * 12;
-  const cudaError_t e = with_smem(k_router<T, N, VEC, true>, smem);
-  if (e != cudaSuccess) return e;
-  k_router<T, N, VEC, true>
-      <<<d.G * d.cps, W * 32, smem, st>>>(d, (const T*)logits, mask, out, ws);
+  kernel<<<d.G * d.cps, W * 32, smem, st>>>(d, (const T*)logits, mask, out, ws);
   return cudaGetLastError();
 }
 
 template <typename T, int N, bool VEC>
-static cudaError_t backward(const RouterDims& d, const void* logits, const uint8_t* mask,
+static cudaError_t backward(RouterDims d, const void* logits, const uint8_t* mask,
                             const int32_t* topk_idx, const float* d_gates, const int32_t* counts,
                             const int32_t* seg_tokens, const float* d_loss, void* d_logits,
                             cudaStream_t st) {
   constexpr int W = router_warps<N>();
   const size_t smem = (size_t)W * ((d.E + 3) & ~3) * 4;
-  const cudaError_t e = with_smem(k_router_backward<T, N, VEC>, smem);
+  const cudaError_t e = plan_blocks(k_router_backward<T, N, VEC>, W, smem, d);
   if (e != cudaSuccess) return e;
   k_router_backward<T, N, VEC><<<d.G * d.cps, W * 32, smem, st>>>(
       d, (const T*)logits, mask, topk_idx, d_gates, counts, seg_tokens, d_loss, (T*)d_logits);
@@ -610,7 +713,11 @@ struct ForwardCall {
   cudaStream_t st;
   template <typename T, int N, bool VEC>
   cudaError_t operator()() const {
-    return forward<T, N, VEC>(d, logits, mask, out, ws, st);
+    if (out.loss == nullptr)
+      return d.K <= 32 ? forward<T, N, VEC, false, true>(d, logits, mask, out, ws, st)
+                       : forward<T, N, VEC, false, false>(d, logits, mask, out, ws, st);
+    return d.K <= 32 ? forward<T, N, VEC, true, true>(d, logits, mask, out, ws, st)
+                     : forward<T, N, VEC, true, false>(d, logits, mask, out, ws, st);
   }
 };
 

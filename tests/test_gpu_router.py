@@ -143,6 +143,17 @@ def test_rows_of_infinities_and_nan(score, E):
     assert np.isfinite(out["loss"]).all()
 
 
+def test_very_low_logits_keep_their_shares():
+    l = draw(6, 40, 4)
+    l[0] -= 100.0    # sigmoids below the smallest float
+    l[1] -= 1e6
+    l[2] += 100.0
+    l[3] = -3e38
+    for score in ("softmax", "sigmoid"):
+        check(mx.router_dims(6, 40, 3, 2, score, True, 1.0), l, score=score)
+        check(mx.router_dims(6, 40, 3, 2, score, False, 1.0), l, score=score)
+
+
 def test_segments_without_tokens():
     rd = mx.router_dims(40, 64, 4, 8, "softmax", True, 1.0)
     mask = np.ones(40, np.uint8)

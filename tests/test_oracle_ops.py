@@ -38,6 +38,14 @@ def test_all_masked_by_minus_infinity():
         assert ids.tolist() == [[0, 1]] and not gates.any() and not sums.any() and loss == 0
 
 
+def test_shares_of_vanishing_sigmoids():
+    # sigmoid(-2000) is 0 in 64 bits; the shares are those of e^-2000 and e^-2001
+    l = np.array([[-2000.0, -2001.0, -3000.0]])
+    _, gates, _, sums, _, _ = ops.router(l, 2, 1, "sigmoid", True, 1.0)
+    want = np.array([1.0, np.exp(-1.0)]) / (1 + np.exp(-1.0))
+    assert np.allclose(gates[0], want) and np.allclose(sums[0, :2], want)
+
+
 @pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("normalise", [True, False])
 def test_gradient_against_differences(kind, normalise):
@@ -51,7 +59,7 @@ def test_gradient_against_differences(kind, normalise):
     def value(x):
         s, q = ops.scores(x, kind)
         loss = ops.balance(q, ids, live, seg)[3]
-        return (dg * ops.gates_of(s, ids, normalise, scale, live)).sum() + d_loss * loss
+        return (dg * ops.gates_of(x, kind, ids, normalise, scale, live)).sum() + d_loss * loss
 
     grad, size = ops.router_backward(l, ids, seg, kind, normalise, scale, live, dg, d_loss)
     h = 1e-5
