@@ -26,7 +26,7 @@ static int check_router(const moonep_router_dims* in, RouterDims* d) {
   d->bf16 = x.dtype;
   d->scale = x.scale;
   d->G = (int)(((int64_t)x.T + d->segment - 1) / d->segment);
-  d->chunk = d->cps = 0;  // set where the kernel's occupancy is known
+  d->per_block = d->blocks = 0;
   if ((int64_t)d->G * d->E >= (int64_t(1) << 31)) return MOONEP_ERR_SHAPE;
   int bits = 0;  // a sum of `segment` probabilities fits 62 bits
   while ((int64_t(1) << bits) < d->segment) ++bits;

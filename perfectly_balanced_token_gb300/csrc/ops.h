@@ -9,10 +9,9 @@ namespace moonep {
 struct RouterDims {
   int T, E, K, segment, score, normalise, bf16;
   float scale;
-  int G;      // segments
-  int chunk;  // tokens per block of threads, within one segment
-  int cps;    // blocks per segment
-  int shift;  // fixed-point bits below one of the probability sums
+  int G;                  // segments
+  int shift;              // fixed-point bits below one of the probability sums
+  int per_block, blocks;  // launch shape: tokens a block, set by the launcher
 };
 
 // The router's scratch: what is zeroed before a launch comes first.

@@ -58,25 +58,63 @@ __device__ __forceinline__ void load_row(const T* __restrict__ row, int E, int l
   }
 }
 
+template <typename T, int N, bool VEC>
+__device__ __forceinline__ void store_row(T* __restrict__ row, int E, int lane,
+                                          const float (&l)[N]) {
+  if constexpr (VEC) {
+#pragma unroll
+    for (int c = 0; c < N / 4; ++c) {
+      const int at = c * 128 + lane * 4;
+      if (at >= E) continue;
+      if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float4*>(row + at) =
+            make_float4(l[4 * c], l[4 * c + 1], l[4 * c + 2], l[4 * c + 3]);
+      } else {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(l[4 * c], l[4 * c + 1]);
+        const __nv_bfloat162 hi = __floats2bfloat162_rn(l[4 * c + 2], l[4 * c + 3]);
+        *reinterpret_cast<uint2*>(row + at) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                                         *reinterpret_cast<const uint32_t*>(&hi));
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int at = j * 32 + lane;
+      if (at < E) row[at] = (T)l[j];
+    }
+  }
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
   return v;
 }
 __device__ __forceinline__ float warp_max(float v) {  // NaN is passed over
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
-  return v;
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
 
-// The lanes' values sorted downwards over the warp (bitonic network).
-__device__ __forceinline__ float warp_sort_down(float v, int lane) {
+// The lanes' values sorted downwards over the warp (bitonic network).  `keep` has a
+// bit for each step where the lane keeps the larger value: see sort_directions.
+__device__ __forceinline__ uint32_t sort_directions(int lane) {
+  uint32_t keep = 0, bit = 1;
 #pragma unroll
   for (int k = 2; k <= 32; k <<= 1)
 #pragma unroll
-    for (int j = k >> 1; j; j >>= 1) {
+    for (int j = k >> 1; j; j >>= 1, bit <<= 1)
+      if (((lane & k) == 0) == ((lane & j) == 0)) keep |= bit;
+  return keep;
+}
+__device__ __forceinline__ float warp_sort_down(float v, uint32_t keep) {
+  uint32_t bit = 1;
+#pragma unroll
+  for (int k = 2; k <= 32; k <<= 1)
+#pragma unroll
+    for (int j = k >> 1; j; j >>= 1, bit <<= 1) {
       const float o = __shfl_xor_sync(kAll, v, j);
-      v = (((lane & k) == 0) == ((lane & j) == 0)) ? fmaxf(v, o) : fminf(v, o);
+      v = (keep & bit) ? fmaxf(v, o) : fminf(v, o);
     }
   return v;
 }
@@ -107,16 +145,19 @@ __device__ __forceinline__ float fast_rcp(float x) {  // 1 ulp
 //   sigmoid: 1 / (e^(b - l) + e^b) with b = min(m, 0), which is sigmoid(l) e^-b: at
 //   least 1/2 for l = m, so a sum of them never vanishes, however low the row's logits
 // (a row of nothing but -inf takes m = 0, and all its scores are 0).
+// KIND: 0 softmax, 1 sigmoid, -1 as the call says.
+template <int KIND>
 struct Scores {
-  int kind;
+  int called;
   float shift, one;  // m; or b and e^b
-  __device__ __forceinline__ Scores(int kind_, float m) : kind(kind_) {
+  __device__ __forceinline__ Scores(int called_, float m) : called(called_) {
     if (m == -INFINITY) m = 0.f;
-    shift = kind == 0 ? m : fminf(m, 0.f);
+    shift = softmax() ? m : fminf(m, 0.f);
     one = fast_exp(shift);
   }
+  __device__ __forceinline__ bool softmax() const { return KIND < 0 ? called == 0 : KIND == 0; }
   __device__ __forceinline__ float operator()(float l) const {
-    return kind == 0 ? fast_exp(l - shift) : fast_rcp(fast_exp(shift - l) + one);
+    return softmax() ? fast_exp(l - shift) : fast_rcp(fast_exp(shift - l) + one);
   }
 };
 
@@ -170,18 +211,22 @@ __device__ __forceinline__ void select_top(const float (&l)[N], int E, int K, in
   rank = 32;
   value = 0.f, expert = 0;
   if (bound > -INFINITY) {
-    int total = 0;
+    int mine = 0;
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const unsigned who = __ballot_sync(kAll, l[j] >= bound);
-      if (who) {
-        const int at = total + __popc(who & ((1u << lane) - 1u));
-        if ((who >> lane & 1u) && at < 32)
-          cand[at] = ((unsigned long long)__float_as_uint(l[j]) << 32) | (uint32_t)place<N, VEC>(j, lane);
-        total += __popc(who);
-      }
+    for (int j = 0; j < N; ++j) mine += l[j] >= bound;
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(kAll, upto, o);
+      if (lane >= o) upto += v;
     }
+    const int total = __shfl_sync(kAll, upto, 31);
     if (total <= 32) {
+      unsigned long long* at = cand + (upto - mine);
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (l[j] >= bound)
+          *at++ = ((unsigned long long)__float_as_uint(l[j]) << 32) | (uint32_t)place<N, VEC>(j, lane);
       __syncwarp();
       unsigned long long key = 0;
       if (lane < total) {
@@ -235,15 +280,18 @@ __device__ __forceinline__ double block_sum(double v, double* s) {
   return r;
 }
 
-// The end of a block with the loss: its warps' probability sums s_q [W][E], counts
-// s_cnt [E] and tokens go to its segment's, and the last block of a segment writes
-// the segment's outputs, the last segment the loss.
+// A block is done with segment g: its warps' probability sums s_q [W][E], counts s_cnt
+// [E] and tokens go to the segment's; the last block of a segment writes the
+// segment's outputs, the last segment the loss.
 template <int W>
 __device__ __forceinline__ void join_blocks(const RouterDims& d, const RouterOut& out,
                                             const RouterScratch& ws, int g, const float* s_q,
                                             const int32_t* s_cnt, int& s_tokens, int& s_bad) {
   __shared__ int s_last;
-  const bool alone = d.cps == 1;  // the segment's only block
+  // the blocks that take tokens of this segment
+  const int from = (int)((int64_t)g * d.segment / d.per_block);
+  const int to = (int)((min((int64_t)(g + 1) * d.segment, (int64_t)d.T) - 1) / d.per_block);
+  const bool alone = from == to;
   if (!alone) {
     // Joined across blocks as integers (steps of 2^-shift), so the order of the
     // atomics changes nothing; what is not finite is only noted (q of such a token is
@@ -263,7 +311,7 @@ __device__ __forceinline__ void join_blocks(const RouterDims& d, const RouterOut
       atomicAdd(&ws.tokens[g], s_tokens);
       if (s_bad) atomicOr(&ws.bad[g], 1);
       __threadfence();
-      s_last = atomicAdd(&ws.seg_done[g], 1) == d.cps - 1;
+      s_last = atomicAdd(&ws.seg_done[g], 1) == to - from;
       __threadfence();
       if (s_last) {
         s_tokens = __ldcg(&ws.tokens[g]);
@@ -318,9 +366,9 @@ __device__ __forceinline__ void join_blocks(const RouterDims& d, const RouterOut
   if (threadIdx.x == 0) *out.loss = (float)(mean / d.G);
 }
 
-// A block takes `chunk` tokens of one segment, a warp every W-th of them.
-// SHORT: K <= 32.
-template <typename T, int N, bool VEC, bool LOSS, bool SHORT>
+// A block takes per_block consecutive tokens, a warp every W-th of them; with the
+// loss, segment by segment.  SHORT: K <= 32.
+template <typename T, int N, bool VEC, bool LOSS, bool SHORT, int KIND>
 __global__ void __launch_bounds__(router_warps<N>() * 32, router_blocks<N>())
 k_router(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__ mask,
          RouterOut out, RouterScratch ws) {
@@ -331,112 +379,117 @@ k_router(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__
   __shared__ int s_tokens, s_bad;
   int32_t* s_cnt = reinterpret_cast<int32_t*>(s_dyn + (size_t)W * d.E);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t keep = sort_directions(lane);
 
-  const int g = LOSS ? blockIdx.x / d.cps : 0;
-  const int base = LOSS ? g * d.segment : 0;  // first token of the segment
-  const int t0 = base + (LOSS ? blockIdx.x % d.cps : blockIdx.x) * d.chunk;
-  const int t1 = min(min(t0 + d.chunk, LOSS ? base + d.segment : d.T), d.T);
-  if (LOSS) {
-    for (int e = threadIdx.x; e < d.E; e += blockDim.x) s_cnt[e] = 0;
-    if (threadIdx.x == 0) s_tokens = s_bad = 0;
-    __syncthreads();
-  }
-
-  float acc[LOSS ? N : 1];
+  const int first = blockIdx.x * d.per_block;
+  const int last = min(first + d.per_block, d.T);
+  for (int begin = first; begin < last;) {
+    const int g = LOSS ? begin / d.segment : 0;
+    const int end = LOSS ? (int)min((int64_t)last, (int64_t)(g + 1) * d.segment) : last;
+    float acc[LOSS ? N : 1];
+    int live_tokens = 0;
+    if constexpr (LOSS) {
 #pragma unroll
-  for (int j = 0; j < (LOSS ? N : 1); ++j) acc[j] = 0.f;
-  int live_tokens = 0;
+      for (int j = 0; j < N; ++j) acc[j] = 0.f;
+      for (int e = threadIdx.x; e < d.E; e += blockDim.x) s_cnt[e] = 0;
+      if (threadIdx.x == 0) s_tokens = s_bad = 0;
+      __syncthreads();
+    }
 
-  for (int t = t0 + warp; t < t1; t += W) {
-    float l[N];
-    load_row<T, N, VEC>(logits + (size_t)t * d.E, d.E, lane, l);
-    const bool live = mask == nullptr || mask[t] != 0;
-    float most = l[0];
+    for (int t = begin + warp; t < end; t += W) {
+      float l[N];
+      load_row<T, N, VEC>(logits + (size_t)t * d.E, d.E, lane, l);
+      const bool live = mask == nullptr || mask[t] != 0;
+      float most = -INFINITY;
 #pragma unroll
-    for (int j = 1; j < N; ++j) most = fmaxf(most, l[j]);  // passes NaN over
-    if (N == 1) most = fmaxf(most, -INFINITY);
-    const float sorted = warp_sort_down(most, lane);
-    const Scores score(d.score, __shfl_sync(kAll, sorted, 0));
+      for (int j = 0; j < N; ++j) most = fmaxf(most, l[j]);  // passes NaN over
+      const float sorted = warp_sort_down(most, keep);
+      const Scores<KIND> score(d.score, __shfl_sync(kAll, sorted, 0));
 
-    // the chosen ones of this lane: SHORT, the one with rank `rank`; else those with
-    // rank i * 32 + lane
-    float value[KI];
-    int expert[KI], rank = 0;
-    if constexpr (SHORT) {
-      select_top<N, VEC>(l, d.E, d.K, lane, __shfl_sync(kAll, sorted, d.K - 1), s_list[warp], rank,
-                         value[0], expert[0]);
-    } else {
-      select_in_turn<N, VEC>(l, d.E, d.K, lane, [&](int k, float v, int e) {
-        if (lane == 0)
-          s_list[warp][k] = ((unsigned long long)__float_as_uint(v) << 32) | (uint32_t)e;
-      });
-      __syncwarp();
+      // the chosen ones of this lane: SHORT, the one with rank `rank`; else those with
+      // rank i * 32 + lane
+      float value[KI];
+      int expert[KI], rank = 0;
+      if constexpr (SHORT) {
+        select_top<N, VEC>(l, d.E, d.K, lane, __shfl_sync(kAll, sorted, d.K - 1), s_list[warp],
+                           rank, value[0], expert[0]);
+      } else {
+        select_in_turn<N, VEC>(l, d.E, d.K, lane, [&](int k, float v, int e) {
+          if (lane == 0)
+            s_list[warp][k] = ((unsigned long long)__float_as_uint(v) << 32) | (uint32_t)e;
+        });
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < KI; ++i) {
+          const unsigned long long c = i * 32 + lane < d.K ? s_list[warp][i * 32 + lane] : 0;
+          value[i] = __uint_as_float((uint32_t)(c >> 32)), expert[i] = (int)(uint32_t)c;
+        }
+        __syncwarp();
+      }
+
+      // 1 / sum of the row's scores, where it is needed; a NaN in the row, which is in
+      // every softmax score, shows in it
+      float inv = 1.f;
+      bool nan = false;
+      if (LOSS || (score.softmax() && !d.normalise)) {
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          l[j] = score(l[j]);
+          sum += l[j];
+        }
+        sum = warp_sum(sum);
+        inv = sum == 0.f ? 0.f : fast_rcp(sum);
+        nan = sum != sum;
+      } else if (score.softmax()) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) nan |= l[j] != l[j];
+        nan = __any_sync(kAll, nan);
+      }
+      if constexpr (LOSS) {
+        if (live) {
+#pragma unroll
+          for (int j = 0; j < N; ++j) acc[j] = fmaf(l[j], inv, acc[j]);
+          ++live_tokens;
+        }
+      }
+
+      float gate[KI], total = 0.f;
 #pragma unroll
       for (int i = 0; i < KI; ++i) {
-        const unsigned long long c = i * 32 + lane < d.K ? s_list[warp][i * 32 + lane] : 0;
-        value[i] = __uint_as_float((uint32_t)(c >> 32)), expert[i] = (int)(uint32_t)c;
+        const bool mine = SHORT ? rank < d.K : i * 32 + lane < d.K;
+        gate[i] = mine ? score(value[i]) : 0.f;
+        total += gate[i];
       }
-      __syncwarp();
+      float factor = score.softmax() ? inv : score.one;
+      if (d.normalise) {
+        total = warp_sum(total);
+        factor = total == 0.f ? 0.f : fast_rcp(total);
+      }
+      factor *= d.scale;
+      if (score.softmax() && nan) factor = NAN;
+#pragma unroll
+      for (int i = 0; i < KI; ++i) {
+        const int k = SHORT ? rank : i * 32 + lane;
+        if (k < d.K) {
+          out.topk_idx[(size_t)t * d.K + k] = expert[i];
+          out.gates[(size_t)t * d.K + k] = live ? gate[i] * factor : 0.f;
+          if (LOSS && live) atomicAdd(&s_cnt[expert[i]], 1);
+        }
+      }
     }
-
-    // 1 / sum of the row's scores, where it is needed; a NaN in the row, which is in
-    // every softmax score, shows in it
-    float inv = 1.f;
-    bool nan = false;
-    if (LOSS || (d.score == 0 && !d.normalise)) {
-      float sum = 0.f;
+    if constexpr (LOSS) {
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        l[j] = score(l[j]);
-        sum += l[j];
+        const int e = place<N, VEC>(j, lane);
+        if (e < d.E) s_dyn[(size_t)warp * d.E + e] = acc[j];
       }
-      sum = warp_sum(sum);
-      inv = sum == 0.f ? 0.f : fast_rcp(sum);
-      nan = sum != sum;
-    } else {
-#pragma unroll
-      for (int j = 0; j < N; ++j) nan |= l[j] != l[j];
-      nan = __any_sync(kAll, nan);
+      if (lane == 0) atomicAdd(&s_tokens, live_tokens);
+      __syncthreads();
+      join_blocks<W>(d, out, ws, g, s_dyn, s_cnt, s_tokens, s_bad);
+      __syncthreads();  // the next segment uses the sums' memory
     }
-    if (LOSS && live) {
-#pragma unroll
-      for (int j = 0; j < (LOSS ? N : 1); ++j) acc[j] = fmaf(l[j], inv, acc[j]);
-      ++live_tokens;
-    }
-
-    float gate[KI], total = 0.f;
-#pragma unroll
-    for (int i = 0; i < KI; ++i) {
-      const bool mine = SHORT ? rank < d.K : i * 32 + lane < d.K;
-      gate[i] = mine ? score(value[i]) : 0.f;
-      total += gate[i];
-    }
-    float factor = d.score == 0 ? inv : score.one;
-    if (d.normalise) {
-      total = warp_sum(total);
-      factor = total == 0.f ? 0.f : fast_rcp(total);
-    }
-    factor *= d.scale;
-    if (d.score == 0 && nan) factor = NAN;
-#pragma unroll
-    for (int i = 0; i < KI; ++i) {
-      const int k = SHORT ? rank : i * 32 + lane;
-      if (k < d.K) {
-        out.topk_idx[(size_t)t * d.K + k] = expert[i];
-        out.gates[(size_t)t * d.K + k] = live ? gate[i] * factor : 0.f;
-        if (LOSS && live) atomicAdd(&s_cnt[expert[i]], 1);
-      }
-    }
-  }
-  if constexpr (LOSS) {
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const int e = place<N, VEC>(j, lane);
-      if (e < d.E) s_dyn[(size_t)warp * d.E + e] = acc[j];
-    }
-    if (lane == 0) atomicAdd(&s_tokens, live_tokens);
-    __syncthreads();
-    join_blocks<W>(d, out, ws, g, s_dyn, s_cnt, s_tokens, s_bad);
+    begin = end;
   }
 }
 
@@ -448,13 +501,14 @@ k_router(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__
 //   a_k = scale n_k (d_gate_k - sum_j n_j d_gate_j), n = chosen s / their sum, when
 //   normalised; else scale s_k d_gate_k
 // The chosen experts' a lie in a row of shared memory that is zero elsewhere.
-template <typename T, int N, bool VEC>
+template <typename T, int N, bool VEC, bool SHORT, int KIND>
 __global__ void __launch_bounds__(router_warps<N>() * 32)
 k_router_backward(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__ mask,
                   const int32_t* __restrict__ topk_idx, const float* __restrict__ d_gates,
                   const int32_t* __restrict__ counts, const int32_t* __restrict__ seg_tokens,
                   const float* __restrict__ d_loss, T* __restrict__ d_logits) {
   constexpr int W = router_warps<N>();
+  constexpr int KI = SHORT ? 1 : kRouterMaxK / 32;
   extern __shared__ float s_a[];  // [W][E rounded up to 4]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int E4 = (d.E + 3) & ~3;
@@ -462,64 +516,68 @@ k_router_backward(RouterDims d, const T* __restrict__ logits, const uint8_t* __r
   for (int e = lane; e < E4; e += 32) a[e] = 0.f;
   __syncwarp();
 
-  const int g = blockIdx.x / d.cps;
-  const int base = g * d.segment;
-  const int t0 = base + (blockIdx.x % d.cps) * d.chunk;
-  const int t1 = min(min(t0 + d.chunk, base + d.segment), d.T);
-
+  const int first = blockIdx.x * d.per_block;
+  const int last = min(first + d.per_block, d.T);
+  int seg = -1;
   float w[N];
-  float coef = 0.f;
-  if (d_loss != nullptr) {
-    const float n = (float)seg_tokens[g];
-    if (n > 0.f) coef = *d_loss * ((float)d.E / ((float)d.G * (float)d.K * n)) / n;
-  }
 #pragma unroll
-  for (int j = 0; j < N; ++j) {
-    const int e = place<N, VEC>(j, lane);
-    w[j] = d_loss != nullptr && e < d.E ? coef * (float)counts[(size_t)g * d.E + e] : 0.f;
-  }
+  for (int j = 0; j < N; ++j) w[j] = 0.f;
 
-  for (int t = t0 + warp; t < t1; t += W) {
+  // a token's chosen experts and their gradients, loaded one token ahead
+  int id[KI], next_id[KI];
+  float dg[KI], next_dg[KI];
+  auto fetch = [&](int t) {
+#pragma unroll
+    for (int i = 0; i < KI; ++i) {
+      const int k = i * 32 + lane;
+      const bool there = d_gates != nullptr && t < last && k < d.K;
+      next_id[i] = there ? topk_idx[(size_t)t * d.K + k] : -1;
+      next_dg[i] = there ? d_gates[(size_t)t * d.K + k] : 0.f;
+    }
+  };
+  fetch(first + warp);
+  for (int t = first + warp; t < last; t += W) {
+#pragma unroll
+    for (int i = 0; i < KI; ++i) {
+      id[i] = next_id[i] < d.E ? next_id[i] : -1;
+      dg[i] = next_dg[i];
+    }
+    fetch(t + W);
     const T* row = logits + (size_t)t * d.E;
     T* drow = d_logits + (size_t)t * d.E;
     const bool live = mask == nullptr || mask[t] != 0;
     float l[N];
-    float dl[N];
     if (live) {
       load_row<T, N, VEC>(row, d.E, lane, l);
-      int id[kRouterMaxK / 32];
-      float s[kRouterMaxK / 32], dg[kRouterMaxK / 32];
-      if (d_gates != nullptr) {
+      float s[KI];
 #pragma unroll
-        for (int i = 0; i < kRouterMaxK / 32; ++i) {
-          const int k = i * 32 + lane;
-          id[i] = -1;
-          if (k < d.K) {
-            const int e = topk_idx[(size_t)t * d.K + k];
-            dg[i] = d_gates[(size_t)t * d.K + k];
-            if (e >= 0 && e < d.E) {
-              id[i] = e;
-              s[i] = to_f32(row[e]);
-            }
-          }
+      for (int i = 0; i < KI; ++i) s[i] = id[i] >= 0 ? to_f32(row[id[i]]) : 0.f;
+      if (d_loss != nullptr && t / d.segment != seg) {
+        seg = t / d.segment;
+        const float n = (float)seg_tokens[seg];
+        const float coef = n > 0.f ? *d_loss * ((float)d.E / ((float)d.G * (float)d.K * n)) / n : 0.f;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          const int e = place<N, VEC>(j, lane);
+          w[j] = e < d.E ? coef * (float)__ldg(counts + (size_t)seg * d.E + e) : 0.f;
         }
       }
       float m = -INFINITY;
 #pragma unroll
       for (int j = 0; j < N; ++j) m = fmaxf(m, l[j]);
-      const Scores score(d.score, warp_max(m));
+      const Scores<KIND> score(d.score, warp_max(m));
       // the scores (up to their common factor), their sum and that with w
+      float rest[N];  // sigmoid: 1 - s
       float sum = 0.f, dot = 0.f;
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        if (d.score == 0) {
+        if (score.softmax()) {
           l[j] = score(l[j]);
-          dl[j] = 1.f;
         } else {
           const float x = fast_exp(score.shift - l[j]);
           const float v = fast_rcp(x + score.one);
-          // 1 - s; near s = 1 (then the shift is 0) without cancellation
-          dl[j] = l[j] > 0.f ? x * v : fmaf(-v, score.one, 1.f);
+          // near s = 1 (then the shift is 0) without cancellation
+          rest[j] = l[j] > 0.f ? x * v : fmaf(-v, score.one, 1.f);
           l[j] = v;
         }
         sum += l[j];
@@ -532,67 +590,42 @@ k_router_backward(RouterDims d, const T* __restrict__ logits, const uint8_t* __r
       if (d_gates != nullptr) {
         float total = 0.f, with = 0.f;
 #pragma unroll
-        for (int i = 0; i < kRouterMaxK / 32; ++i)
-          if (id[i] >= 0) {
-            s[i] = score(s[i]);
-            total += s[i];
-            with = fmaf(s[i], dg[i], with);
-          }
-        float factor = d.score == 0 ? inv : score.one, mean = 0.f;
+        for (int i = 0; i < KI; ++i) {
+          s[i] = id[i] >= 0 ? score(s[i]) : 0.f;
+          total += s[i];
+          with = fmaf(s[i], dg[i], with);
+        }
+        float factor = score.softmax() ? inv : score.one, mean = 0.f;
         if (d.normalise) {
           total = warp_sum(total);
           factor = total == 0.f ? 0.f : fast_rcp(total);
           mean = warp_sum(with) * factor;
-        } else if (d.score == 0) {
+        } else if (score.softmax()) {
           dot = fmaf(warp_sum(with), d.scale * inv, dot);
         }
 #pragma unroll
-        for (int i = 0; i < kRouterMaxK / 32; ++i)
+        for (int i = 0; i < KI; ++i)
           if (id[i] >= 0) a[id[i]] = d.scale * (s[i] * factor) * (dg[i] - mean);
         __syncwarp();
       }
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         const int e = place<N, VEC>(j, lane);
-        const float own = d_gates != nullptr && e < d.E ? a[e] : 0.f;
-        dl[j] *= fmaf(l[j] * inv, w[j] - dot, own);
+        l[j] = fmaf(l[j] * inv, w[j] - dot, e < E4 ? a[e] : 0.f);
+        if (!score.softmax()) l[j] *= rest[j];
       }
       if (d_gates != nullptr) {
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < kRouterMaxK / 32; ++i)
+        for (int i = 0; i < KI; ++i)
           if (id[i] >= 0) a[id[i]] = 0.f;
         __syncwarp();
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < N; ++j) dl[j] = 0.f;
+      for (int j = 0; j < N; ++j) l[j] = 0.f;
     }
-    if constexpr (VEC) {
-#pragma unroll
-      for (int c = 0; c < N / 4; ++c) {
-        const int at = c * 128 + lane * 4;
-        if (at < d.E) {
-          if constexpr (sizeof(T) == 4) {
-            *reinterpret_cast<float4*>(drow + at) =
-                make_float4(dl[4 * c], dl[4 * c + 1], dl[4 * c + 2], dl[4 * c + 3]);
-          } else {
-            const __nv_bfloat162 lo = __floats2bfloat162_rn(dl[4 * c], dl[4 * c + 1]);
-            const __nv_bfloat162 hi = __floats2bfloat162_rn(dl[4 * c + 2], dl[4 * c + 3]);
-            uint2 u;
-            u.x = *reinterpret_cast<const uint32_t*>(&lo);
-            u.y = *reinterpret_cast<const uint32_t*>(&hi);
-            *reinterpret_cast<uint2*>(drow + at) = u;
-          }
-        }
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const int at = j * 32 + lane;
-        if (at < d.E) drow[at] = (T)dl[j];
-      }
-    }
+    store_row<T, N, VEC>(drow, d.E, lane, l);
   }
 }
 
@@ -618,9 +651,9 @@ RouterScratch router_scratch(const RouterDims& d, void* ws) {
   return r;
 }
 
-// Launch shape of a router kernel: blocks for one round of what fits the GPU at
-// once, so that all warps take equally many tokens; whole rounds of the block's
-// warps, and at most 64 tokens a warp, so that a warp's fp32 sums stay short.
+// Launch shape of a router kernel: as many blocks as fit the GPU at once, with
+// equally many tokens: whole rounds of the block's warps, and at most 64 tokens a
+// warp, so that a warp's fp32 sums stay short.
 template <typename Kernel>
 static cudaError_t plan_blocks(Kernel* k, int warps, size_t smem, RouterDims& d) {
   if (smem > (32u << 10)) {
@@ -634,74 +667,60 @@ static cudaError_t plan_blocks(Kernel* k, int warps, size_t smem, RouterDims& d)
   if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, warps * 32, smem);
   if (e != cudaSuccess) return e;
   const int64_t blocks = std::max(1, sms * per_sm);
-  // blocks a segment in that round, or one where there are more segments than blocks
-  const int64_t each = std::max<int64_t>(1, blocks / d.G);
-  int64_t chunk = (d.segment + each - 1) / each;
-  chunk = (chunk + warps - 1) / warps * warps;
-  d.chunk = (int)std::min<int64_t>(chunk, 64 * warps);
-  d.cps = (d.segment + d.chunk - 1) / d.chunk;
+  const int64_t each = ((int64_t)d.T + blocks * warps - 1) / (blocks * warps);  // tokens a warp
+  d.per_block = (int)std::min<int64_t>(each, 64) * warps;
+  d.blocks = (int)(((int64_t)d.T + d.per_block - 1) / d.per_block);
   return cudaSuccess;
 }
 
-template <typename T, int N, bool VEC, bool LOSS, bool SHORT>
+template <typename T, int N, bool VEC, bool LOSS, bool SHORT, int KIND>
 static cudaError_t forward(RouterDims d, const void* logits, const uint8_t* mask,
                            const RouterOut& out, const RouterScratch& ws, cudaStream_t st) {
   constexpr int W = router_warps<N>();
-  auto* kernel = k_router<T, N, VEC, LOSS, SHORT>;
+  auto* kernel = k_router<T, N, VEC, LOSS, SHORT, KIND>;
   const size_t smem = LOSS ? (size_t)d.E * 4 * (W + 1) : 0;
-  if (!LOSS) d.G = 1, d.segment = d.T;
   cudaError_t e = plan_blocks(kernel, W, smem, d);
   if (e != cudaSuccess) return e;
-  if (LOSS) {  // one block a segment: only the count of finished segments is used
-    const size_t zero = d.cps > 1 ? ws.zero_bytes : (d.G > 1 ? 4 : 0);
-    if (zero) e = cudaMemsetAsync(ws.done, 0, zero, st);
+  if (LOSS && (d.blocks > 1 || d.G > 1)) {
+    // (one block joins nothing and only counts the segments)
+    e = cudaMemsetAsync(ws.done, 0, d.blocks > 1 ? ws.zero_bytes : 4, st);
     if (e != cudaSuccess) return e;
   }
-  kernel<<<d.G * d.cps, W * 32, smem, st>>>(d, (const T*)logits, mask, out, ws);
+  kernel<<<d.blocks, W * 32, smem, st>>>(d, (const T*)logits, mask, out, ws);
   return cudaGetLastError();
 }
 
-template <typename T, int N, bool VEC>
-static cudaError_t backward(RouterDims d, const void* logits, const uint8_t* mask,
-                            const int32_t* topk_idx, const float* d_gates, const int32_t* counts,
-                            const int32_t* seg_tokens, const float* d_loss, void* d_logits,
-                            cudaStream_t st) {
-  constexpr int W = router_warps<N>();
-  const size_t smem = (size_t)W * ((d.E + 3) & ~3) * 4;
-  const cudaError_t e = plan_blocks(k_router_backward<T, N, VEC>, W, smem, d);
-  if (e != cudaSuccess) return e;
-  k_router_backward<T, N, VEC><<<d.G * d.cps, W * 32, smem, st>>>(
-      d, (const T*)logits, mask, topk_idx, d_gates, counts, seg_tokens, d_loss, (T*)d_logits);
-  return cudaGetLastError();
-}
-
-// Calls f with the kernel's row shape: values per lane, and whether they lie in
-// vectors of four.  Rows of up to 128 experts are spread over all lanes one
-// value at a time (vectors would leave lanes empty); so are rows that 4 does not
-// divide and rows of more than 1024.
+// Calls f with the kernel's row shape: values per lane, whether they lie in vectors
+// of four, K <= 32, and the score.  Rows of up to 128 experts are spread over all
+// lanes one value at a time (vectors would leave lanes empty); so are rows that 4
+// does not divide, rows of more than 1024, and K > 32.
 template <typename T, typename F>
-static cudaError_t by_row(int E, F&& f) {
-#define ROW(n, vec) return f.template operator()<T, n, vec>()
-  if (E % 4 == 0 && E > 128 && E <= 1024) {
+static cudaError_t by_row(const RouterDims& d, F&& f) {
+#define ROW(n)                                                   \
+  return d.score == 0 ? f.template operator()<T, n, true, true, 0>() \
+                      : f.template operator()<T, n, true, true, 1>()
+#define LONG_ROW(n)                                                   \
+  return d.K <= 32 ? f.template operator()<T, n, false, true, -1>() \
+                   : f.template operator()<T, n, false, false, -1>()
+  const int E = d.E;
+  if (E % 4 == 0 && E > 128 && E <= 1024 && d.K <= 32) {
     switch ((E + 127) / 128) {
-      case 2: ROW(8, true);
-      case 3: ROW(12, true);
-      case 4: ROW(16, true);
-      case 5: ROW(20, true);
-      case 6: ROW(24, true);
-      case 7: ROW(28, true);
-      default: ROW(32, true);
+      case 2: ROW(8);
+      case 3: ROW(12);
+      case 4: ROW(16);
+      case 5: ROW(20);
+      case 6: ROW(24);
+      case 7: ROW(28);
+      default: ROW(32);
     }
   }
-  if (E <= 32) ROW(1, false);
-  if (E <= 64) ROW(2, false);
-  if (E <= 128) ROW(4, false);
-  if (E <= 256) ROW(8, false);
-  if (E <= 512) ROW(16, false);
-  if (E <= 1024) ROW(32, false);
-  if (E <= 2048) ROW(64, false);
-  ROW(128, false);
+  if (E <= 32) LONG_ROW(1);
+  if (E <= 128) LONG_ROW(4);
+  if (E <= 512) LONG_ROW(16);
+  if (E <= 1024) LONG_ROW(32);
+  LONG_ROW(128);
 #undef ROW
+#undef LONG_ROW
 }
 
 struct ForwardCall {
@@ -711,13 +730,10 @@ struct ForwardCall {
   const RouterOut& out;
   const RouterScratch& ws;
   cudaStream_t st;
-  template <typename T, int N, bool VEC>
+  template <typename T, int N, bool VEC, bool SHORT, int KIND>
   cudaError_t operator()() const {
-    if (out.loss == nullptr)
-      return d.K <= 32 ? forward<T, N, VEC, false, true>(d, logits, mask, out, ws, st)
-                       : forward<T, N, VEC, false, false>(d, logits, mask, out, ws, st);
-    return d.K <= 32 ? forward<T, N, VEC, true, true>(d, logits, mask, out, ws, st)
-                     : forward<T, N, VEC, true, false>(d, logits, mask, out, ws, st);
+    return out.loss == nullptr ? forward<T, N, VEC, false, SHORT, KIND>(d, logits, mask, out, ws, st)
+                               : forward<T, N, VEC, true, SHORT, KIND>(d, logits, mask, out, ws, st);
   }
 };
 
@@ -732,10 +748,17 @@ struct BackwardCall {
   const float* d_loss;
   void* d_logits;
   cudaStream_t st;
-  template <typename T, int N, bool VEC>
+  template <typename T, int N, bool VEC, bool SHORT, int KIND>
   cudaError_t operator()() const {
-    return backward<T, N, VEC>(d, logits, mask, topk_idx, d_gates, counts, seg_tokens, d_loss,
-                               d_logits, st);
+    constexpr int W = router_warps<N>();
+    auto* kernel = k_router_backward<T, N, VEC, SHORT, KIND>;
+    const size_t smem = (size_t)W * ((d.E + 3) & ~3) * 4;
+    RouterDims r = d;
+    const cudaError_t e = plan_blocks(kernel, W, smem, r);
+    if (e != cudaSuccess) return e;
+    kernel<<<r.blocks, W * 32, smem, st>>>(r, (const T*)logits, mask, topk_idx, d_gates, counts,
+                                           seg_tokens, d_loss, (T*)d_logits);
+    return cudaGetLastError();
   }
 };
 
@@ -743,7 +766,7 @@ cudaError_t launch_router_forward(const RouterDims& d, const void* logits, const
                                   const RouterOut& out, const RouterScratch& ws, cudaStream_t st,
                                   int* launches) {
   const ForwardCall call{d, logits, mask, out, ws, st};
-  const cudaError_t e = d.bf16 ? by_row<__nv_bfloat16>(d.E, call) : by_row<float>(d.E, call);
+  const cudaError_t e = d.bf16 ? by_row<__nv_bfloat16>(d, call) : by_row<float>(d, call);
   if (e == cudaSuccess) *launches += 1;
   return e;
 }
@@ -755,7 +778,7 @@ cudaError_t launch_router_backward(const RouterDims& d, const void* logits, cons
                                    int* launches) {
   const BackwardCall call{d,      logits,     mask,   topk_idx, d_gates,
                           counts, seg_tokens, d_loss, d_logits, st};
-  const cudaError_t e = d.bf16 ? by_row<__nv_bfloat16>(d.E, call) : by_row<float>(d.E, call);
+  const cudaError_t e = d.bf16 ? by_row<__nv_bfloat16>(d, call) : by_row<float>(d, call);
   if (e == cudaSuccess) *launches += 1;
   return e;
 }
