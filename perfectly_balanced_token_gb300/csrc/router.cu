@@ -119,14 +119,6 @@ __device__ __forceinline__ float warp_sort_down(float v, uint32_t keep) {
   return v;
 }
 
-// Rank of a logit (not NaN) as an integer: larger logits first, equal ones (-0 and
-// +0 too) by ascending expert.
-__device__ __forceinline__ unsigned long long rank_key(float v, int e) {
-  const uint32_t u = __float_as_uint(v + 0.0f);
-  const uint32_t k = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
-  return ((unsigned long long)k << 32) | (uint32_t)~e;
-}
-
 // e^x in one multiplication and the hardware's power of two (off by 2 ulp and by
 // what rounding x log2(e) leaves: |x| 2^-24); results below 2^-126 are 0.
 __device__ __forceinline__ float fast_exp(float x) {
@@ -197,61 +189,119 @@ __device__ __forceinline__ void select_in_turn(const float (&l)[N], int E, int K
   }
 }
 
-// The K <= 32 largest of a token: lanes with 0 <= rank < K hold one each.
+// A bf16 logit (not NaN) and its expert as one integer: larger logits first, equal
+// ones (-0 and +0 too) by ascending expert.
+__device__ __forceinline__ uint32_t bf16_key(float v, int e) {
+  const uint32_t u = __float_as_uint(v + 0.0f);
+  return ((u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u)) & 0xffff0000u) | (0xffffu - (uint32_t)e);
+}
+
+__device__ __forceinline__ float bf16_key_logit(uint32_t k) {
+  k &= 0xffff0000u;
+  return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k & 0xffff0000u);
+}
+
+// Candidates of a warp: all logits that reach a bound, at most 32.
+struct __align__(16) Candidates {
+  uint32_t value[32];  // bf16 rows: the key above; fp32 rows: the logit
+  int32_t expert[32];
+};
+
+// The K <= 32 largest of a token, the k-th to lane k.
 //
-// The K-th largest of the 32 lanes' maxima is a bound that at least K values reach,
-// and few more (K = 8 of 384 normal logits: 9 on average), so the values that reach
-// it are gathered, and each finds its rank by counting the larger ones.  More than
-// 32 of them (ties) and a bound of -inf (which the places past the row's end reach
-// too) take the K largest one after the other.
-template <int N, bool VEC>
-__device__ __forceinline__ void select_top(const float (&l)[N], int E, int K, int lane,
-                                           float bound, unsigned long long* cand, int& rank,
-                                           float& value, int& expert) {
-  rank = 32;
+// The logits that reach a bound are gathered, and each finds its rank by counting the
+// larger ones; any bound that K to 32 logits reach gives the same result.  The one of
+// the token before is tried first, moved each time so that about `target` logits
+// reach it (on the model that their number falls off exponentially up to the row's
+// largest, m).  Where it fails, the K-th largest of the lanes' maxima is a bound that
+// at least K logits reach.  More than 32 (ties) and a bound of -inf (which the
+// places past the row's end reach too) take the K largest one after the other.
+// 512 of 593 instructions a token at 65536 x 384, K = 8 were spent on sorting the
+// maxima for every token and on gathering with 64-bit keys; this takes ...
+template <typename T, int N, bool VEC>
+__device__ __forceinline__ void select_top(const float (&l)[N], const T* __restrict__ row, int E,
+                                           int K, int lane, float most, float m, uint32_t keep,
+                                           float& guess, Candidates& list, float& value,
+                                           int& expert) {
+  constexpr int NW = (N + 31) / 32;
   value = 0.f, expert = 0;
-  if (bound > -INFINITY) {
+  const float target = (float)min(K + 8, (K + 30) / 2);
+#pragma unroll 1
+  for (int exact = 0; exact < 2; ++exact) {
+    const float bound = exact ? __shfl_sync(kAll, warp_sort_down(most, keep), K - 1) : guess;
+    if (!(bound > -INFINITY)) continue;
+    uint32_t reach[NW] = {};
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (l[j] >= bound) reach[j / 32] |= 1u << (j & 31);
     int mine = 0;
 #pragma unroll
-    for (int j = 0; j < N; ++j) mine += l[j] >= bound;
-    int upto = mine;
+    for (int w = 0; w < NW; ++w) mine += __popc(reach[w]);
+    const int total = __reduce_add_sync(kAll, mine);
+    // the next token's bound
+    const float off = 1.f - __log2f(target) * fast_rcp(__log2f((float)max(total, 2)));
+    guess = fmaf((exact ? 1.f : 0.25f) * (m - bound), off, bound);
+    if (!(fabsf(guess) < INFINITY)) guess = -INFINITY;
+    if (total < K || total > 32) continue;
+
+    int base = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(kAll, upto, o);
-      if (lane >= o) upto += v;
-    }
-    const int total = __shfl_sync(kAll, upto, 31);
-    if (total <= 32) {
-      unsigned long long* at = cand + (upto - mine);
-#pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (l[j] >= bound)
-          *at++ = ((unsigned long long)__float_as_uint(l[j]) << 32) | (uint32_t)place<N, VEC>(j, lane);
-      __syncwarp();
-      unsigned long long key = 0;
-      if (lane < total) {
-        const unsigned long long c = cand[lane];
-        value = __uint_as_float((uint32_t)(c >> 32)), expert = (int)(uint32_t)c;
-        key = rank_key(value, expert);
+    for (int w = 0; w < NW; ++w) {
+      while (true) {
+        const unsigned who = __ballot_sync(kAll, reach[w] != 0);
+        if (!who) break;
+        if (reach[w]) {
+          const int j = w * 32 + __ffs(reach[w]) - 1;
+          reach[w] &= reach[w] - 1;
+          const int at = base + __popc(who & ((1u << lane) - 1u));
+          const int e = place<N, VEC>(j, lane);
+          const float v = to_f32(row[e]);
+          list.value[at] = sizeof(T) == 2 ? bf16_key(v, e) : __float_as_uint(v);
+          list.expert[at] = e;
+        }
+        base += __popc(who);
       }
-      __syncwarp();
-      cand[lane] = key;  // 0 past the last: counts for nobody
-      __syncwarp();
-      int r = 0;
+    }
+    if (lane >= total) list.value[lane] = sizeof(T) == 2 ? 0u : 0xff800000u;  // larger than none
+    __syncwarp();
+    const uint32_t own = list.value[lane];
+    const int e = lane < total ? list.expert[lane] : 0;
+    int r = 0;
 #pragma unroll 1
-      for (int i = 0; i < total; i += 4) {
-        const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(cand + i);
-        const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(cand + i + 2);
-        r += (a.x > key) + (a.y > key) + (b.x > key) + (b.y > key);
+    for (int i = 0; i < total; i += 4) {
+      const uint4 c = *reinterpret_cast<const uint4*>(&list.value[i]);
+      if constexpr (sizeof(T) == 2) {
+        r += (c.x > own) + (c.y > own) + (c.z > own) + (c.w > own);
+      } else {
+        const float f = __uint_as_float(own);
+        r += (__uint_as_float(c.x) > f) + (__uint_as_float(c.y) > f) +
+             (__uint_as_float(c.z) > f) + (__uint_as_float(c.w) > f);
       }
-      __syncwarp();
-      if (lane < total) rank = r;
-      return;
     }
+    if constexpr (sizeof(T) == 4) {
+      // equal logits share a rank: then the lower expert goes first
+      if (__reduce_add_sync(kAll, lane < total ? r : 0) != total * (total - 1) / 2) {
+        for (int i = 0; i < total; ++i)
+          r += __uint_as_float(list.value[i]) == __uint_as_float(own) && list.expert[i] < e;
+      }
+    }
+    // to the lanes in their order, so that nothing depends on how they were found
+    __syncwarp();
+    if (lane < total && r < K) {
+      list.value[r] = own;
+      list.expert[r] = e;
+    }
+    __syncwarp();
+    if (lane < K) {
+      const uint32_t v = list.value[lane];
+      value = sizeof(T) == 2 ? bf16_key_logit(v) : __uint_as_float(v);
+      expert = list.expert[lane];
+    }
+    __syncwarp();
+    return;
   }
-  __syncwarp();
   select_in_turn<N, VEC>(l, E, K, lane, [&](int k, float v, int e) {
-    if (lane == k) value = v, expert = e, rank = k;
+    if (lane == k) value = v, expert = e;
   });
 }
 
@@ -374,12 +424,14 @@ k_router(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__
          RouterOut out, RouterScratch ws) {
   constexpr int W = router_warps<N>();
   constexpr int KI = SHORT ? 1 : kRouterMaxK / 32;
-  __shared__ __align__(16) unsigned long long s_list[W][SHORT ? 32 : kRouterMaxK];  // candidates
+  __shared__ Candidates s_cand[SHORT ? W : 1];
+  __shared__ unsigned long long s_list[SHORT ? 1 : W][kRouterMaxK];
   extern __shared__ float s_dyn[];  // LOSS: the warps' sums [W][E], then counts [E]
   __shared__ int s_tokens, s_bad;
   int32_t* s_cnt = reinterpret_cast<int32_t*>(s_dyn + (size_t)W * d.E);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t keep = sort_directions(lane);
+  float guess = -INFINITY;
 
   const int first = blockIdx.x * d.per_block;
   const int last = min(first + d.per_block, d.T);
@@ -398,21 +450,21 @@ k_router(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__
 
     for (int t = begin + warp; t < end; t += W) {
       float l[N];
-      load_row<T, N, VEC>(logits + (size_t)t * d.E, d.E, lane, l);
+      const T* row = logits + (size_t)t * d.E;
+      load_row<T, N, VEC>(row, d.E, lane, l);
       const bool live = mask == nullptr || mask[t] != 0;
       float most = -INFINITY;
 #pragma unroll
       for (int j = 0; j < N; ++j) most = fmaxf(most, l[j]);  // passes NaN over
-      const float sorted = warp_sort_down(most, keep);
-      const Scores<KIND> score(d.score, __shfl_sync(kAll, sorted, 0));
+      const float m = warp_max(most);
+      const Scores<KIND> score(d.score, m);
 
-      // the chosen ones of this lane: SHORT, the one with rank `rank`; else those with
-      // rank i * 32 + lane
+      // the chosen ones of this lane: those with rank i * 32 + lane
       float value[KI];
-      int expert[KI], rank = 0;
+      int expert[KI];
       if constexpr (SHORT) {
-        select_top<N, VEC>(l, d.E, d.K, lane, __shfl_sync(kAll, sorted, d.K - 1), s_list[warp],
-                           rank, value[0], expert[0]);
+        select_top<T, N, VEC>(l, row, d.E, d.K, lane, most, m, keep, guess, s_cand[warp],
+                              value[0], expert[0]);
       } else {
         select_in_turn<N, VEC>(l, d.E, d.K, lane, [&](int k, float v, int e) {
           if (lane == 0)
@@ -457,8 +509,7 @@ k_router(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__
       float gate[KI], total = 0.f;
 #pragma unroll
       for (int i = 0; i < KI; ++i) {
-        const bool mine = SHORT ? rank < d.K : i * 32 + lane < d.K;
-        gate[i] = mine ? score(value[i]) : 0.f;
+        gate[i] = i * 32 + lane < d.K ? score(value[i]) : 0.f;
         total += gate[i];
       }
       float factor = score.softmax() ? inv : score.one;
@@ -470,7 +521,7 @@ k_router(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__
       if (score.softmax() && nan) factor = NAN;
 #pragma unroll
       for (int i = 0; i < KI; ++i) {
-        const int k = SHORT ? rank : i * 32 + lane;
+        const int k = i * 32 + lane;
         if (k < d.K) {
           out.topk_idx[(size_t)t * d.K + k] = expert[i];
           out.gates[(size_t)t * d.K + k] = live ? gate[i] * factor : 0.f;
