@@ -127,12 +127,21 @@ def _check(rc: int, what: str):
         raise MoonepError(rc, what)
 
 
+# The current stream's handle without a torch.cuda.Stream object around it (measured on the host
+# of a GB300: 0.1 us against 2.9 us a call); None where this torch does not have the two calls.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None and _raw_device is not None:
+            torch.cuda.init()
+            return _raw_stream(_raw_device())
         stream = torch.cuda.current_stream()
     if isinstance(stream, torch.cuda.Stream):
         stream = stream.cuda_stream
-    return ctypes.c_void_p(int(stream))
+    return int(stream)
 
 
 def _ptr(t, dtype, numel, name, allow_none=False):
@@ -140,6 +149,9 @@ def _ptr(t, dtype, numel, name, allow_none=False):
         if allow_none:
             return None
         raise ValueError(f"{name} is required")
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.is_cuda and t.is_contiguous()
+            and (numel is None or t.numel() == numel)):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
@@ -148,14 +160,21 @@ def _ptr(t, dtype, numel, name, allow_none=False):
         raise ValueError(f"{name} must be contiguous")
     if numel is not None and t.numel() != numel:
         raise ValueError(f"{name} has {t.numel()} elements, expected {numel}")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
+
+
+_workspace_bytes: dict = {}  # of dims already asked for, by their fields
 
 
 def moonep_plan_workspace_bytes(d: moonep_dims) -> int:
-    n = ctypes.c_size_t(0)
-    _check(library().moonep_plan_workspace_bytes(ctypes.byref(d), ctypes.byref(n)),
-           "moonep_plan_workspace_bytes")
-    return n.value
+    key = bytes(d)
+    size = _workspace_bytes.get(key)
+    if size is None:
+        n = ctypes.c_size_t(0)
+        _check(library().moonep_plan_workspace_bytes(ctypes.byref(d), ctypes.byref(n)),
+               "moonep_plan_workspace_bytes")
+        size = _workspace_bytes[key] = n.value
+    return size
 
 
 def moonep_get_plan_layout(d: moonep_dims) -> moonep_plan_layout:

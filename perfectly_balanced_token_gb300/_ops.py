@@ -71,11 +71,18 @@ def router_dims(T, E, K, segment=0, score="softmax", normalise=True, scale=1.0,
                               scale)
 
 
+_workspace_bytes: dict = {}  # of dims already asked for, by their fields
+
+
 def moonep_router_workspace_bytes(rd: moonep_router_dims) -> int:
-    n = ctypes.c_size_t(0)
-    _check(library().moonep_router_workspace_bytes(ctypes.byref(rd), ctypes.byref(n)),
-           "moonep_router_workspace_bytes")
-    return n.value
+    key = bytes(rd)
+    size = _workspace_bytes.get(key)
+    if size is None:
+        n = ctypes.c_size_t(0)
+        _check(library().moonep_router_workspace_bytes(ctypes.byref(rd), ctypes.byref(n)),
+               "moonep_router_workspace_bytes")
+        size = _workspace_bytes[key] = n.value
+    return size
 
 
 def moonep_router_forward(rd, logits, topk_idx, gates, token_mask=None, ws=None, counts=None,

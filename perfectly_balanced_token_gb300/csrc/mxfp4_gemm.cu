@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(MxCfg<CG>::kThreads, 1)
 k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_wh,
              const __grid_constant__ CUtensorMap tm_ws, const __grid_constant__ CUtensorMap tm_sa,
              const __grid_constant__ CUtensorMap tm_sh, const __grid_constant__ CUtensorMap tm_ss,
-             const __grid_constant__ CUtensorMap tm_y, int K, int N, PlanPtrs p,
+             const __grid_constant__ CUtensorMap tm_y, int K, int N, int rank_rows, PlanPtrs p,
              uint16_t* __restrict__ y) {
   using Cfg = MxCfg<CG>;
   constexpr int STAGES = Cfg::kStages, SLOTS = Cfg::kScaleSlots;
@@ -140,7 +140,8 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
   const uint32_t crank = kPair ? pair_rank() : 0;
   const bool leader = crank == 0;
   if (plan_failed(p.status)) return;  // uniform over the pair: before any barrier
-  if (p.counters[MOONEP_CNT_TILE_ROWS] != CG * kMmaM) return;
+  // the other kernel's tiles; where a rank has at most 128 rows this one takes all
+  if (p.counters[MOONEP_CNT_TILE_ROWS] != CG * kMmaM && rank_rows > kMmaM) return;
   const int NT = (N + kMxBN - 1) / kMxBN;
   const int total = p.counters[MOONEP_CNT_MTILES] * NT;
   const int KB = (K + kMxK - 1) / kMxK;
@@ -516,25 +517,15 @@ static bool encode_out(CUtensorMap* m, const void* base, uint64_t N, uint64_t ro
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-struct MxOperands {
-  const uint8_t *a, *a_scales, *home, *home_scales, *slot, *slot_scales;
-  uint64_t a_rows, home_rows, slot_rows;
+struct MxMaps {
+  CUtensorMap a, a_scales, home_scales, slot_scales, y;
 };
 
 template <int CG>
-static cudaError_t launch_mx(const Dims& d, const PlanPtrs& p, const MxOperands& m, uint16_t* y,
+static cudaError_t launch_mx(const Dims& d, const PlanPtrs& p, const MxMaps& m,
+                             const CUtensorMap& home, const CUtensorMap& slot, uint16_t* y,
                              cudaStream_t st) {
   using Cfg = MxCfg<CG>;
-  const uint64_t bytes = d.H / 2, pitch = MOONEP_MXFP4_SCALE_PITCH(d.H);
-  CUtensorMap ta, twh, tws, tsa, tsh, tss, ty;
-  if (!encode_bytes(&ta, m.a, bytes, m.a_rows, 128, kMmaM) ||
-      !encode_bytes(&twh, m.home, bytes, m.home_rows, 128, Cfg::kBRows) ||
-      !encode_bytes(&tws, m.slot, bytes, m.slot_rows, 128, Cfg::kBRows) ||
-      !encode_bytes(&tsa, m.a_scales, pitch, m.a_rows, 16, kMmaM) ||
-      !encode_bytes(&tsh, m.home_scales, pitch, m.home_rows, 16, kMxBN) ||
-      !encode_bytes(&tss, m.slot_scales, pitch, m.slot_rows, 16, kMxBN) ||
-      !encode_out(&ty, y, (uint64_t)d.Hp, m.a_rows))
-    return cudaErrorInvalidValue;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = CG;
@@ -560,7 +551,8 @@ static cudaError_t launch_mx(const Dims& d, const PlanPtrs& p, const MxOperands&
   }
   const long long items = (long long)d.max_mtiles * ((d.Hp + kMxBN - 1) / kMxBN);
   cfg.gridDim = dim3((unsigned)std::min<long long>(grid, CG * items));
-  return cudaLaunchKernelEx(&cfg, k_mxfp4_gemm<CG>, ta, twh, tws, tsa, tsh, tss, ty, d.H, d.Hp, p, y);
+  return cudaLaunchKernelEx(&cfg, k_mxfp4_gemm<CG>, m.a, home, slot, m.a_scales, m.home_scales,
+                            m.slot_scales, m.y, d.H, d.Hp, d.C, p, y);
 }
 
 cudaError_t launch_mxfp4_grouped_gemm(const Dims& d, const PlanPtrs& p, const uint8_t* a,
@@ -569,19 +561,37 @@ cudaError_t launch_mxfp4_grouped_gemm(const Dims& d, const PlanPtrs& p, const ui
                                       const uint8_t* slot_scales, void* y, cudaStream_t st,
                                       int* launches) {
   const bool slots = slot != nullptr && d.B > 0;
-  const uint64_t home_rows = (uint64_t)d.E * d.Hp;
-  const MxOperands m{a, a_scales, home, home_scales, slots ? slot : home,
-                     slots ? slot_scales : home_scales, (uint64_t)d.R * d.C, home_rows,
-                     slots ? (uint64_t)d.R * d.B * d.Hp : home_rows};
-  // the plan's tile height is on the device: the variant it did not choose
-  // returns at once (as in the bf16 product)
-  if (d.tile_m != 2 * kMmaM) {
-    const cudaError_t e = launch_mx<1>(d, p, m, (uint16_t*)y, st);
+  const uint64_t bytes = d.H / 2, pitch = MOONEP_MXFP4_SCALE_PITCH(d.H);
+  const uint64_t rows = (uint64_t)d.R * d.C, home_rows = (uint64_t)d.E * d.Hp;
+  const uint64_t slot_rows = (uint64_t)d.R * d.B * d.Hp;
+  MxMaps m;
+  if (!encode_bytes(&m.a, a, bytes, rows, 128, kMmaM) ||
+      !encode_bytes(&m.a_scales, a_scales, pitch, rows, 16, kMmaM) ||
+      !encode_bytes(&m.home_scales, home_scales, pitch, home_rows, 16, kMxBN) ||
+      !encode_out(&m.y, y, (uint64_t)d.Hp, rows))
+    return cudaErrorInvalidValue;
+  m.slot_scales = m.home_scales;
+  if (slots && !encode_bytes(&m.slot_scales, slot_scales, pitch, slot_rows, 16, kMxBN))
+    return cudaErrorInvalidValue;
+  CUtensorMap wh, ws;
+  auto weights = [&](uint32_t box_rows) {
+    if (!encode_bytes(&wh, home, bytes, home_rows, 128, box_rows)) return false;
+    ws = wh;
+    return !slots || encode_bytes(&ws, slot, bytes, slot_rows, 128, box_rows);
+  };
+  // The plan's tile height is on the device: the variant it did not choose returns at
+  // once (as in the bf16 product).  Where no rank has more than 128 rows, no tile has,
+  // whatever its height, and the 128-row kernel takes both.
+  const bool pair = d.tile_m != kMmaM && d.C > kMmaM;
+  if (d.tile_m != 2 * kMmaM || !pair) {
+    if (!weights(MxCfg<1>::kBRows)) return cudaErrorInvalidValue;
+    const cudaError_t e = launch_mx<1>(d, p, m, wh, ws, (uint16_t*)y, st);
     if (e != cudaSuccess) return e;
     *launches += 1;
   }
-  if (d.tile_m != kMmaM) {
-    const cudaError_t e = launch_mx<2>(d, p, m, (uint16_t*)y, st);
+  if (pair) {
+    if (!weights(MxCfg<2>::kBRows)) return cudaErrorInvalidValue;
+    const cudaError_t e = launch_mx<2>(d, p, m, wh, ws, (uint16_t*)y, st);
     if (e != cudaSuccess) return e;
     *launches += 1;
   }

@@ -7,6 +7,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "ops.h"
 
@@ -196,36 +197,32 @@ __device__ __forceinline__ uint32_t bf16_key(float v, int e) {
   return ((u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u)) & 0xffff0000u) | (0xffffu - (uint32_t)e);
 }
 
-__device__ __forceinline__ float bf16_key_logit(uint32_t k) {
-  k &= 0xffff0000u;
-  return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k & 0xffff0000u);
-}
-
 // Candidates of a warp: all logits that reach a bound, at most 32.
 struct __align__(16) Candidates {
   uint32_t value[32];  // bf16 rows: the key above; fp32 rows: the logit
   int32_t expert[32];
 };
 
-// The K <= 32 largest of a token, the k-th to lane k.
+// The K <= 32 largest of a token: a lane with rank < K holds the one of that rank.
 //
-// The logits that reach a bound are gathered, and each finds its rank by counting the
-// larger ones; any bound that K to 32 logits reach gives the same result.  The one of
-// the token before is tried first, moved each time so that about `target` logits
-// reach it (on the model that their number falls off exponentially up to the row's
-// largest, m).  Where it fails, the K-th largest of the lanes' maxima is a bound that
-// at least K logits reach.  More than 32 (ties) and a bound of -inf (which the
-// places past the row's end reach too) take the K largest one after the other.
-// 512 of 593 instructions a token at 65536 x 384, K = 8 were spent on sorting the
-// maxima for every token and on gathering with 64-bit keys; this takes ...
+// The logits that reach a bound are gathered, one a lane, and each finds its rank by
+// counting the larger ones; any bound that K to 32 logits reach gives the same
+// result.  The bound of the token before is tried first, moved each time so that
+// about `target` logits reach it (on the model that their number falls off
+// exponentially up to the row's largest, m; on normal logits nine tokens of ten
+// succeed).  Where it fails, the K-th largest of the lanes' maxima is a bound that at
+// least K logits reach.  More than 32 (ties) and a bound of -inf (which the places
+// past the row's end reach too) take the K largest one after the other.
 template <typename T, int N, bool VEC>
 __device__ __forceinline__ void select_top(const float (&l)[N], const T* __restrict__ row, int E,
                                            int K, int lane, float most, float m, uint32_t keep,
-                                           float& guess, Candidates& list, float& value,
+                                           float& guess, Candidates& list, int& rank, float& value,
                                            int& expert) {
   constexpr int NW = (N + 31) / 32;
+  rank = 32;
   value = 0.f, expert = 0;
   const float target = (float)min(K + 8, (K + 30) / 2);
+  const float pull = fast_rcp(target * __logf(target));
 #pragma unroll 1
   for (int exact = 0; exact < 2; ++exact) {
     const float bound = exact ? __shfl_sync(kAll, warp_sort_down(most, keep), K - 1) : guess;
@@ -238,70 +235,54 @@ __device__ __forceinline__ void select_top(const float (&l)[N], const T* __restr
 #pragma unroll
     for (int w = 0; w < NW; ++w) mine += __popc(reach[w]);
     const int total = __reduce_add_sync(kAll, mine);
-    // the next token's bound
-    const float off = 1.f - __log2f(target) * fast_rcp(__log2f((float)max(total, 2)));
-    guess = fmaf((exact ? 1.f : 0.25f) * (m - bound), off, bound);
+    // the next token's bound: a number off by a part x of the target asks for a step of
+    // x / log(target) of the way to m; a quarter of it, but all after a fresh start
+    guess = fmaf((m - bound) * pull, (exact ? 1.f : 0.25f) * ((float)min(total, 64) - target), bound);
     if (!(fabsf(guess) < INFINITY)) guess = -INFINITY;
     if (total < K || total > 32) continue;
 
     int base = 0;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      while (true) {
-        const unsigned who = __ballot_sync(kAll, reach[w] != 0);
-        if (!who) break;
-        if (reach[w]) {
-          const int j = w * 32 + __ffs(reach[w]) - 1;
-          reach[w] &= reach[w] - 1;
-          const int at = base + __popc(who & ((1u << lane) - 1u));
-          const int e = place<N, VEC>(j, lane);
-          const float v = to_f32(row[e]);
-          list.value[at] = sizeof(T) == 2 ? bf16_key(v, e) : __float_as_uint(v);
-          list.expert[at] = e;
-        }
+    for (int w = 0; w < NW; ++w)
+      while (const unsigned who = __ballot_sync(kAll, reach[w] != 0)) {
+        if (reach[w])
+          list.expert[base + __popc(who & ((1u << lane) - 1u))] =
+              place<N, VEC>(w * 32 + __ffs(reach[w]) - 1, lane);
+        reach[w] &= reach[w] - 1;
         base += __popc(who);
       }
-    }
-    if (lane >= total) list.value[lane] = sizeof(T) == 2 ? 0u : 0xff800000u;  // larger than none
     __syncwarp();
-    const uint32_t own = list.value[lane];
-    const int e = lane < total ? list.expert[lane] : 0;
+    uint32_t own = sizeof(T) == 2 ? 0u : 0xff800000u;  // larger than none
+    if (lane < total) {
+      expert = list.expert[lane];
+      value = to_f32(row[expert]);
+      own = sizeof(T) == 2 ? bf16_key(value, expert) : __float_as_uint(value);
+    }
+    list.value[lane] = own;
+    __syncwarp();
     int r = 0;
 #pragma unroll 1
     for (int i = 0; i < total; i += 4) {
       const uint4 c = *reinterpret_cast<const uint4*>(&list.value[i]);
-      if constexpr (sizeof(T) == 2) {
+      if constexpr (sizeof(T) == 2)
         r += (c.x > own) + (c.y > own) + (c.z > own) + (c.w > own);
-      } else {
-        const float f = __uint_as_float(own);
-        r += (__uint_as_float(c.x) > f) + (__uint_as_float(c.y) > f) +
-             (__uint_as_float(c.z) > f) + (__uint_as_float(c.w) > f);
-      }
+      else
+        r += (__uint_as_float(c.x) > value) + (__uint_as_float(c.y) > value) +
+             (__uint_as_float(c.z) > value) + (__uint_as_float(c.w) > value);
     }
     if constexpr (sizeof(T) == 4) {
       // equal logits share a rank: then the lower expert goes first
       if (__reduce_add_sync(kAll, lane < total ? r : 0) != total * (total - 1) / 2) {
         for (int i = 0; i < total; ++i)
-          r += __uint_as_float(list.value[i]) == __uint_as_float(own) && list.expert[i] < e;
+          r += __uint_as_float(list.value[i]) == value && list.expert[i] < expert;
       }
     }
-    // to the lanes in their order, so that nothing depends on how they were found
     __syncwarp();
-    if (lane < total && r < K) {
-      list.value[r] = own;
-      list.expert[r] = e;
-    }
-    __syncwarp();
-    if (lane < K) {
-      const uint32_t v = list.value[lane];
-      value = sizeof(T) == 2 ? bf16_key_logit(v) : __uint_as_float(v);
-      expert = list.expert[lane];
-    }
-    __syncwarp();
+    if (lane < total) rank = r;
     return;
   }
   select_in_turn<N, VEC>(l, E, K, lane, [&](int k, float v, int e) {
-    if (lane == k) value = v, expert = e;
+    if (lane == k) value = v, expert = e, rank = k;
   });
 }
 
@@ -459,12 +440,12 @@ k_router(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__
       const float m = warp_max(most);
       const Scores<KIND> score(d.score, m);
 
-      // the chosen ones of this lane: those with rank i * 32 + lane
+      // the chosen ones of this lane, with their ranks (K and more: none)
       float value[KI];
-      int expert[KI];
+      int expert[KI], rank[KI];
       if constexpr (SHORT) {
         select_top<T, N, VEC>(l, row, d.E, d.K, lane, most, m, keep, guess, s_cand[warp],
-                              value[0], expert[0]);
+                              rank[0], value[0], expert[0]);
       } else {
         select_in_turn<N, VEC>(l, d.E, d.K, lane, [&](int k, float v, int e) {
           if (lane == 0)
@@ -473,7 +454,8 @@ k_router(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < KI; ++i) {
-          const unsigned long long c = i * 32 + lane < d.K ? s_list[warp][i * 32 + lane] : 0;
+          rank[i] = i * 32 + lane;
+          const unsigned long long c = rank[i] < d.K ? s_list[warp][rank[i]] : 0;
           value[i] = __uint_as_float((uint32_t)(c >> 32)), expert[i] = (int)(uint32_t)c;
         }
         __syncwarp();
@@ -482,7 +464,7 @@ k_router(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__
       // 1 / sum of the row's scores, where it is needed; a NaN in the row, which is in
       // every softmax score, shows in it
       float inv = 1.f;
-      bool nan = false;
+      bool nan = score.softmax() && m == INFINITY;
       if (LOSS || (score.softmax() && !d.normalise)) {
         float sum = 0.f;
 #pragma unroll
@@ -492,11 +474,10 @@ k_router(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__
         }
         sum = warp_sum(sum);
         inv = sum == 0.f ? 0.f : fast_rcp(sum);
-        nan = sum != sum;
+        nan |= score.softmax() && sum != sum;
       } else if (score.softmax()) {
 #pragma unroll
         for (int j = 0; j < N; ++j) nan |= l[j] != l[j];
-        nan = __any_sync(kAll, nan);
       }
       if constexpr (LOSS) {
         if (live) {
@@ -506,28 +487,31 @@ k_router(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__
         }
       }
 
-      float gate[KI], total = 0.f;
+      // The chosen scores are at most 1 and the largest of them at least 1/2: summed as
+      // integers, in steps of 2^-24, the sum does not depend on which lane holds which.
+      float gate[KI];
+      uint32_t part = 0;
 #pragma unroll
       for (int i = 0; i < KI; ++i) {
-        gate[i] = i * 32 + lane < d.K ? score(value[i]) : 0.f;
-        total += gate[i];
+        gate[i] = rank[i] < d.K ? score(value[i]) : 0.f;
+        nan |= gate[i] != gate[i];
+        part += __float2uint_rn(gate[i] * 16777216.f);
       }
       float factor = score.softmax() ? inv : score.one;
       if (d.normalise) {
-        total = warp_sum(total);
-        factor = total == 0.f ? 0.f : fast_rcp(total);
+        const float total = (float)__reduce_add_sync(kAll, part);
+        factor = total == 0.f ? 0.f : 16777216.f * fast_rcp(total);
       }
       factor *= d.scale;
-      if (score.softmax() && nan) factor = NAN;
+      if (__any_sync(kAll, nan) && (score.softmax() || d.normalise)) factor = NAN;
 #pragma unroll
-      for (int i = 0; i < KI; ++i) {
-        const int k = i * 32 + lane;
-        if (k < d.K) {
-          out.topk_idx[(size_t)t * d.K + k] = expert[i];
-          out.gates[(size_t)t * d.K + k] = live ? gate[i] * factor : 0.f;
+      for (int i = 0; i < KI; ++i)
+        if (rank[i] < d.K) {
+          const size_t at = (size_t)t * d.K + rank[i];
+          out.topk_idx[at] = expert[i];
+          out.gates[at] = live ? gate[i] * factor : 0.f;
           if (LOSS && live) atomicAdd(&s_cnt[expert[i]], 1);
         }
-      }
     }
     if constexpr (LOSS) {
 #pragma unroll
@@ -537,6 +521,7 @@ k_router(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__
       }
       if (lane == 0) atomicAdd(&s_tokens, live_tokens);
       __syncthreads();
+      cudaGridDependencySynchronize();  // the scratch is zero
       join_blocks<W>(d, out, ws, g, s_dyn, s_cnt, s_tokens, s_bad);
       __syncthreads();  // the next segment uses the sums' memory
     }
@@ -702,43 +687,88 @@ RouterScratch router_scratch(const RouterDims& d, void* ws) {
   return r;
 }
 
-// Launch shape of a router kernel: as many blocks as fit the GPU at once, with
-// equally many tokens: whole rounds of the block's warps, and at most 64 tokens a
-// warp, so that a warp's fp32 sums stay short.
-template <typename Kernel>
-static cudaError_t plan_blocks(Kernel* k, int warps, size_t smem, RouterDims& d) {
-  if (smem > (32u << 10)) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+// Blocks of `kernel` that fit the current device at once.  What the runtime answers
+// is kept for each device and size of shared memory (the last one asked for): the
+// three questions take longer than a small launch.
+template <auto kernel, int N>
+static cudaError_t blocks_at_once(size_t smem, int64_t* blocks) {
+  constexpr int W = router_warps<N>();
+  constexpr int kDevices = 64;
+  static std::atomic<uint64_t> known[kDevices];  // shared memory, blocks
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
+  const uint64_t k = known[dev].load(std::memory_order_relaxed);
+  if (k != 0 && (uint32_t)(k >> 32) == (uint32_t)smem) {
+    *blocks = (uint32_t)k;
+    return cudaSuccess;
+  }
+  constexpr int most = 32 * N * 4 * (W + 1);  // of the longest row that this kernel takes
+  if (most > (32 << 10)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
   }
-  int dev = 0, sms = 0, per_sm = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, warps * 32, smem);
+  int sms = 0, per_sm = 0;
+  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, W * 32, smem);
   if (e != cudaSuccess) return e;
-  const int64_t blocks = std::max(1, sms * per_sm);
-  const int64_t each = ((int64_t)d.T + blocks * warps - 1) / (blocks * warps);  // tokens a warp
-  d.per_block = (int)std::min<int64_t>(each, 64) * warps;
+  *blocks = std::max(1, sms * per_sm);
+  known[dev].store((uint64_t)smem << 32 | (uint64_t)*blocks, std::memory_order_relaxed);
+  return cudaSuccess;
+}
+
+// Launch shape: one round of blocks with equally many tokens: whole rounds of the
+// block's warps, and at most 64 tokens a warp, so that a warp's fp32 sums stay short.
+template <auto kernel, int N>
+static cudaError_t plan_blocks(size_t smem, RouterDims& d) {
+  constexpr int W = router_warps<N>();
+  int64_t blocks = 0;
+  const cudaError_t e = blocks_at_once<kernel, N>(smem, &blocks);
+  if (e != cudaSuccess) return e;
+  const int64_t each = ((int64_t)d.T + blocks * W - 1) / (blocks * W);  // tokens a warp
+  d.per_block = (int)std::min<int64_t>(each, 64) * W;
   d.blocks = (int)(((int64_t)d.T + d.per_block - 1) / d.per_block);
   return cudaSuccess;
 }
 
+// Zeroes the scratch; the router's kernel is launched while it runs and waits for it
+// before it joins its sums (programmatic dependent launch).
+__global__ void k_router_zero(uint4* at, size_t n) {
+  cudaTriggerProgrammaticLaunchCompletion();
+  for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (size_t)gridDim.x * blockDim.x)
+    at[i] = make_uint4(0, 0, 0, 0);
+}
+
 template <typename T, int N, bool VEC, bool LOSS, bool SHORT, int KIND>
 static cudaError_t forward(RouterDims d, const void* logits, const uint8_t* mask,
-                           const RouterOut& out, const RouterScratch& ws, cudaStream_t st) {
+                           const RouterOut& out, const RouterScratch& ws, cudaStream_t st,
+                           int* launches) {
   constexpr int W = router_warps<N>();
-  auto* kernel = k_router<T, N, VEC, LOSS, SHORT, KIND>;
+  constexpr auto kernel = k_router<T, N, VEC, LOSS, SHORT, KIND>;
   const size_t smem = LOSS ? (size_t)d.E * 4 * (W + 1) : 0;
-  cudaError_t e = plan_blocks(kernel, W, smem, d);
+  cudaError_t e = plan_blocks<kernel, N>(smem, d);
   if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(d.blocks);
+  cfg.blockDim = dim3(W * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
   if (LOSS && (d.blocks > 1 || d.G > 1)) {
     // (one block joins nothing and only counts the segments)
-    e = cudaMemsetAsync(ws.done, 0, d.blocks > 1 ? ws.zero_bytes : 4, st);
+    const size_t n = (d.blocks > 1 ? ws.zero_bytes : 16) / 16;
+    k_router_zero<<<(unsigned)std::min<size_t>((n + 255) / 256, 1024), 256, 0, st>>>((uint4*)ws.done, n);
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    *launches += 1;
   }
-  kernel<<<d.blocks, W * 32, smem, st>>>(d, (const T*)logits, mask, out, ws);
-  return cudaGetLastError();
+  *launches += 1;
+  return cudaLaunchKernelEx(&cfg, kernel, d, (const T*)logits, mask, out, ws);
 }
 
 // Calls f with the kernel's row shape: values per lane, whether they lie in vectors
@@ -781,10 +811,12 @@ struct ForwardCall {
   const RouterOut& out;
   const RouterScratch& ws;
   cudaStream_t st;
+  int* launches;
   template <typename T, int N, bool VEC, bool SHORT, int KIND>
   cudaError_t operator()() const {
-    return out.loss == nullptr ? forward<T, N, VEC, false, SHORT, KIND>(d, logits, mask, out, ws, st)
-                               : forward<T, N, VEC, true, SHORT, KIND>(d, logits, mask, out, ws, st);
+    return out.loss == nullptr
+               ? forward<T, N, VEC, false, SHORT, KIND>(d, logits, mask, out, ws, st, launches)
+               : forward<T, N, VEC, true, SHORT, KIND>(d, logits, mask, out, ws, st, launches);
   }
 };
 
@@ -802,10 +834,10 @@ struct BackwardCall {
   template <typename T, int N, bool VEC, bool SHORT, int KIND>
   cudaError_t operator()() const {
     constexpr int W = router_warps<N>();
-    auto* kernel = k_router_backward<T, N, VEC, SHORT, KIND>;
+    constexpr auto kernel = k_router_backward<T, N, VEC, SHORT, KIND>;
     const size_t smem = (size_t)W * ((d.E + 3) & ~3) * 4;
     RouterDims r = d;
-    const cudaError_t e = plan_blocks(kernel, W, smem, r);
+    const cudaError_t e = plan_blocks<kernel, N>(smem, r);
     if (e != cudaSuccess) return e;
     kernel<<<r.blocks, W * 32, smem, st>>>(r, (const T*)logits, mask, topk_idx, d_gates, counts,
                                            seg_tokens, d_loss, (T*)d_logits);
@@ -816,10 +848,8 @@ struct BackwardCall {
 cudaError_t launch_router_forward(const RouterDims& d, const void* logits, const uint8_t* mask,
                                   const RouterOut& out, const RouterScratch& ws, cudaStream_t st,
                                   int* launches) {
-  const ForwardCall call{d, logits, mask, out, ws, st};
-  const cudaError_t e = d.bf16 ? by_row<__nv_bfloat16>(d, call) : by_row<float>(d, call);
-  if (e == cudaSuccess) *launches += 1;
-  return e;
+  const ForwardCall call{d, logits, mask, out, ws, st, launches};
+  return d.bf16 ? by_row<__nv_bfloat16>(d, call) : by_row<float>(d, call);
 }
 
 cudaError_t launch_router_backward(const RouterDims& d, const void* logits, const uint8_t* mask,
