@@ -22,7 +22,7 @@ struct RouterScratch {
   int32_t* bad;           // [G] set where a sum met a value that is not finite
   int32_t* counts;        // [G][E]
   unsigned long long* q;  // [G][E] fixed-point probability sums
-  double* seg_loss;       // [G], written before it is read
+  float* seg_loss;        // [G], written before it is read
   size_t zero_bytes, total_bytes;
 };
 RouterScratch router_scratch(const RouterDims& d, void* ws);

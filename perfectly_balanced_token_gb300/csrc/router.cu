@@ -209,10 +209,11 @@ struct __align__(16) Candidates {
 // counting the larger ones; any bound that K to 32 logits reach gives the same
 // result.  The bound of the token before is tried first, moved each time so that
 // about `target` logits reach it (on the model that their number falls off
-// exponentially up to the row's largest, m; on normal logits nine tokens of ten
-// succeed).  Where it fails, the K-th largest of the lanes' maxima is a bound that at
-// least K logits reach.  More than 32 (ties) and a bound of -inf (which the places
-// past the row's end reach too) take the K largest one after the other.
+// exponentially up to the row's largest, m; on normal logits 84 to 90 tokens of a
+// hundred succeed at once).  Where too few reach it, the K-th largest of the lanes'
+// maxima is a bound that at least K do; where too many do, it is raised, then halved
+// in on.  What no bound tells apart (ties) and a bound of -inf (which the places past
+// the row's end reach too) take the K largest one after the other.
 template <typename T, int N, bool VEC>
 __device__ __forceinline__ void select_top(const float (&l)[N], const T* __restrict__ row, int E,
                                            int K, int lane, float most, float m, uint32_t keep,
@@ -223,10 +224,11 @@ __device__ __forceinline__ void select_top(const float (&l)[N], const T* __restr
   value = 0.f, expert = 0;
   const float target = (float)min(K + 8, (K + 30) / 2);
   const float pull = fast_rcp(target * __logf(target));
+  float bound = guess, low = -INFINITY, high = INFINITY;  // too many reach low, too few high
+  bool fresh = !(bound > -INFINITY);
+  if (fresh) bound = __shfl_sync(kAll, warp_sort_down(most, keep), K - 1);
 #pragma unroll 1
-  for (int exact = 0; exact < 2; ++exact) {
-    const float bound = exact ? __shfl_sync(kAll, warp_sort_down(most, keep), K - 1) : guess;
-    if (!(bound > -INFINITY)) continue;
+  for (int tries = 0; tries < 8 && bound > -INFINITY; ++tries) {
     uint32_t reach[NW] = {};
 #pragma unroll
     for (int j = 0; j < N; ++j)
@@ -235,11 +237,27 @@ __device__ __forceinline__ void select_top(const float (&l)[N], const T* __restr
 #pragma unroll
     for (int w = 0; w < NW; ++w) mine += __popc(reach[w]);
     const int total = __reduce_add_sync(kAll, mine);
+    if (total < K) {
+      high = bound;
+      bound = low;
+      if (!(low > -INFINITY)) {
+        bound = __shfl_sync(kAll, warp_sort_down(most, keep), K - 1);
+        fresh = true;
+        continue;
+      }
+    }
+    if (total < K || total > 32) {
+      low = bound;
+      bound = high < INFINITY
+                  ? low + 0.5f * (high - low)
+                  : low + (m - low) * (1.f - __log2f(target) * fast_rcp(__log2f((float)total)));
+      if (!(bound > low && bound < high)) break;
+      continue;
+    }
     // the next token's bound: a number off by a part x of the target asks for a step of
     // x / log(target) of the way to m; a quarter of it, but all after a fresh start
-    guess = fmaf((m - bound) * pull, (exact ? 1.f : 0.25f) * ((float)min(total, 64) - target), bound);
+    guess = fmaf((m - bound) * pull, (fresh ? 1.f : 0.25f) * ((float)total - target), bound);
     if (!(fabsf(guess) < INFINITY)) guess = -INFINITY;
-    if (total < K || total > 32) continue;
 
     int base = 0;
 #pragma unroll
@@ -288,6 +306,7 @@ __device__ __forceinline__ void select_top(const float (&l)[N], const T* __restr
 
 constexpr int kRouterMaxK = 128;
 
+// Warps of a block
 template <int N>
 constexpr int router_warps() {
   return N > 32 ? 4 : 8;
@@ -295,20 +314,25 @@ constexpr int router_warps() {
 // Blocks a multiprocessor has to hold, which caps the registers
 template <int N>
 constexpr int router_blocks() {
-  return N <= 8 ? 5 : N <= 16 ? 4 : N <= 32 ? 2 : 1;
+  return N <= 8 ? 5 : N <= 16 ? 4 : N <= 32 ? 3 : 1;
+}
+// Rows of more than 512 keep the warp's probability sums in shared memory: in
+// registers, next to the row, they cost a third of the warps that fit.
+template <int N>
+constexpr bool sums_in_smem() {
+  return N > 16;
 }
 
-// Sum over the block in a fixed order (every thread gets it).
-__device__ __forceinline__ double block_sum(double v, double* s) {
-  s[threadIdx.x] = v;
+// Sum over the block in a fixed order, to thread 0.  (fp32: each of these sums has
+// terms of one sign, so its error is a few 2^-24 of it; this GPU's 64-bit units would
+// take longer than the whole call on eight tokens.)
+__device__ __forceinline__ float block_sum(float v, float* s) {
+  v = warp_sum(v);
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
   __syncthreads();
-  for (int o = blockDim.x >> 1; o; o >>= 1) {
-    if ((int)threadIdx.x < o) s[threadIdx.x] += s[threadIdx.x + o];
-    __syncthreads();
-  }
-  const double r = s[0];
-  __syncthreads();
-  return r;
+  const int warps = blockDim.x >> 5;
+  v = (int)threadIdx.x < warps ? s[threadIdx.x] : 0.f;
+  return threadIdx.x < 32 ? warp_sum(v) : 0.f;
 }
 
 // A block is done with segment g: its warps' probability sums s_q [W][E], counts s_cnt
@@ -354,30 +378,30 @@ __device__ __forceinline__ void join_blocks(const RouterDims& d, const RouterOut
   }
 
   // the segment's outputs and its part of the loss
-  __shared__ double s_red[W * 32];
-  const double step = ldexp(1.0, -d.shift);
-  double part = 0.0;
+  __shared__ float s_red[32];
+  const float step = ldexpf(1.f, -d.shift);
+  float part = 0.f;
   for (int e = threadIdx.x; e < d.E; e += blockDim.x) {
     const size_t at = (size_t)g * d.E + e;
     int32_t c;
-    double q;
+    float q;
     if (alone) {
-      float v = 0.f;
+      q = 0.f;
 #pragma unroll
-      for (int w = 0; w < W; ++w) v += s_q[(size_t)w * d.E + e];
-      c = s_cnt[e], q = v;
+      for (int w = 0; w < W; ++w) q += s_q[(size_t)w * d.E + e];
+      c = s_cnt[e];
     } else {
       c = __ldcg(&ws.counts[at]);
-      q = s_bad ? (double)NAN : (double)__ldcg(&ws.q[at]) * step;
+      q = s_bad ? NAN : __ull2float_rn(__ldcg(&ws.q[at])) * step;
     }
     out.counts[at] = c;
-    out.prob_sum[at] = (float)q;
-    part += (double)c * q;
+    out.prob_sum[at] = q;
+    part = fmaf((float)c, q, part);
   }
-  const double sum = block_sum(part, s_red);
-  const double n = s_tokens;
-  const double seg = s_tokens ? (double)d.E * sum / ((double)d.K * n * n) : 0.0;
+  part = block_sum(part, s_red);
   if (threadIdx.x == 0) {
+    const float n = (float)s_tokens;
+    const float seg = s_tokens ? part / n * ((float)d.E / ((float)d.K * n)) : 0.f;
     out.seg_tokens[g] = s_tokens;
     if (d.G > 1) {
       ws.seg_loss[g] = seg;
@@ -385,16 +409,16 @@ __device__ __forceinline__ void join_blocks(const RouterDims& d, const RouterOut
       s_last = atomicAdd(ws.done, 1) == d.G - 1;
       __threadfence();
     } else {
-      *out.loss = (float)seg;
+      *out.loss = seg;
     }
   }
   if (d.G == 1) return;
   __syncthreads();
   if (!s_last) return;
-  double mean = 0.0;
+  float mean = 0.f;
   for (int i = threadIdx.x; i < d.G; i += blockDim.x) mean += __ldcg(&ws.seg_loss[i]);
   mean = block_sum(mean, s_red);
-  if (threadIdx.x == 0) *out.loss = (float)(mean / d.G);
+  if (threadIdx.x == 0) *out.loss = mean / (float)d.G;
 }
 
 // A block takes per_block consecutive tokens, a warp every W-th of them; with the
@@ -404,6 +428,7 @@ __global__ void __launch_bounds__(router_warps<N>() * 32, router_blocks<N>())
 k_router(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__ mask,
          RouterOut out, RouterScratch ws) {
   constexpr int W = router_warps<N>();
+  constexpr bool kSmemSums = LOSS && sums_in_smem<N>(), kRegSums = LOSS && !kSmemSums;
   constexpr int KI = SHORT ? 1 : kRouterMaxK / 32;
   __shared__ Candidates s_cand[SHORT ? W : 1];
   __shared__ unsigned long long s_list[SHORT ? 1 : W][kRouterMaxK];
@@ -419,11 +444,17 @@ k_router(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__
   for (int begin = first; begin < last;) {
     const int g = LOSS ? begin / d.segment : 0;
     const int end = LOSS ? (int)min((int64_t)last, (int64_t)(g + 1) * d.segment) : last;
-    float acc[LOSS ? N : 1];
+    float acc[kRegSums ? N : 1];
+    float* sums = s_dyn + (size_t)warp * d.E;  // this warp's, in its lanes' own places
     int live_tokens = 0;
     if constexpr (LOSS) {
 #pragma unroll
-      for (int j = 0; j < N; ++j) acc[j] = 0.f;
+      for (int j = 0; j < (kRegSums ? N : 1); ++j) acc[j] = 0.f;
+      if constexpr (kSmemSums) {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+          if (place<N, VEC>(j, lane) < d.E) sums[place<N, VEC>(j, lane)] = 0.f;
+      }
       for (int e = threadIdx.x; e < d.E; e += blockDim.x) s_cnt[e] = 0;
       if (threadIdx.x == 0) s_tokens = s_bad = 0;
       __syncthreads();
@@ -479,11 +510,23 @@ k_router(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__
 #pragma unroll
         for (int j = 0; j < N; ++j) nan |= l[j] != l[j];
       }
-      if constexpr (LOSS) {
-        if (live) {
+      if (LOSS && live) {
+        ++live_tokens;
+        if constexpr (kRegSums) {
 #pragma unroll
           for (int j = 0; j < N; ++j) acc[j] = fmaf(l[j], inv, acc[j]);
-          ++live_tokens;
+        } else if constexpr (kSmemSums && VEC) {
+#pragma unroll
+          for (int c = 0; c < N / 4; ++c)
+            if (c * 128 + lane * 4 < d.E) {
+              float4& q = *reinterpret_cast<float4*>(sums + c * 128 + lane * 4);
+              q = make_float4(fmaf(l[4 * c], inv, q.x), fmaf(l[4 * c + 1], inv, q.y),
+                              fmaf(l[4 * c + 2], inv, q.z), fmaf(l[4 * c + 3], inv, q.w));
+            }
+        } else if constexpr (kSmemSums) {
+#pragma unroll
+          for (int j = 0; j < N; ++j)
+            if (j * 32 + lane < d.E) sums[j * 32 + lane] = fmaf(l[j], inv, sums[j * 32 + lane]);
         }
       }
 
@@ -514,10 +557,10 @@ k_router(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__
         }
     }
     if constexpr (LOSS) {
+      if constexpr (kRegSums) {
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const int e = place<N, VEC>(j, lane);
-        if (e < d.E) s_dyn[(size_t)warp * d.E + e] = acc[j];
+        for (int j = 0; j < N; ++j)
+          if (place<N, VEC>(j, lane) < d.E) sums[place<N, VEC>(j, lane)] = acc[j];
       }
       if (lane == 0) atomicAdd(&s_tokens, live_tokens);
       __syncthreads();
@@ -682,7 +725,7 @@ RouterScratch router_scratch(const RouterDims& d, void* ws) {
   r.counts = (int32_t*)take(4 * GE);
   r.q = (unsigned long long*)take(8 * GE);
   r.zero_bytes = off;
-  r.seg_loss = (double*)take(8 * G);
+  r.seg_loss = (float*)take(4 * G);
   r.total_bytes = off;
   return r;
 }
@@ -690,9 +733,8 @@ RouterScratch router_scratch(const RouterDims& d, void* ws) {
 // Blocks of `kernel` that fit the current device at once.  What the runtime answers
 // is kept for each device and size of shared memory (the last one asked for): the
 // three questions take longer than a small launch.
-template <auto kernel, int N>
+template <auto kernel, int N, int W>
 static cudaError_t blocks_at_once(size_t smem, int64_t* blocks) {
-  constexpr int W = router_warps<N>();
   constexpr int kDevices = 64;
   static std::atomic<uint64_t> known[kDevices];  // shared memory, blocks
   int dev = 0;
@@ -720,11 +762,10 @@ static cudaError_t blocks_at_once(size_t smem, int64_t* blocks) {
 
 // Launch shape: one round of blocks with equally many tokens: whole rounds of the
 // block's warps, and at most 64 tokens a warp, so that a warp's fp32 sums stay short.
-template <auto kernel, int N>
+template <auto kernel, int N, int W>
 static cudaError_t plan_blocks(size_t smem, RouterDims& d) {
-  constexpr int W = router_warps<N>();
   int64_t blocks = 0;
-  const cudaError_t e = blocks_at_once<kernel, N>(smem, &blocks);
+  const cudaError_t e = blocks_at_once<kernel, N, W>(smem, &blocks);
   if (e != cudaSuccess) return e;
   const int64_t each = ((int64_t)d.T + blocks * W - 1) / (blocks * W);  // tokens a warp
   d.per_block = (int)std::min<int64_t>(each, 64) * W;
@@ -747,7 +788,7 @@ static cudaError_t forward(RouterDims d, const void* logits, const uint8_t* mask
   constexpr int W = router_warps<N>();
   constexpr auto kernel = k_router<T, N, VEC, LOSS, SHORT, KIND>;
   const size_t smem = LOSS ? (size_t)d.E * 4 * (W + 1) : 0;
-  cudaError_t e = plan_blocks<kernel, N>(smem, d);
+  cudaError_t e = plan_blocks<kernel, N, W>(smem, d);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -837,7 +878,7 @@ struct BackwardCall {
     constexpr auto kernel = k_router_backward<T, N, VEC, SHORT, KIND>;
     const size_t smem = (size_t)W * ((d.E + 3) & ~3) * 4;
     RouterDims r = d;
-    const cudaError_t e = plan_blocks<kernel, N>(smem, r);
+    const cudaError_t e = plan_blocks<kernel, N, W>(smem, r);
     if (e != cudaSuccess) return e;
     kernel<<<r.blocks, W * 32, smem, st>>>(r, (const T*)logits, mask, topk_idx, d_gates, counts,
                                            seg_tokens, d_loss, (T*)d_logits);
