@@ -495,21 +495,6 @@ k_ggemm_m256(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
   }
 }
 
-// Tensor maps edited on the device: `map` (128 bytes in global memory, this
-// thread's own copy) gets a new extent for dimension 1, and the edit is made
-// visible to this thread's later TMA copies through the tensor-map proxy.
-__device__ __forceinline__ void tmap_set_dim1(void* map, int extent) {
-  asm volatile(
-      "tensormap.replace.tile.global_dim.global.b1024.b32 [%0], 1, %1;" ::"l"((uint64_t)map),
-      "r"(extent)
-      : "memory");
-}
-__device__ __forceinline__ void tmap_publish(void* map) {
-  asm volatile("fence.proxy.tensormap::generic.release.gpu;" ::: "memory");
-  asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"((uint64_t)map)
-               : "memory");
-}
-
 // Ring depth of the pair kernel (32 KiB stages).  Measured with work items
 // claimed in order, on one box: 6 stages 9.17-9.18 ms at the pages shape and
 // 5.44-5.46 ms at the K3 shape, against 9.23-9.30 and 5.53-5.54 ms with 5.

@@ -139,9 +139,15 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t crank = kPair ? pair_rank() : 0;
   const bool leader = crank == 0;
-  if (plan_failed(p.status)) return;  // uniform over the pair: before any barrier
-  // the other kernel's tiles; where a rank has at most 128 rows this one takes all
-  if (p.counters[MOONEP_CNT_TILE_ROWS] != CG * kMmaM && rank_rows > kMmaM) return;
+  // The pair kernel is launched while the 128-row one runs (only one of them has
+  // tiles), and does not end before it.
+  if constexpr (!kPair) cudaTriggerProgrammaticLaunchCompletion();
+  if (plan_failed(p.status) ||  // uniform over the pair: before any barrier
+      // the other kernel's tiles; where a rank has at most 128 rows this one takes all
+      (p.counters[MOONEP_CNT_TILE_ROWS] != CG * kMmaM && rank_rows > kMmaM)) {
+    if constexpr (kPair) cudaGridDependencySynchronize();
+    return;
+  }
   const int NT = (N + kMxBN - 1) / kMxBN;
   const int total = p.counters[MOONEP_CNT_MTILES] * NT;
   const int KB = (K + kMxK - 1) / kMxK;
@@ -195,7 +201,11 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
   if (warp == 0) {
     // ---------------- TMA producer ----------------
     if (elect_one()) {
-      int stage = 0, issued = 0;
+      // this CTA's ring of copies of A's tensor map (the first map of each slot)
+      uint4* maps = reinterpret_cast<uint4*>(p.tmaps) + (size_t)blockIdx.x * kTmapSlots * 16;
+      for (int i = 0; i < kTmapSlots; ++i)
+        for (int j = 0; j < 8; ++j) maps[i * 16 + j] = reinterpret_cast<const uint4*>(&tm_a)[j];
+      int stage = 0, issued = 0, slot = 0;
       uint32_t phase = 0;
       bool ok = true;
       int next = leader ? atomicAdd(sched, 1) : 0;  // claimed one item ahead
@@ -214,17 +224,29 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         const CUtensorMap* wmap = mt.wsel >= 0 ? &tm_wh : &tm_ws;
         const int wrow = weight_row(mt, t) + (int)crank * Cfg::kBRows;
         const int row0 = mt.row0 + (int)crank * kMmaM;
+        // Rows past the group's end are loaded as zeros, through a copy of the map that
+        // ends there: their products are not stored, and on zeros they take less power
+        const CUtensorMap* amap = &tm_a;
+        if (mt.rows < (int)(crank + 1) * kMmaM) {
+          uint4* m = maps + slot * 16;
+          tmap_set_dim1(m, mt.row0 + mt.rows);
+          tmap_publish(m);
+          amap = reinterpret_cast<const CUtensorMap*>(m);
+          if (++slot == kTmapSlots) slot = 0;
+        }
         for (int kb = 0; kb < KB; ++kb) {
           if (!mbar_wait(empty(stage), phase ^ 1u, abort_flag)) { ok = false; break; }
           const uint32_t sa = smem_u32(smem + stage * Cfg::kStageBytes);
           if (leader) mbar_expect_tx(full(stage), CG * Cfg::kStageBytes);
           if constexpr (kPair) {
             const uint32_t fb = pair_map(full(stage), 0);
-            tma_load_2d_pair(sa, &tm_a, fb, kb * (kMxK / 2), row0);
+            tma_load_2d_pair(sa, amap, fb, kb * (kMxK / 2), row0);
             tma_load_2d_pair(sa + Cfg::kABytes, wmap, fb, kb * (kMxK / 2), wrow);
           } else {
-            tma_load_2d(sa, &tm_a, full(stage), kb * (kMxK / 2), row0);
-            tma_load_2d(sa + Cfg::kABytes, wmap, full(stage), kb * (kMxK / 2), wrow);
+            tma_load_2d(sa, amap, full(stage), kb * (kMxK / 2), row0);
+            for (int h = 0; h < 2; ++h)
+              tma_load_2d(sa + Cfg::kABytes + h * 128 * 128, wmap, full(stage), kb * (kMxK / 2),
+                          wrow + h * 128);
           }
           ++issued;
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
@@ -483,6 +505,7 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     if constexpr (kPair) tmem_dealloc_pair(tmem_base, kMxTmemCols);
     else tmem_dealloc(tmem_base, kMxTmemCols);
   }
+  if constexpr (kPair) cudaGridDependencySynchronize();
 }
 
 // ---------------------------------------------------------------------------
@@ -518,18 +541,19 @@ static bool encode_out(CUtensorMap* m, const void* base, uint64_t N, uint64_t ro
 }
 
 struct MxMaps {
-  CUtensorMap a, a_scales, home_scales, slot_scales, y;
+  CUtensorMap a, a_scales, home, home_scales, slot, slot_scales, y;
 };
 
 template <int CG>
 static cudaError_t launch_mx(const Dims& d, const PlanPtrs& p, const MxMaps& m,
-                             const CUtensorMap& home, const CUtensorMap& slot, uint16_t* y,
-                             cudaStream_t st) {
+                             uint16_t* y, bool after_other, cudaStream_t st) {
   using Cfg = MxCfg<CG>;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = CG;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(Cfg::kThreads);
   cfg.dynamicSmemBytes = Cfg::kSmem;
@@ -550,9 +574,11 @@ static cudaError_t launch_mx(const Dims& d, const PlanPtrs& p, const MxMaps& m,
     grid = CG * std::max(1, n);
   }
   const long long items = (long long)d.max_mtiles * ((d.Hp + kMxBN - 1) / kMxBN);
+  if (grid > kMaxGemmCtas) return cudaErrorInvalidConfiguration;  // tensor-map scratch per CTA
   cfg.gridDim = dim3((unsigned)std::min<long long>(grid, CG * items));
-  return cudaLaunchKernelEx(&cfg, k_mxfp4_gemm<CG>, m.a, home, slot, m.a_scales, m.home_scales,
-                            m.slot_scales, m.y, d.H, d.Hp, d.C, p, y);
+  if (after_other) cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, k_mxfp4_gemm<CG>, m.a, m.home, m.slot, m.a_scales,
+                            m.home_scales, m.slot_scales, m.y, d.H, d.Hp, d.C, p, y);
 }
 
 cudaError_t launch_mxfp4_grouped_gemm(const Dims& d, const PlanPtrs& p, const uint8_t* a,
@@ -567,31 +593,27 @@ cudaError_t launch_mxfp4_grouped_gemm(const Dims& d, const PlanPtrs& p, const ui
   MxMaps m;
   if (!encode_bytes(&m.a, a, bytes, rows, 128, kMmaM) ||
       !encode_bytes(&m.a_scales, a_scales, pitch, rows, 16, kMmaM) ||
+      !encode_bytes(&m.home, home, bytes, home_rows, 128, 128) ||
       !encode_bytes(&m.home_scales, home_scales, pitch, home_rows, 16, kMxBN) ||
       !encode_out(&m.y, y, (uint64_t)d.Hp, rows))
     return cudaErrorInvalidValue;
+  m.slot = m.home;
   m.slot_scales = m.home_scales;
-  if (slots && !encode_bytes(&m.slot_scales, slot_scales, pitch, slot_rows, 16, kMxBN))
+  if (slots && (!encode_bytes(&m.slot, slot, bytes, slot_rows, 128, 128) ||
+                !encode_bytes(&m.slot_scales, slot_scales, pitch, slot_rows, 16, kMxBN)))
     return cudaErrorInvalidValue;
-  CUtensorMap wh, ws;
-  auto weights = [&](uint32_t box_rows) {
-    if (!encode_bytes(&wh, home, bytes, home_rows, 128, box_rows)) return false;
-    ws = wh;
-    return !slots || encode_bytes(&ws, slot, bytes, slot_rows, 128, box_rows);
-  };
   // The plan's tile height is on the device: the variant it did not choose returns at
   // once (as in the bf16 product).  Where no rank has more than 128 rows, no tile has,
   // whatever its height, and the 128-row kernel takes both.
   const bool pair = d.tile_m != kMmaM && d.C > kMmaM;
-  if (d.tile_m != 2 * kMmaM || !pair) {
-    if (!weights(MxCfg<1>::kBRows)) return cudaErrorInvalidValue;
-    const cudaError_t e = launch_mx<1>(d, p, m, wh, ws, (uint16_t*)y, st);
+  const bool solo = d.tile_m != 2 * kMmaM || !pair;
+  if (solo) {
+    const cudaError_t e = launch_mx<1>(d, p, m, (uint16_t*)y, false, st);
     if (e != cudaSuccess) return e;
     *launches += 1;
   }
   if (pair) {
-    if (!weights(MxCfg<2>::kBRows)) return cudaErrorInvalidValue;
-    const cudaError_t e = launch_mx<2>(d, p, m, wh, ws, (uint16_t*)y, st);
+    const cudaError_t e = launch_mx<2>(d, p, m, (uint16_t*)y, solo, st);
     if (e != cudaSuccess) return e;
     *launches += 1;
   }

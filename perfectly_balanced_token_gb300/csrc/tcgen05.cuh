@@ -264,6 +264,22 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
   }
 }
 
+// ---- tensor maps edited on the device ----------------------------------------
+// Tensor maps edited on the device: `map` (128 bytes in global memory, this
+// thread's own copy) gets a new extent for dimension 1, and the edit is made
+// visible to this thread's later TMA copies through the tensor-map proxy.
+__device__ __forceinline__ void tmap_set_dim1(void* map, int extent) {
+  asm volatile(
+      "tensormap.replace.tile.global_dim.global.b1024.b32 [%0], 1, %1;" ::"l"((uint64_t)map),
+      "r"(extent)
+      : "memory");
+}
+__device__ __forceinline__ void tmap_publish(void* map) {
+  asm volatile("fence.proxy.tensormap::generic.release.gpu;" ::: "memory");
+  asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"((uint64_t)map)
+               : "memory");
+}
+
 // ---- work items of a CTA pair, claimed in order -------------------------------
 // The pair's leader claims work items one at a time from a counter in global
 // memory, one item ahead of the one it hands out (so the atomic's round trip
