@@ -28,9 +28,9 @@ constexpr int kCopyChunk = kCopyThreads * kCopyVec * 16;      // 16 KiB per work
 // CTAs per SM keep the last round of items short (measured: 2-3 % faster than
 // 32 KiB items loaded and stored in turn).
 __global__ void __launch_bounds__(kCopyThreads)
-k_prefetch(PlanPtrs p, size_t vec_per_w, const uint4* __restrict__ w_home,
-           uint4* __restrict__ w_slot) {
+k_prefetch(Dims d, PlanPtrs p, const uint4* __restrict__ w_home, uint4* __restrict__ w_slot) {
   if (plan_failed(p.status)) return;
+  const size_t vec_per_w = (size_t)d.H * d.Hp * 2 / 16;
   const int nch = (int)((vec_per_w * 16 + kCopyChunk - 1) / kCopyChunk);
   const int items = p.counters[MOONEP_CNT_OCCUPIED] * nch;
   uint4 v[kCopyVec], nv[kCopyVec];
@@ -452,19 +452,13 @@ static int sm_count() {
   return n;
 }
 
-cudaError_t launch_prefetch_rows(const Dims& d, const PlanPtrs& p, size_t bytes_per_expert,
-                                 const void* home, void* slot, cudaStream_t st, int* launches) {
-  if (d.B == 0) return cudaSuccess;
-  const int grid = sm_count() * 16;
-  k_prefetch<<<grid, kCopyThreads, 0, st>>>(p, bytes_per_expert / 16, (const uint4*)home,
-                                            (uint4*)slot);
-  *launches += 1;
-  return cudaGetLastError();
-}
-
 cudaError_t launch_prefetch(const Dims& d, const PlanPtrs& p, const void* w_home, void* w_slot,
                             cudaStream_t st, int* launches) {
-  return launch_prefetch_rows(d, p, (size_t)d.H * d.Hp * 2, w_home, w_slot, st, launches);
+  if (d.B == 0) return cudaSuccess;
+  const int grid = sm_count() * 16;
+  k_prefetch<<<grid, kCopyThreads, 0, st>>>(d, p, (const uint4*)w_home, (uint4*)w_slot);
+  *launches += 1;
+  return cudaGetLastError();
 }
 
 cudaError_t launch_dispatch(const Dims& d, const PlanPtrs& p, const void* x, void* recv,

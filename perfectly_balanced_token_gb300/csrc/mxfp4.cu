@@ -97,15 +97,33 @@ __device__ __forceinline__ UnitCodes encode_unit(const uint4 (&x)[2], int lane, 
 constexpr int kQuantThreads = 128;
 constexpr int kQuantWarps = kQuantThreads / 32;
 
+// The units of all rows, warp by warp over the whole grid: neighbouring warps take
+// neighbouring units, and all take equally many (a block per row would leave two of
+// its four warps idle for a seventh of the time at 14 units).  The row advances
+// without a division.
+struct UnitWalk {
+  int64_t row, rows_ahead;
+  int unit, units_ahead, per_row;
+  __device__ __forceinline__ UnitWalk(int per_row_) : per_row(per_row_) {
+    const int64_t first = (int64_t)blockIdx.x * kQuantWarps + (threadIdx.x >> 5);
+    const int64_t stride = (int64_t)gridDim.x * kQuantWarps;
+    row = first / per_row, unit = (int)(first % per_row);
+    rows_ahead = stride / per_row, units_ahead = (int)(stride % per_row);
+  }
+  __device__ __forceinline__ void advance() {
+    row += rows_ahead, unit += units_ahead;
+    if (unit >= per_row) unit -= per_row, ++row;
+  }
+};
+
 __global__ void __launch_bounds__(kQuantThreads)
-k_mxfp4_quantize(int64_t units, int per_row, int cols, const uint16_t* __restrict__ src,
+k_mxfp4_quantize(int64_t rows, int per_row, int cols, const uint16_t* __restrict__ src,
                  uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
   __shared__ __align__(16) uint8_t s_bytes[kQuantWarps][16];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int64_t i = (int64_t)blockIdx.x * kQuantWarps + warp; i < units;
-       i += (int64_t)gridDim.x * kQuantWarps) {
-    const int64_t row = i / per_row;
-    const int unit = (int)(i - row * per_row);
+  for (UnitWalk w(per_row); w.row < rows; w.advance()) {
+    const int64_t row = w.row;
+    const int unit = w.unit;
     uint4 x[2];
     load_unit(src + row * cols, cols, unit, lane, x);
     const UnitCodes r = encode_unit(x, lane, s_bytes[warp]);
@@ -115,25 +133,24 @@ k_mxfp4_quantize(int64_t units, int per_row, int cols, const uint16_t* __restric
       const int at = unit * kUnit + h * 256 + lane * 8;
       if (at < cols) *reinterpret_cast<uint32_t*>(out + at / 2) = r.code[h];
     }
-    if (lane == 0) *reinterpret_cast<uint4*>(scales + i * 16) = r.scales;
+    if (lane == 0) *reinterpret_cast<uint4*>(scales + (row * per_row + unit) * 16) = r.scales;
   }
 }
 
 __global__ void __launch_bounds__(kQuantThreads)
-k_mxfp4_dequantize(int64_t units, int per_row, int cols, const uint8_t* __restrict__ codes,
+k_mxfp4_dequantize(int64_t rows, int per_row, int cols, const uint8_t* __restrict__ codes,
                    const uint8_t* __restrict__ scales, uint16_t* __restrict__ dst) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int64_t i = (int64_t)blockIdx.x * kQuantWarps + warp; i < units;
-       i += (int64_t)gridDim.x * kQuantWarps) {
-    const int64_t row = i / per_row;
-    const int unit = (int)(i - row * per_row);
+  const int lane = threadIdx.x & 31;
+  for (UnitWalk w(per_row); w.row < rows; w.advance()) {
+    const int64_t row = w.row;
+    const int unit = w.unit;
     const uint8_t* in = codes + row * (cols / 2);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int at = unit * kUnit + h * 256 + lane * 8;
       if (at >= cols) continue;
       const uint32_t c = __ldcs(reinterpret_cast<const uint32_t*>(in + at / 2));
-      const float f = scale_value(__ldg(scales + i * 16 + h * 8 + (lane >> 2)));
+      const float f = scale_value(__ldg(scales + (row * per_row + unit) * 16 + h * 8 + (lane >> 2)));
       uint32_t half2[4];
       asm("{\n\t.reg .b8 a, b, c, d;\n\t"
           "mov.b32 {a, b, c, d}, %4;\n\t"
@@ -211,54 +228,91 @@ k_mxfp4_quantize_weights(int h_tiles, int H, int Hp, int pitch, const uint16_t* 
         *reinterpret_cast<const uint2*>(s_scale[threadIdx.x]);
 }
 
-// Dispatch: a block of threads per token, a warp per unit of its row; the unit
-// is quantised once and stored to the token's K rows.
+// Dispatch: a warp quantises a unit of a token's row once and stores it to the
+// token's K rows.
 __global__ void __launch_bounds__(kQuantThreads)
 k_mxfp4_dispatch(Dims d, PlanPtrs p, int pitch, const uint16_t* __restrict__ x,
                  uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
   if (plan_failed(p.status)) return;
   __shared__ __align__(16) uint8_t s_bytes[kQuantWarps][16];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int ntok = d.R * d.S, units = pitch / 16;
-  for (int t = blockIdx.x; t < ntok; t += gridDim.x) {
-    const int32_t* dst = p.dst + (size_t)t * d.K;
-    for (int u = warp; u < units; u += kQuantWarps) {
-      uint4 v[2];
-      load_unit(x + (size_t)t * d.H, d.H, u, lane, v);
-      const UnitCodes r = encode_unit(v, lane, s_bytes[warp]);
-      for (int k = 0; k < d.K; ++k) {
-        uint8_t* out = codes + (size_t)__ldg(dst + k) * (d.H / 2);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int at = u * kUnit + h * 256 + lane * 8;
-          if (at < d.H) *reinterpret_cast<uint32_t*>(out + at / 2) = r.code[h];
-        }
-      }
-      for (int k = lane; k < d.K; k += 32)
-        *reinterpret_cast<uint4*>(scales + (size_t)__ldg(dst + k) * pitch + u * 16) = r.scales;
+  const int ntok = d.R * d.S;
+  for (UnitWalk w(pitch / 16); w.row < ntok; w.advance()) {
+    const int32_t* dst = p.dst + w.row * d.K;
+    uint4 v[2];
+    load_unit(x + w.row * d.H, d.H, w.unit, lane, v);
+    const UnitCodes r = encode_unit(v, lane, s_bytes[warp]);
+    const int at = w.unit * kUnit + lane * 8;
+    for (int k = 0; k < d.K; ++k) {
+      uint8_t* out = codes + (size_t)__ldg(dst + k) * (d.H / 2) + at / 2;
+      if (at < d.H) *reinterpret_cast<uint32_t*>(out) = r.code[0];
+      if (at + 256 < d.H) *reinterpret_cast<uint32_t*>(out + 128) = r.code[1];
     }
+    for (int k = lane; k < d.K; k += 32)
+      *reinterpret_cast<uint4*>(scales + (size_t)__ldg(dst + k) * pitch + w.unit * 16) = r.scales;
+  }
+}
+
+// Prefetch: the occupied slots' codes and scales in one launch, 16 KiB at a time,
+// the next piece loaded before this one is stored.
+constexpr int kPieceVec = 4;
+constexpr int kPieceThreads = 256;
+constexpr int kPiece = kPieceThreads * kPieceVec;  // 16-byte vectors
+
+__global__ void __launch_bounds__(kPieceThreads)
+k_mxfp4_prefetch(PlanPtrs p, int code_vecs, int scale_vecs, const uint4* __restrict__ home_codes,
+                 const uint4* __restrict__ home_scales, uint4* __restrict__ slot_codes,
+                 uint4* __restrict__ slot_scales) {
+  if (plan_failed(p.status)) return;
+  const int code_pieces = (code_vecs + kPiece - 1) / kPiece;
+  const int pieces = code_pieces + (scale_vecs + kPiece - 1) / kPiece;
+  const int64_t items = (int64_t)p.counters[MOONEP_CNT_OCCUPIED] * pieces;
+  uint4 v[kPieceVec], next[kPieceVec];
+  auto visit = [&](int64_t it, auto&& f) {  // f(home, slot, vectors) of each vector held here
+    const int s = p.occupied[it / pieces], piece = (int)(it % pieces);
+    const int e = p.slot_expert[s];
+    const bool code = piece < code_pieces;
+    const int n = code ? code_vecs : scale_vecs;
+    const uint4* home = (code ? home_codes : home_scales) + (size_t)e * n;
+    uint4* slot = (code ? slot_codes : slot_scales) + (size_t)s * n;
+    const int at = (code ? piece : piece - code_pieces) * kPiece + threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < kPieceVec; ++i)
+      if (at + i * kPieceThreads < n) f(i, home + at + i * kPieceThreads, slot + at + i * kPieceThreads);
+  };
+  int64_t it = blockIdx.x;
+  if (it < items) visit(it, [&](int i, const uint4* home, uint4*) { v[i] = __ldcs(home); });
+  for (; it < items; it += gridDim.x) {
+    if (it + gridDim.x < items)
+      visit(it + gridDim.x, [&](int i, const uint4* home, uint4*) { next[i] = __ldcs(home); });
+    visit(it, [&](int i, const uint4*, uint4* slot) { __stcs(slot, v[i]); });
+#pragma unroll
+    for (int i = 0; i < kPieceVec; ++i) v[i] = next[i];
   }
 }
 
 // ---------------------------------------------------------------------------
 // launchers
 // ---------------------------------------------------------------------------
-static int blocks_for(int64_t units) {
+static int multiprocessors() {
   int dev = 0, sms = 0;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms > 0 ? sms : 1;
+}
+
+static int blocks_for(int64_t units) {
   const int64_t want = (units + kQuantWarps - 1) / kQuantWarps;
-  const int64_t most = (int64_t)(sms > 0 ? sms : 1) * 16;
+  const int64_t most = (int64_t)multiprocessors() * 16;
   return (int)(want < most ? want : most);
 }
 
 cudaError_t launch_mxfp4_quantize(int64_t rows, int cols, const void* src, uint8_t* codes,
                                   uint8_t* scales, cudaStream_t st, int* launches) {
   const int per_row = MOONEP_MXFP4_SCALE_PITCH(cols) / 16;
-  const int64_t units = rows * per_row;
-  if (units == 0) return cudaSuccess;
-  k_mxfp4_quantize<<<blocks_for(units), kQuantThreads, 0, st>>>(
-      units, per_row, cols, (const uint16_t*)src, codes, scales);
+  if (rows == 0) return cudaSuccess;
+  k_mxfp4_quantize<<<blocks_for(rows * per_row), kQuantThreads, 0, st>>>(
+      rows, per_row, cols, (const uint16_t*)src, codes, scales);
   *launches += 1;
   return cudaGetLastError();
 }
@@ -267,10 +321,9 @@ cudaError_t launch_mxfp4_dequantize(int64_t rows, int cols, const uint8_t* codes
                                     const uint8_t* scales, void* dst, cudaStream_t st,
                                     int* launches) {
   const int per_row = MOONEP_MXFP4_SCALE_PITCH(cols) / 16;
-  const int64_t units = rows * per_row;
-  if (units == 0) return cudaSuccess;
-  k_mxfp4_dequantize<<<blocks_for(units), kQuantThreads, 0, st>>>(units, per_row, cols, codes,
-                                                                 scales, (uint16_t*)dst);
+  if (rows == 0) return cudaSuccess;
+  k_mxfp4_dequantize<<<blocks_for(rows * per_row), kQuantThreads, 0, st>>>(
+      rows, per_row, cols, codes, scales, (uint16_t*)dst);
   *launches += 1;
   return cudaGetLastError();
 }
@@ -289,9 +342,25 @@ cudaError_t launch_mxfp4_quantize_weights(int n, int H, int Hp, const void* w, u
 
 cudaError_t launch_mxfp4_dispatch(const Dims& d, const PlanPtrs& p, const void* x, uint8_t* codes,
                                   uint8_t* scales, cudaStream_t st, int* launches) {
-  const int grid = blocks_for((int64_t)d.R * d.S * kQuantWarps);
-  k_mxfp4_dispatch<<<grid, kQuantThreads, 0, st>>>(d, p, MOONEP_MXFP4_SCALE_PITCH(d.H),
-                                                   (const uint16_t*)x, codes, scales);
+  const int pitch = MOONEP_MXFP4_SCALE_PITCH(d.H);
+  const int grid = blocks_for((int64_t)d.R * d.S * (pitch / 16));
+  k_mxfp4_dispatch<<<grid, kQuantThreads, 0, st>>>(d, p, pitch, (const uint16_t*)x, codes, scales);
+  *launches += 1;
+  return cudaGetLastError();
+}
+
+cudaError_t launch_mxfp4_prefetch(const Dims& d, const PlanPtrs& p, const uint8_t* home_codes,
+                                  const uint8_t* home_scales, uint8_t* slot_codes,
+                                  uint8_t* slot_scales, cudaStream_t st, int* launches) {
+  if (d.B == 0) return cudaSuccess;
+  const int64_t code = (int64_t)d.Hp * (d.H / 2) / 16;
+  const int64_t scale = (int64_t)d.Hp * MOONEP_MXFP4_SCALE_PITCH(d.H) / 16;
+  if (code >= (int64_t(1) << 30)) return cudaErrorInvalidValue;
+  // eight blocks a multiprocessor: with sixteen a prefetch of two slots takes longer
+  // to start its blocks than to copy
+  k_mxfp4_prefetch<<<multiprocessors() * 8, kPieceThreads, 0, st>>>(
+      p, (int)code, (int)scale, (const uint4*)home_codes, (const uint4*)home_scales,
+      (uint4*)slot_codes, (uint4*)slot_scales);
   *launches += 1;
   return cudaGetLastError();
 }

@@ -164,11 +164,9 @@ int moonep_mxfp4_prefetch_weights(const moonep_dims* dims, void* plan_ws, const 
     MOONEP_NEED(slot_scales);
   }
   int n = 0;
-  cudaError_t e = launch_prefetch_rows(d, P, (size_t)d.Hp * (d.H / 2), home_codes, slot_codes,
-                                       (cudaStream_t)stream, &n);
-  if (e == cudaSuccess)
-    e = launch_prefetch_rows(d, P, (size_t)d.Hp * MOONEP_MXFP4_SCALE_PITCH(d.H), home_scales,
-                             slot_scales, (cudaStream_t)stream, &n);
+  if ((int64_t)d.Hp * (d.H / 2) / 16 >= (int64_t(1) << 30)) return MOONEP_ERR_SHAPE;
+  const cudaError_t e = launch_mxfp4_prefetch(d, P, home_codes, home_scales, slot_codes,
+                                              slot_scales, (cudaStream_t)stream, &n);
   return finish(e, n);
 }
 

@@ -51,8 +51,9 @@ cudaError_t launch_mxfp4_quantize_weights(int n, int H, int Hp, const void* w, u
                                           uint8_t* scales, cudaStream_t, int*);
 cudaError_t launch_mxfp4_dispatch(const Dims&, const PlanPtrs&, const void* x, uint8_t* codes,
                                   uint8_t* scales, cudaStream_t, int*);
-cudaError_t launch_prefetch_rows(const Dims&, const PlanPtrs&, size_t bytes_per_expert,
-                                 const void* home, void* slot, cudaStream_t, int*);
+cudaError_t launch_mxfp4_prefetch(const Dims&, const PlanPtrs&, const uint8_t* home_codes,
+                                  const uint8_t* home_scales, uint8_t* slot_codes,
+                                  uint8_t* slot_scales, cudaStream_t, int*);
 cudaError_t launch_mxfp4_grouped_gemm(const Dims&, const PlanPtrs&, const uint8_t* a,
                                       const uint8_t* a_scales, const uint8_t* home,
                                       const uint8_t* home_scales, const uint8_t* slot,
