@@ -71,55 +71,55 @@ def router_dims(T, E, K, segment=0, score="softmax", normalise=True, scale=1.0,
                               scale)
 
 
-_workspace_bytes: dict = {}  # of dims already asked for, by their fields
+_sizes: dict = {}  # of router dims already seen, by their fields
 
 
-def moonep_router_workspace_bytes(rd: moonep_router_dims) -> int:
+def _router_sizes(rd):
+    """(workspace bytes, T*E, T*K, G*E, G, logits dtype), kept: the fields of a ctypes structure
+    take longer to read than a small call may last."""
     key = bytes(rd)
-    size = _workspace_bytes.get(key)
-    if size is None:
+    got = _sizes.get(key)
+    if got is None:
         n = ctypes.c_size_t(0)
         _check(library().moonep_router_workspace_bytes(ctypes.byref(rd), ctypes.byref(n)),
                "moonep_router_workspace_bytes")
-        size = _workspace_bytes[key] = n.value
-    return size
+        got = _sizes[key] = (n.value, rd.T * rd.E, rd.T * rd.K, rd.G * rd.E, rd.G, rd.torch_dtype)
+    return got
+
+
+def moonep_router_workspace_bytes(rd: moonep_router_dims) -> int:
+    return _router_sizes(rd)[0]
 
 
 def moonep_router_forward(rd, logits, topk_idx, gates, token_mask=None, ws=None, counts=None,
                           prob_sum=None, seg_tokens=None, loss=None, stream=None):
     """The balance outputs (ws, counts, prob_sum, seg_tokens, loss) are all given or all None."""
-    lib = library()
-    TK, GE = rd.T * rd.K, rd.G * rd.E
-    if ws is not None:
-        need = moonep_router_workspace_bytes(rd)
-        if isinstance(ws, torch.Tensor) and ws.numel() < need:
-            raise ValueError(f"ws has {ws.numel()} bytes, expected at least {need}")
-    _check(lib.moonep_router_forward(
-        ctypes.byref(rd), _ptr(logits, rd.torch_dtype, rd.T * rd.E, "logits"),
-        _ptr(token_mask, torch.uint8, rd.T, "token_mask", allow_none=True),
+    need, TE, TK, GE, G, dtype = _router_sizes(rd)
+    if ws is not None and isinstance(ws, torch.Tensor) and ws.numel() < need:
+        raise ValueError(f"ws has {ws.numel()} bytes, expected at least {need}")
+    _check(library().moonep_router_forward(
+        ctypes.byref(rd), _ptr(logits, dtype, TE, "logits"),
+        _ptr(token_mask, torch.uint8, rd.T, "token_mask", True) if token_mask is not None else None,
         _ptr(topk_idx, torch.int32, TK, "topk_idx"), _ptr(gates, torch.float32, TK, "gates"),
-        _ptr(ws, torch.uint8, None, "ws", allow_none=True),
-        _ptr(counts, torch.int32, GE, "counts", allow_none=True),
-        _ptr(prob_sum, torch.float32, GE, "prob_sum", allow_none=True),
-        _ptr(seg_tokens, torch.int32, rd.G, "seg_tokens", allow_none=True),
-        _ptr(loss, torch.float32, 1, "loss", allow_none=True), _stream(stream)),
-        "moonep_router_forward")
+        _ptr(ws, torch.uint8, None, "ws", True), _ptr(counts, torch.int32, GE, "counts", True),
+        _ptr(prob_sum, torch.float32, GE, "prob_sum", True),
+        _ptr(seg_tokens, torch.int32, G, "seg_tokens", True),
+        _ptr(loss, torch.float32, 1, "loss", True), _stream(stream)), "moonep_router_forward")
 
 
 def moonep_router_backward(rd, logits, topk_idx, d_logits, d_gates=None, token_mask=None,
                            counts=None, seg_tokens=None, d_loss=None, stream=None):
     """counts, seg_tokens and d_loss are all given or all None; d_gates may be None with them."""
-    TK, GE = rd.T * rd.K, rd.G * rd.E
+    _, TE, TK, GE, G, dtype = _router_sizes(rd)
     _check(library().moonep_router_backward(
-        ctypes.byref(rd), _ptr(logits, rd.torch_dtype, rd.T * rd.E, "logits"),
-        _ptr(token_mask, torch.uint8, rd.T, "token_mask", allow_none=True),
+        ctypes.byref(rd), _ptr(logits, dtype, TE, "logits"),
+        _ptr(token_mask, torch.uint8, rd.T, "token_mask", True) if token_mask is not None else None,
         _ptr(topk_idx, torch.int32, TK, "topk_idx"),
-        _ptr(d_gates, torch.float32, TK, "d_gates", allow_none=True),
-        _ptr(counts, torch.int32, GE, "counts", allow_none=True),
-        _ptr(seg_tokens, torch.int32, rd.G, "seg_tokens", allow_none=True),
-        _ptr(d_loss, torch.float32, 1, "d_loss", allow_none=True),
-        _ptr(d_logits, rd.torch_dtype, rd.T * rd.E, "d_logits"), _stream(stream)),
-        "moonep_router_backward")
+        _ptr(d_gates, torch.float32, TK, "d_gates", True),
+        _ptr(counts, torch.int32, GE, "counts", True),
+        _ptr(seg_tokens, torch.int32, G, "seg_tokens", True),
+        _ptr(d_loss, torch.float32, 1, "d_loss", True),
+        _ptr(d_logits, dtype, TE, "d_logits"), _stream(stream)), "moonep_router_backward")
 
 
 def mxfp4_scale_pitch(cols: int) -> int:
