@@ -65,8 +65,8 @@ int moonep_router_workspace_bytes(const moonep_router_dims* dims, size_t* bytes)
  * fp32 [T][K] (written).  The balance outputs are all given or all NULL: ws
  * (overwritten), counts int32 [G][E], prob_sum fp32 [G][E], seg_tokens int32
  * [G] (n_g), loss fp32 [1] (4-byte aligned).
- * MOONEP_ERR_SHAPE: K > E, K > 128, E > 4096, T*K or G*E reaches 2^31, or
- * segment > T.  Two calls that overlap on the GPU need two workspaces. */
+ * MOONEP_ERR_SHAPE: K > E, K > 128, E > 4096, T*K reaches 2^31 - 4096, G*E
+ * reaches 2^31, or segment > T.  Two calls that overlap on the GPU need two workspaces. */
 int moonep_router_forward(const moonep_router_dims* dims, const void* logits,
                           const uint8_t* token_mask, int32_t* topk_idx, float* gates, void* ws,
                           int32_t* counts, float* prob_sum, int32_t* seg_tokens, float* loss,

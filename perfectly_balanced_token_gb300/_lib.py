@@ -167,11 +167,11 @@ _workspace_bytes: dict = {}  # of dims already asked for, by their fields
 
 
 def moonep_plan_workspace_bytes(d: moonep_dims) -> int:
-    key = bytes(d)
+    lib, key = library(), bytes(d)
     size = _workspace_bytes.get(key)
     if size is None:
         n = ctypes.c_size_t(0)
-        _check(library().moonep_plan_workspace_bytes(ctypes.byref(d), ctypes.byref(n)),
+        _check(lib.moonep_plan_workspace_bytes(ctypes.byref(d), ctypes.byref(n)),
                "moonep_plan_workspace_bytes")
         size = _workspace_bytes[key] = n.value
     return size

@@ -77,11 +77,11 @@ _sizes: dict = {}  # of router dims already seen, by their fields
 def _router_sizes(rd):
     """(workspace bytes, T*E, T*K, G*E, G, logits dtype), kept: the fields of a ctypes structure
     take longer to read than a small call may last."""
-    key = bytes(rd)
+    lib, key = library(), bytes(rd)
     got = _sizes.get(key)
     if got is None:
         n = ctypes.c_size_t(0)
-        _check(library().moonep_router_workspace_bytes(ctypes.byref(rd), ctypes.byref(n)),
+        _check(lib.moonep_router_workspace_bytes(ctypes.byref(rd), ctypes.byref(n)),
                "moonep_router_workspace_bytes")
         got = _sizes[key] = (n.value, rd.T * rd.E, rd.T * rd.K, rd.G * rd.E, rd.G, rd.torch_dtype)
     return got

@@ -16,7 +16,8 @@ static int check_router(const moonep_router_dims* in, RouterDims* d) {
   if (x.dtype != 0 && x.dtype != 1) return MOONEP_ERR_ARG;
   if (!std::isfinite(x.scale)) return MOONEP_ERR_ARG;
   if (x.K > x.E || x.K > 128 || x.E > kMaxExperts || x.segment > x.T) return MOONEP_ERR_SHAPE;
-  if ((int64_t)x.T * x.K >= (int64_t(1) << 31)) return MOONEP_ERR_SHAPE;
+  // (token counters run a block past the last token)
+  if ((int64_t)x.T * x.K >= (int64_t(1) << 31) - 4096) return MOONEP_ERR_SHAPE;
   d->T = x.T;
   d->E = x.E;
   d->K = x.K;

@@ -69,6 +69,55 @@ def test_every_code_and_scale_back():
     assert np.array_equal(out.double().cpu().numpy(), want, equal_nan=True)
 
 
+def test_offsets_past_32_bits():
+    rows, cols = 640_000, 7168  # 4.6e9 values
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    tail = rows_with_everything(4, cols, 1)
+    x[-4:] = tail.cuda()
+    codes = torch.full((rows, cols // 2), 0xEE, dtype=torch.uint8, device="cuda")
+    scales = torch.full((rows, mx.mxfp4_scale_pitch(cols)), 0xEE, dtype=torch.uint8, device="cuda")
+    mx.moonep_mxfp4_quantize(x, codes, scales)
+    want_c, want_s = ops.mxfp4_quantize(tail.double().numpy())
+    assert np.array_equal(codes[-4:].cpu().numpy(), want_c)
+    assert np.array_equal(scales[-4:].cpu().numpy(), want_s)
+    assert not codes[:-4].any() and not scales[:-4].any()
+    x.fill_(7.0)
+    mx.moonep_mxfp4_dequantize(codes, scales, x)
+    assert np.array_equal(x[-4:].double().cpu().numpy(), ops.mxfp4_values(want_c, want_s),
+                          equal_nan=True)
+    assert not x[:-4].any()
+
+
+def test_product_with_offsets_past_32_bits():
+    # 1.3 million rows of 3584 bytes of codes; the last rows' outputs against the definition
+    w = syn.Workload("long", R=1, E=2, B=0, K=1, S=1_300_000, H=7168, Hp=64, mode=1)
+    d = mx.dims(w.R, w.E, w.B, w.K, w.S, w.H, w.Hp, w.mode)
+    ids = torch.ones(w.N, dtype=torch.int32, device="cuda")
+    ids[: w.N // 2] = 0
+    ws = mx.PlanWorkspace(d)
+    mx.moonep_plan(d, ids, ws.buf)
+    x = torch.zeros(w.S, w.H, dtype=torch.bfloat16, device="cuda")
+    tail = syn.normal_bf16((6, w.H), 1.0, 5)
+    x[-6:] = tail.cuda()
+    wt = syn.normal_bf16((2, w.H, w.Hp), 0.05, 6)
+    u8 = dict(dtype=torch.uint8, device="cuda")
+    pitch = mx.mxfp4_scale_pitch(w.H)
+    hq, hs = torch.empty(2, w.Hp, w.H // 2, **u8), torch.empty(2, w.Hp, pitch, **u8)
+    mx.moonep_mxfp4_quantize_weights(wt.cuda(), hq, hs)
+    rq, rs = torch.full((w.N, w.H // 2), 0xEE, **u8), torch.full((w.N, pitch), 0xEE, **u8)
+    y = torch.full((w.N, w.Hp), 7.0, dtype=torch.bfloat16, device="cuda")
+    mx.moonep_mxfp4_dispatch(d, ws.buf, x, rq, rs)
+    mx.moonep_mxfp4_grouped_gemm(d, ws.buf, rq, rs, hq, hs, None, None, y)
+    torch.cuda.synchronize()
+    assert mx.moonep_read_status(d, ws.buf) == 0
+    xv = ops.mxfp4_values(*ops.mxfp4_quantize(tail.double().numpy()))
+    wv = ops.mxfp4_values(*ops.mxfp4_quantize(wt[1].double().numpy().T.copy()))
+    want, size = xv @ wv.T, np.abs(xv) @ np.abs(wv.T)
+    err = np.abs(y[-6:].double().cpu().numpy() - want)
+    assert (err <= 2.0 ** -8 * np.abs(want) + (w.H / 64 + 1) * 2.0 ** -22 * size).all()
+    assert not y[:-6].any()
+
+
 def test_no_rows():
     e = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
     u = torch.empty(0, 32, dtype=torch.uint8, device="cuda")
@@ -178,6 +227,7 @@ WORKLOADS = [
     syn.Workload("no-slots", R=4, E=16, B=0, K=2, S=200, H=576, Hp=256, mode=1),
     syn.Workload("deep", R=2, E=4, B=2, K=2, S=256, H=4160, Hp=512),
     syn.Workload("wide", R=2, E=8, B=4, K=2, S=700, H=512, Hp=1088),
+    syn.Workload("many-k", R=2, E=48, B=24, K=40, S=30, H=128, Hp=64),
 ]
 
 

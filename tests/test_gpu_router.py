@@ -180,6 +180,51 @@ def test_same_bits_in_every_run_and_on_another_stream():
         assert torch.equal(first[k], second[k]) and torch.equal(first[k], third[k]), k
 
 
+def test_in_a_graph():
+    rd = mx.router_dims(5000, 384, 8, 1700, "sigmoid", True, 1.0)
+    l = draw(5000, 384, 10).cuda()
+    want = forward(rd, l)
+    outs = {}
+    ws = torch.full((mx.moonep_router_workspace_bytes(rd),), 0xA5, dtype=torch.uint8, device="cuda")
+    got = {k: torch.zeros_like(v) for k, v in want.items()}
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        mx.moonep_router_forward(rd, l, got["topk_idx"], got["gates"], ws=ws,
+                                 **{k: got[k] for k in ("counts", "prob_sum", "seg_tokens", "loss")})
+    for _ in range(3):
+        for v in got.values():
+            v.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        outs = {k: torch.equal(got[k], want[k]) for k in want}
+        assert all(outs.values()), outs
+
+
+def test_offsets_past_32_bits():
+    T, E, K = 4_900_000, 896, 2  # 4.4e9 logits
+    rd = mx.router_dims(T, E, K, 0, "softmax", True, 1.0, torch.bfloat16)
+    l = torch.zeros(T, E, dtype=torch.bfloat16, device="cuda")
+    tail = draw(5, E, 3, torch.bfloat16)
+    l[-5:] = tail.cuda()
+    idx = torch.full((T, K), -7, dtype=torch.int32, device="cuda")
+    gates = torch.full((T, K), 7e7, device="cuda")
+    mx.moonep_router_forward(rd, l, idx, gates)
+    ids, want, *_ = ops.router(tail.double().numpy(), K, 5, "softmax", True, 1.0)
+    assert np.array_equal(idx[-5:].cpu().numpy(), ids)
+    close(gates[-5:].cpu().numpy(), want, "gates")
+    assert bool((idx[:-5] == torch.arange(K, device="cuda", dtype=torch.int32)).all())
+    dg = torch.zeros(T, K, device="cuda")
+    dg[-5:, 0] = 1.0
+    got = torch.full_like(l, 7.0)
+    mx.moonep_router_backward(rd, l, idx, got, d_gates=dg)
+    grad, size = ops.router_backward(tail.double().numpy(), ids, 5, "softmax", True, 1.0, None,
+                                     dg[-5:].cpu().numpy(), 0.0)
+    err = np.abs(got[-5:].double().cpu().numpy() - grad)
+    assert (err <= 3 * RTOL * size + 2.0 ** -8 * np.abs(grad) + 1e-12).all()
+    assert not got[:-5].any()
+
+
 def test_ids_feed_the_plan():
     d = mx.dims(4, 64, 16, 4, 100, 64, 64)
     rd = mx.router_dims(400, 64, 4, 100)
