@@ -187,6 +187,7 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
   }
   tc_fence_before();
   __syncthreads();
+  __syncwarp();
   tc_fence_after();
   if constexpr (kPair) pair_sync();  // the peer's barriers are ready
   const uint32_t tmem_base = *tmem_slot;
@@ -346,6 +347,7 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         // first accumulator, the first 128 of the second
         const int c0 = (half ^ acc ^ 1) * 128;
         uint32_t r[4][32];
+        __syncwarp();  // one lane issued the stores before: tcgen05.ld wants the warp together
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld_x32(tbase + c0 + c * 32, r[c]);
         tmem_ld_wait();
@@ -420,9 +422,6 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         for (int a = 0; a < 3; ++a)
 #pragma unroll
           for (int j = 0; j < 4; ++j) v[a][j] = rows[a * 128 + 32 * j + lane];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(raw_empty(slot));
-        if (++slot == SLOTS) { slot = 0; phase ^= 1u; }
 #pragma unroll
         for (int h = 0; h < kMxGroup; ++h) {
           if (kb == KB) break;
@@ -449,11 +448,20 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
               rb[8 + 4 * a + j] = h == 0 ? v[1 + a][j].y : v[1 + a][j].w;
             }
           }
+          __syncwarp();  // one lane announced the stage before
           tmem_st_x8(dst, ra);
           tmem_st_x16(dst + 8, rb);
           asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
           tc_fence_before();
           __syncwarp();
+          if (h == 0) {
+            // The ring slot is free only now: the stores took every loaded vector.  An
+            // arrival right after the loads overtook some of them (an mbarrier
+            // operation does not wait for loads in flight): the next scales in the
+            // slot were read instead, once in about 10^5 to 10^7 stages.
+            if (lane == 0) mbar_arrive(raw_empty(slot));
+            if (++slot == SLOTS) { slot = 0; phase ^= 1u; }
+          }
           if (lane == 0) {
             if constexpr (kPair) mbar_arrive_remote_relaxed(pair_map(full(stage), 0));
             else mbar_arrive(full(stage));
@@ -497,8 +505,12 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     }
   }
 
+  // roles of one thread end here one by one: the warps' other lanes wait, and the
+  // instructions that take whole warps come after they are together again
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
+  __syncwarp();
   if constexpr (kPair) pair_sync();  // both CTAs done with TMEM and each other's barriers
   if (warp == 1) {
     tc_fence_after();
