@@ -35,6 +35,8 @@ constexpr int kMxUmmaK = 64;  // K of one MMA
 constexpr int kMxBN = 256;    // columns of a work tile
 constexpr int kMxGroup = 2;   // stages that one load of scales lasts: 512 values of K
 
+constexpr int kMxQueue = 3;   // work items handed out ahead of the epilogue
+
 constexpr uint32_t kMxTmemCols = 512;
 constexpr uint32_t kMxAccStep = 128;   // the second accumulator starts here: 128 columns shared
 constexpr uint32_t kMxScaleCol = 384;  // a slot for a stage's scales: A 2 x 4 columns, B 2 x 8
@@ -55,11 +57,11 @@ struct MxCfg {
   static constexpr int kScaleSlots = 2;
   static constexpr int kTmemSlots = kMxTmemSlots < kStages ? kMxTmemSlots : kStages;
   static constexpr int kOutBytes = 4 * 4096;  // a 32 x 64 bf16 staging buffer a warp
-  static constexpr int kThreads = 32 * 11;
-  static constexpr int kConsumers = CG == 2 ? 20 : 10;  // every role but the claiming producer
-  static constexpr int kNumBars = 2 * kStages + 2 * kScaleSlots + 4 + 2 * kQueue;
+  static constexpr int kThreads = 32 * 12;
+  static constexpr int kConsumers = CG * 10 + 1;  // two producers, 4 + 4 warps a CTA; the MMAs
+  static constexpr int kNumBars = 2 * kStages + 2 * kScaleSlots + 4 + 2 * kMxQueue;
   static constexpr int kSmem = kStages * kStageBytes + kOutBytes + kScaleSlots * kScaleBytes + 1024 +
-                               kNumBars * 8 + 16 + 4 * kQueue;
+                               16 * kMxQueue + kNumBars * 8 + 16;
 };
 static_assert(MxCfg<1>::kSmem <= 232448 && MxCfg<2>::kSmem <= 232448, "shared memory of a CTA");
 
@@ -107,6 +109,76 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[
       : "memory");
 }
 
+// A work item as every role needs it, handed out through a ring in shared memory by
+// a thread that does nothing else.  With the claims and the tile list read by the TMA
+// producer, between one item's loads and the next's, the first two stages of an item
+// came some 2500 clocks late: 1193 -> 1117 us at 262144 rows x 7168 x 2048, 459 -> 379 us
+// at 262144 rows x 4096 x 1024 in 224 groups.  A slot is filled when it is free and not
+// before: an item claimed earlier is one that no idle CTA can take (decoding 16
+// tokens: 125 us with the next item claimed ahead, 117 without).
+struct __align__(16) MxItem {
+  int32_t row0;   // first row of the tile in recv and y
+  int32_t rows;   // rows inside the group
+  int32_t wrow;   // row of the weights of column n0; slots: -1 - that row
+  int32_t n0;     // first column; -1 ends the sequence
+};
+
+template <int CG>
+struct MxQueue {
+  uint32_t full0, empty0;  // this CTA's barriers of slot 0
+  MxItem* items;
+  __device__ uint32_t full(int s) const { return full0 + 8u * s; }
+  __device__ uint32_t empty(int s) const { return empty0 + 8u * s; }
+  // The i-th item, by every lane of a warp or by one thread
+  __device__ __forceinline__ bool wait(int i, bool leader, MxItem& item, volatile int* abort_flag) const {
+    const int s = i % kMxQueue;
+    const uint32_t parity = (i / kMxQueue) & 1;
+    // the leader's items come from its own CTA
+    if (!(leader ? mbar_wait(full(s), parity, abort_flag)
+                 : mbar_wait_cluster(full(s), parity, abort_flag)))
+      return false;
+    const int4 v = *reinterpret_cast<const int4*>(items + s);
+    item = MxItem{v.x, v.y, v.z, v.w};
+    return true;
+  }
+  // Once a role, after its lanes have read the item.  `read` comes out of the item and
+  // is 0: with it in the address the arrival cannot be issued before the load has
+  // landed, which nothing else makes an mbarrier operation wait for.
+  __device__ __forceinline__ void announce(int i, bool leader, uint32_t read) const {
+    const uint32_t bar = empty(i % kMxQueue) + 8u * read;
+    if (leader) mbar_arrive(bar);
+    else mbar_arrive_remote_relaxed(pair_map(bar, 0));
+  }
+  __device__ __forceinline__ bool take(int i, bool leader, MxItem& item, volatile int* abort_flag) const {
+    if (!wait(i, leader, item, abort_flag)) return false;
+    announce(i, leader, item.n0 < -1 ? 1u : 0u);
+    return true;
+  }
+  __device__ __forceinline__ bool take_warp(int i, bool leader, MxItem& item,
+                                            volatile int* abort_flag) const {
+    if (!__all_sync(0xffffffffu, wait(i, leader, item, abort_flag))) return false;
+    const uint32_t read = __any_sync(0xffffffffu, item.n0 < -1) ? 1u : 0u;
+    if ((threadIdx.x & 31) == 0) announce(i, leader, read);
+    __syncwarp();
+    return true;
+  }
+  // For the thread that hands items out: the i-th slot is free; the i-th item
+  __device__ __forceinline__ bool wait_free(int i, volatile int* abort_flag) const {
+    return mbar_wait_cluster(empty(i % kMxQueue), ((i / kMxQueue) & 1) ^ 1u, abort_flag);
+  }
+  __device__ __forceinline__ void push(int i, const MxItem& item) const {
+    const int s = i % kMxQueue;
+    *reinterpret_cast<int4*>(items + s) = make_int4(item.row0, item.rows, item.wrow, item.n0);
+    if constexpr (CG == 2)
+      asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                       pair_map(smem_u32(items + s), 1)),
+                   "r"(item.row0), "r"(item.rows), "r"(item.wrow), "r"(item.n0)
+                   : "memory");
+    mbar_arrive(full(s));
+    if constexpr (CG == 2) mbar_arrive_remote(pair_map(full(s), 1));
+  }
+};
+
 template <int CG>
 __global__ void __launch_bounds__(MxCfg<CG>::kThreads, 1)
 k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_wh,
@@ -121,7 +193,8 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* out_stage = smem + STAGES * Cfg::kStageBytes;
   uint8_t* scale_ring = out_stage + Cfg::kOutBytes;
-  uint64_t* bars = (uint64_t*)(scale_ring + SLOTS * Cfg::kScaleBytes);
+  MxItem* items = (MxItem*)(scale_ring + SLOTS * Cfg::kScaleBytes);
+  uint64_t* bars = (uint64_t*)(items + kMxQueue);
   uint32_t* tmem_slot = (uint32_t*)(bars + Cfg::kNumBars);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   const uint32_t bar0 = smem_u32(bars);
@@ -133,7 +206,7 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
   const uint32_t bar2 = bar1 + 16u * SLOTS;
   auto tfull = [&](int b) { return bar2 + 8u * b; };
   const uint32_t tempty = bar2 + 16u, drain = bar2 + 24u;
-  const PairQueue q{bar2 + 32u, bar2 + 32u + 8u * kQueue, (int32_t*)(tmem_slot + 2)};
+  const MxQueue<CG> q{bar2 + 32u, bar2 + 32u + 8u * kMxQueue, items};
   constexpr uint64_t kDrainNs = 200000000ull;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -166,7 +239,10 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     for (int b = 0; b < 2; ++b) mbar_init(tfull(b), 1);
     mbar_init(tempty, 4 * CG);
     mbar_init(drain, 1);
-    queue_init(q, Cfg::kConsumers);
+    for (int s = 0; s < kMxQueue; ++s) {
+      mbar_init(q.full(s), 1);
+      mbar_init(q.empty(s), Cfg::kConsumers);
+    }
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -195,10 +271,6 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     *abort_flag = 1;
     set_error(p.status, MOONEP_ERR_TIMEOUT);
   };
-  auto weight_row = [&](const MTile& mt, int t) {  // first weight row of item t
-    return (mt.wsel >= 0 ? mt.wsel : (-1 - mt.wsel)) * N + (t % NT) * kMxBN;
-  };
-
   if (warp == 0) {
     // ---------------- TMA producer ----------------
     if (elect_one()) {
@@ -209,28 +281,19 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
       int stage = 0, issued = 0, slot = 0;
       uint32_t phase = 0;
       bool ok = true;
-      int next = leader ? atomicAdd(sched, 1) : 0;  // claimed one item ahead
       for (int i = 0; ok; ++i) {
-        int t;
-        if (leader) {
-          t = next >= total ? -1 : next;
-          if (!queue_push(q, i, t, abort_flag, kPair)) { ok = false; break; }
-          if (t >= 0) next = atomicAdd(sched, 1);
-        } else if (!queue_take(q, i, false, true, t, abort_flag)) {
-          ok = false;
-          break;
-        }
-        if (t < 0) break;
-        const MTile mt = p.mtiles[t / NT];
-        const CUtensorMap* wmap = mt.wsel >= 0 ? &tm_wh : &tm_ws;
-        const int wrow = weight_row(mt, t) + (int)crank * Cfg::kBRows;
-        const int row0 = mt.row0 + (int)crank * kMmaM;
+        MxItem it;
+        if (!q.take(i, leader, it, abort_flag)) { ok = false; break; }
+        if (it.n0 < 0) break;
+        const CUtensorMap* wmap = it.wrow >= 0 ? &tm_wh : &tm_ws;
+        const int wrow = (it.wrow >= 0 ? it.wrow : -1 - it.wrow) + (int)crank * Cfg::kBRows;
+        const int row0 = it.row0 + (int)crank * kMmaM;
         // Rows past the group's end are loaded as zeros, through a copy of the map that
         // ends there: their products are not stored, and on zeros they take less power
         const CUtensorMap* amap = &tm_a;
-        if (mt.rows < (int)(crank + 1) * kMmaM) {
+        if (it.rows < (int)(crank + 1) * kMmaM) {
           uint4* m = maps + slot * 16;
-          tmap_set_dim1(m, mt.row0 + mt.rows);
+          tmap_set_dim1(m, it.row0 + it.rows);
           tmap_publish(m);
           amap = reinterpret_cast<const CUtensorMap*>(m);
           if (++slot == kTmapSlots) slot = 0;
@@ -253,7 +316,6 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
       }
-      if (leader) queue_finish(sched, sched + 1, gridDim.x / CG);
       if (ok) {
         for (int i = 0; i < STAGES; ++i) {  // every fill released: no commit still in flight
           if (!mbar_wait(empty(stage), phase ^ 1u, nullptr)) { ok = false; break; }
@@ -279,11 +341,9 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
       uint32_t phase = 0;
       bool ok = true;
       for (int i = 0; ok; ++i) {
-        // the leader's own slot, written by its own producer: no cluster-scope order
-        if (!mbar_wait(q.full(i % kQueue), (i / kQueue) & 1, abort_flag)) { ok = false; break; }
-        const int t = *reinterpret_cast<volatile int32_t*>(q.items + i % kQueue);
-        mbar_arrive(q.empty(i % kQueue));
-        if (t < 0) break;
+        MxItem it;
+        if (!q.take(i, true, it, abort_flag)) { ok = false; break; }
+        if (it.n0 < 0) break;
         // the shared columns of the tile before are drained
         if (!mbar_wait(tempty, (i & 1) ^ 1u, abort_flag)) { ok = false; break; }
         tc_fence_after();
@@ -322,14 +382,13 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     const int qw = warp & 3;
     uint8_t* buf = out_stage + qw * 4096;
     for (int i = 0;; ++i) {
-      int t;
-      if (!queue_take_warp(q, i, leader, t, abort_flag)) {
+      MxItem it;
+      if (!q.take_warp(i, leader, it, abort_flag)) {
         if (lane == 0) fail();
         break;
       }
-      if (t < 0) break;
-      const MTile mt = p.mtiles[t / NT];
-      const int n0 = (t % NT) * kMxBN;
+      if (it.n0 < 0) break;
+      const int n0 = it.n0;
       const int acc = i & 1;
       if (!__all_sync(0xffffffffu, mbar_wait(tfull(acc), (i >> 1) & 1, abort_flag))) {
         if (lane == 0) fail();
@@ -338,9 +397,9 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
       tc_fence_after();
       const int wrow0 = (int)crank * kMmaM + qw * 32;  // this warp's first row of the tile
       const uint32_t tbase = tmem_base + ((uint32_t)(qw * 32) << 16) + (uint32_t)acc * kMxAccStep;
-      const bool whole = wrow0 + 32 <= mt.rows;  // all 32 rows inside the group
-      const bool valid = wrow0 + lane < mt.rows;
-      uint16_t* yrow = y + (size_t)(mt.row0 + wrow0 + lane) * N + n0;
+      const bool whole = wrow0 + 32 <= it.rows;  // all 32 rows inside the group
+      const bool valid = wrow0 + lane < it.rows;
+      uint16_t* yrow = y + (size_t)(it.row0 + wrow0 + lane) * N + n0;
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
         // the columns that both accumulators use come first: the last 128 of the
@@ -384,7 +443,7 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
               asm volatile(
                   "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
                       (uint64_t)&tm_y),
-                  "r"(n0 + n), "r"(mt.row0 + wrow0), "r"(smem_u32(buf))
+                  "r"(n0 + n), "r"(it.row0 + wrow0), "r"(smem_u32(buf))
                   : "memory");
               asm volatile("cp.async.bulk.commit_group;" ::: "memory");
             }
@@ -408,9 +467,9 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     int before = Cfg::kTmemSlots;  // stages still without an earlier one
     bool ok = true;
     for (int i = 0; ok; ++i) {
-      int t;
-      if (!queue_take_warp(q, i, leader, t, abort_flag)) { ok = false; break; }
-      if (t < 0) break;
+      MxItem it;
+      if (!q.take_warp(i, leader, it, abort_flag)) { ok = false; break; }
+      if (it.n0 < 0) break;
       for (int kb = 0; ok && kb < KB;) {
         if (!__all_sync(0xffffffffu, mbar_wait(raw_full(slot), phase, abort_flag))) {
           ok = false;
@@ -474,35 +533,52 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     }
     if (!ok && lane == 0) fail();
     __syncwarp();
-  } else if (elect_one()) {
+  } else if (warp == 10) {
     // ---------------- scales to shared memory ----------------
-    int slot = 0, issued = 0;
-    uint32_t phase = 0;
+    if (elect_one()) {
+      int slot = 0, issued = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int i = 0; ok; ++i) {
+        MxItem it;
+        if (!q.take(i, leader, it, abort_flag)) { ok = false; break; }
+        if (it.n0 < 0) break;
+        const CUtensorMap* smap = it.wrow >= 0 ? &tm_sh : &tm_ss;
+        const int wrow = it.wrow >= 0 ? it.wrow : -1 - it.wrow, row0 = it.row0 + (int)crank * kMmaM;
+        for (int g = 0; g < KG; ++g) {
+          if (!mbar_wait(raw_empty(slot), phase ^ 1u, abort_flag)) { ok = false; break; }
+          mbar_expect_tx(raw_full(slot), Cfg::kScaleBytes);
+          const uint32_t dst = smem_u32(scale_ring + slot * Cfg::kScaleBytes);
+          tma_load_2d(dst, &tm_sa, raw_full(slot), g * 16, row0);
+          tma_load_2d(dst + kMmaM * 16, smap, raw_full(slot), g * 16, wrow);
+          ++issued;
+          if (++slot == SLOTS) { slot = 0; phase ^= 1u; }
+        }
+      }
+      if (!ok) {
+        fail();
+        for (int i = 0; i < min(issued, SLOTS); ++i) {  // the copies this thread started
+          if (slot == 0) { slot = SLOTS - 1; phase ^= 1u; } else { --slot; }
+          mbar_wait(raw_full(slot), phase, nullptr, kDrainNs);
+        }
+      }
+    }
+  } else if (leader && lane == 0) {
+    // ---------------- work items ----------------
     bool ok = true;
-    for (int i = 0; ok; ++i) {
-      int t;
-      if (!queue_take(q, i, leader, true, t, abort_flag)) { ok = false; break; }
-      if (t < 0) break;
+    for (int i = 0; (ok = q.wait_free(i, abort_flag)); ++i) {
+      const int t = atomicAdd(sched, 1);
+      if (t >= total) {
+        q.push(i, MxItem{0, 0, 0, -1});
+        break;
+      }
       const MTile mt = p.mtiles[t / NT];
-      const CUtensorMap* smap = mt.wsel >= 0 ? &tm_sh : &tm_ss;
-      const int wrow = weight_row(mt, t), row0 = mt.row0 + (int)crank * kMmaM;
-      for (int g = 0; g < KG; ++g) {
-        if (!mbar_wait(raw_empty(slot), phase ^ 1u, abort_flag)) { ok = false; break; }
-        mbar_expect_tx(raw_full(slot), Cfg::kScaleBytes);
-        const uint32_t dst = smem_u32(scale_ring + slot * Cfg::kScaleBytes);
-        tma_load_2d(dst, &tm_sa, raw_full(slot), g * 16, row0);
-        tma_load_2d(dst + kMmaM * 16, smap, raw_full(slot), g * 16, wrow);
-        ++issued;
-        if (++slot == SLOTS) { slot = 0; phase ^= 1u; }
-      }
+      const int n0 = (t % NT) * kMxBN;
+      const int wrow = (mt.wsel >= 0 ? mt.wsel : -1 - mt.wsel) * N + n0;
+      q.push(i, MxItem{mt.row0, mt.rows, mt.wsel >= 0 ? wrow : -1 - wrow, n0});
     }
-    if (!ok) {
-      fail();
-      for (int i = 0; i < min(issued, SLOTS); ++i) {  // the copies this thread started
-        if (slot == 0) { slot = SLOTS - 1; phase ^= 1u; } else { --slot; }
-        mbar_wait(raw_full(slot), phase, nullptr, kDrainNs);
-      }
-    }
+    queue_finish(sched, sched + 1, gridDim.x / CG);
+    if (!ok) fail();
   }
 
   // roles of one thread end here one by one: the warps' other lanes wait, and the
