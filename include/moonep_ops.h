@@ -115,7 +115,8 @@ int moonep_mxfp4_quantize_weights(int32_t n, int32_t H, int32_t Hp, const uint16
                                   uint8_t* codes, uint8_t* scales, void* stream);
 
 /* moonep_prefetch_weights on quantised weights.  home: [E][Hp][..], slots:
- * [R][B][Hp][..], codes of H/2 and scales of pitch(H) bytes a row. */
+ * [R][B][Hp][..], codes of H/2 and scales of pitch(H) bytes a row.  An expert's
+ * codes stay below 16 GiB (MOONEP_ERR_SHAPE). */
 int moonep_mxfp4_prefetch_weights(const moonep_dims* dims, void* plan_ws, const uint8_t* home_codes,
                                   const uint8_t* home_scales, uint8_t* slot_codes,
                                   uint8_t* slot_scales, void* stream);

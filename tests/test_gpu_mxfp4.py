@@ -291,6 +291,36 @@ def test_same_bits_again_and_on_another_stream_and_in_a_graph():
     assert torch.equal(first, r["y"])
 
 
+@pytest.mark.parametrize("S,E,K,H,Hp,launches", [(16, 96, 8, 7168, 2048, 2000),
+                                                 (2400, 64, 4, 4096, 1024, 2000),
+                                                 (300, 12, 3, 1088, 320, 3000)])
+def test_launch_after_launch_gives_the_same_bits(S, E, K, H, Hp, launches):
+    # rows and scales that differ from stage to stage: a stage that takes another's shows
+    d = mx.dims(1, E, 0, K, S, H, Hp, 1)
+    g = torch.Generator(device="cuda").manual_seed(S)
+    ids = torch.topk(torch.randn(S, E, generator=g, device="cuda"), K).indices.int()
+    ws = mx.PlanWorkspace(d)
+    mx.moonep_plan(d, ids, ws.buf)
+    pitch = mx.mxfp4_scale_pitch(H)
+
+    def codes_and_scales(rows):
+        q = torch.randint(0, 256, (rows, H // 2), generator=g, device="cuda", dtype=torch.uint8)
+        s = torch.randint(120, 130, (rows, pitch), generator=g, device="cuda", dtype=torch.uint8)
+        return q, s
+
+    rq, rs = codes_and_scales(d.N)
+    hq, hs = codes_and_scales(E * Hp)
+    y = torch.empty(d.N, Hp, dtype=torch.bfloat16, device="cuda")
+    run = lambda: mx.moonep_mxfp4_grouped_gemm(d, ws.buf, rq, rs, hq, hs, None, None, y)  # noqa: E731
+    run()
+    first = y.clone()
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(launches):
+        run()
+        differ += (y != first).any()
+    assert int(differ) == 0 and mx.moonep_read_status(d, ws.buf) == 0
+
+
 def test_a_failed_plan_writes_nothing():
     w = syn.TINY
     d = mx.dims(w.R, w.E, w.B, w.K, w.S, w.H, w.Hp)

@@ -180,6 +180,24 @@ def test_same_bits_in_every_run_and_on_another_stream():
         assert torch.equal(first[k], second[k]) and torch.equal(first[k], third[k]), k
 
 
+@pytest.mark.parametrize("E,K,score,dtype", [(384, 8, "softmax", torch.float32),
+                                             (896, 16, "sigmoid", torch.bfloat16)])
+def test_launch_after_launch_gives_the_same_bits(E, K, score, dtype):
+    T = 20000
+    rd = mx.router_dims(T, E, K, 3000, score, True, 1.0, dtype)
+    l = draw(T, E, 12, dtype).cuda()
+    want = forward(rd, l)
+    got = {k: torch.zeros_like(v) for k, v in want.items()}
+    ws = torch.empty(mx.moonep_router_workspace_bytes(rd), dtype=torch.uint8, device="cuda")
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(500):
+        mx.moonep_router_forward(rd, l, got["topk_idx"], got["gates"], ws=ws,
+                                 **{k: got[k] for k in ("counts", "prob_sum", "seg_tokens", "loss")})
+        for k in want:
+            differ += (got[k] != want[k]).any()
+    assert int(differ) == 0
+
+
 def test_in_a_graph():
     rd = mx.router_dims(5000, 384, 8, 1700, "sigmoid", True, 1.0)
     l = draw(5000, 384, 10).cuda()
