@@ -22,27 +22,53 @@ __device__ __forceinline__ int place(int j, int lane) {
   return VEC ? (j >> 2) * 128 + lane * 4 + (j & 3) : j * 32 + lane;
 }
 
+// Whether step c (of four neighbours, or of one value) of a lane lies in the row of E.
+// Vector rows have as many steps as E needs: only the last one can lie outside.
+template <int N, bool VEC>
+__device__ __forceinline__ bool inside(int c, int lane, int E) {
+  return VEC ? c < N / 4 - 1 || c * 128 + lane * 4 < E : c * 32 + lane < E;
+}
+
 template <typename T>
 __device__ __forceinline__ float to_f32(T v) {
   return (float)v;
 }
 
+// Starts the copy of a row (VEC) into the warp's row of shared memory, every lane the
+// values that are its own.
+template <typename T, int N>
+__device__ __forceinline__ void fetch_row(T* s_row, const T* __restrict__ row, int E, int lane) {
+  const uint32_t to = (uint32_t)__cvta_generic_to_shared(s_row + lane * 4);
+  const T* from = row + lane * 4;
+#pragma unroll
+  for (int c = 0; c < N / 4; ++c) {
+    if (inside<N, true>(c, lane, E))
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to + c * 128 * (int)sizeof(T)),
+                   "l"(from + c * 128), "n"(4 * sizeof(T))
+                   : "memory");
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void await_row() {
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncwarp();
+}
+
 // A row's values of this lane; -inf past the row's end, where a value adds
 // nothing to any sum of exponentials.
 template <typename T, int N, bool VEC>
-__device__ __forceinline__ void load_row(const T* __restrict__ row, int E, int lane,
-                                         float (&l)[N]) {
+__device__ __forceinline__ void load_row(const T* row, int E, int lane, float (&l)[N]) {
   if constexpr (VEC) {
 #pragma unroll
     for (int c = 0; c < N / 4; ++c) {
       const int at = c * 128 + lane * 4;
       float v[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      if (at < E) {
+      if (inside<N, true>(c, lane, E)) {
         if constexpr (sizeof(T) == 4) {
-          const float4 f = __ldg(reinterpret_cast<const float4*>(row + at));
+          const float4 f = *reinterpret_cast<const float4*>(row + at);
           v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
         } else {
-          const uint2 u = __ldg(reinterpret_cast<const uint2*>(row + at));
+          const uint2 u = *reinterpret_cast<const uint2*>(row + at);
           v[0] = __uint_as_float(u.x << 16), v[1] = __uint_as_float(u.x & 0xffff0000u);
           v[2] = __uint_as_float(u.y << 16), v[3] = __uint_as_float(u.y & 0xffff0000u);
         }
@@ -66,7 +92,7 @@ __device__ __forceinline__ void store_row(T* __restrict__ row, int E, int lane,
 #pragma unroll
     for (int c = 0; c < N / 4; ++c) {
       const int at = c * 128 + lane * 4;
-      if (at >= E) continue;
+      if (!inside<N, true>(c, lane, E)) continue;
       if constexpr (sizeof(T) == 4) {
         *reinterpret_cast<float4*>(row + at) =
             make_float4(l[4 * c], l[4 * c + 1], l[4 * c + 2], l[4 * c + 3]);
@@ -215,8 +241,8 @@ struct __align__(16) Candidates {
 // in on.  What no bound tells apart (ties) and a bound of -inf (which the places past
 // the row's end reach too) take the K largest one after the other.
 template <typename T, int N, bool VEC>
-__device__ __forceinline__ void select_top(const float (&l)[N], const T* __restrict__ row, int E,
-                                           int K, int lane, float most, float m, uint32_t keep,
+__device__ __forceinline__ void select_top(const float (&l)[N], const T* row, int E, int K,
+                                           int lane, float most, float m, uint32_t keep,
                                            float& guess, Candidates& list, int& rank, float& value,
                                            int& expert) {
   constexpr int NW = (N + 31) / 32;
@@ -321,6 +347,15 @@ constexpr int router_blocks() {
 template <int N>
 constexpr bool sums_in_smem() {
   return N > 16;
+}
+
+// Rows of more than 512 come by way of shared memory, one row ahead: with 24 warps on a
+// multiprocessor, loads waited for at once cost a quarter of the time between two
+// instructions (65536 x 896 bf16: 86 us so, 80 ahead).  With the 32 warps of shorter rows
+// the copy costs as much as it saves (65536 x 384 fp32: 52.5 us at once, 53.6 ahead).
+template <int N, bool VEC>
+constexpr bool rows_ahead() {
+  return VEC && N > 16;
 }
 
 // Sum over the block in a fixed order, to thread 0.  (fp32: each of these sums has
@@ -429,13 +464,16 @@ k_router(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__
          RouterOut out, RouterScratch ws) {
   constexpr int W = router_warps<N>();
   constexpr bool kSmemSums = LOSS && sums_in_smem<N>(), kRegSums = LOSS && !kSmemSums;
+  constexpr bool kAhead = rows_ahead<N, VEC>();
   constexpr int KI = SHORT ? 1 : kRouterMaxK / 32;
   __shared__ Candidates s_cand[SHORT ? W : 1];
   __shared__ unsigned long long s_list[SHORT ? 1 : W][kRouterMaxK];
-  extern __shared__ float s_dyn[];  // LOSS: the warps' sums [W][E], then counts [E]
+  // LOSS: the warps' sums [W][E], then counts [E]; rows ahead: the warps' [W][E]
+  extern __shared__ __align__(16) float s_dyn[];
   __shared__ int s_tokens, s_bad;
   int32_t* s_cnt = reinterpret_cast<int32_t*>(s_dyn + (size_t)W * d.E);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  T* s_row = reinterpret_cast<T*>(s_dyn + (LOSS ? (size_t)(W + 1) * d.E : 0)) + (size_t)warp * d.E;
   const uint32_t keep = sort_directions(lane);
   float guess = -INFINITY;
 
@@ -460,9 +498,12 @@ k_router(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__
       __syncthreads();
     }
 
+    if (kAhead && begin + warp < end)
+      fetch_row<T, N>(s_row, logits + (size_t)(begin + warp) * d.E, d.E, lane);
     for (int t = begin + warp; t < end; t += W) {
       float l[N];
-      const T* row = logits + (size_t)t * d.E;
+      const T* row = kAhead ? s_row : logits + (size_t)t * d.E;
+      if constexpr (kAhead) await_row();
       load_row<T, N, VEC>(row, d.E, lane, l);
       const bool live = mask == nullptr || mask[t] != 0;
       float most = -INFINITY;
@@ -492,6 +533,10 @@ k_router(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__
         __syncwarp();
       }
 
+      // all that was read of this row has been used (and the warp is together): the next
+      // one's way from memory is behind the scores, sums and gates of this one
+      if (kAhead && t + W < end) fetch_row<T, N>(s_row, logits + (size_t)(t + W) * d.E, d.E, lane);
+
       // 1 / sum of the row's scores, where it is needed; a NaN in the row, which is in
       // every softmax score, shows in it
       float inv = 1.f;
@@ -518,7 +563,7 @@ k_router(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__
         } else if constexpr (kSmemSums && VEC) {
 #pragma unroll
           for (int c = 0; c < N / 4; ++c)
-            if (c * 128 + lane * 4 < d.E) {
+            if (inside<N, true>(c, lane, d.E)) {
               float4& q = *reinterpret_cast<float4*>(sums + c * 128 + lane * 4);
               q = make_float4(fmaf(l[4 * c], inv, q.x), fmaf(l[4 * c + 1], inv, q.y),
                               fmaf(l[4 * c + 2], inv, q.z), fmaf(l[4 * c + 3], inv, q.w));
@@ -581,130 +626,174 @@ k_router(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__
 //   normalised; else scale s_k d_gate_k
 // The chosen experts' a lie in a row of shared memory that is zero elsewhere.
 template <typename T, int N, bool VEC, bool SHORT, int KIND>
-__global__ void __launch_bounds__(router_warps<N>() * 32)
+__global__ void __launch_bounds__(router_warps<N>() * 32, router_blocks<N>())
 k_router_backward(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__ mask,
                   const int32_t* __restrict__ topk_idx, const float* __restrict__ d_gates,
                   const int32_t* __restrict__ counts, const int32_t* __restrict__ seg_tokens,
                   const float* __restrict__ d_loss, T* __restrict__ d_logits) {
   constexpr int W = router_warps<N>();
   constexpr int KI = SHORT ? 1 : kRouterMaxK / 32;
-  extern __shared__ float s_a[];  // [W][E rounded up to 4]
+  constexpr int V = VEC ? 4 : 1;  // neighbours in a lane
+  // w [E rounded up to 4], the warps' a [W][same], VEC: the warps' rows [W][E]
+  extern __shared__ __align__(16) float s_dyn[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int E4 = (d.E + 3) & ~3;
-  float* a = s_a + (size_t)warp * E4;
+  float* w = s_dyn;
+  float* a = s_dyn + (size_t)(1 + warp) * E4;
+  T* s_row = reinterpret_cast<T*>(s_dyn + (size_t)(1 + W) * E4) + (size_t)warp * d.E;
   for (int e = lane; e < E4; e += 32) a[e] = 0.f;
   __syncwarp();
+  // V values of a row of shared memory
+  auto values = [](const float* at, float (&v)[V]) {
+    if constexpr (VEC) {
+      const float4 f = *reinterpret_cast<const float4*>(at);
+      v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+    } else {
+      v[0] = *at;
+    }
+  };
 
   const int first = blockIdx.x * d.per_block;
   const int last = min(first + d.per_block, d.T);
-  int seg = -1;
-  float w[N];
-#pragma unroll
-  for (int j = 0; j < N; ++j) w[j] = 0.f;
+  for (int begin = first; begin < last;) {
+    const int g = d_loss != nullptr ? begin / d.segment : 0;
+    const int end = d_loss != nullptr ? (int)min((int64_t)last, (int64_t)(g + 1) * d.segment) : last;
+    float coef = 0.f;
+    if (d_loss != nullptr) {
+      const float n = (float)seg_tokens[g];
+      coef = n > 0.f ? *d_loss * ((float)d.E / ((float)d.G * (float)d.K * n)) / n : 0.f;
+    }
+    __syncthreads();  // the last segment's w has been read
+    for (int e = threadIdx.x; e < E4; e += blockDim.x)
+      w[e] = d_loss != nullptr && e < d.E ? coef * (float)__ldg(counts + (size_t)g * d.E + e) : 0.f;
+    __syncthreads();
 
-  // a token's chosen experts and their gradients, loaded one token ahead
-  int id[KI], next_id[KI];
-  float dg[KI], next_dg[KI];
-  auto fetch = [&](int t) {
+    // a token's chosen experts and their gradients, loaded one token ahead
+    int id[KI], next_id[KI];
+    float dg[KI], next_dg[KI];
+    auto fetch = [&](int t) {
 #pragma unroll
-    for (int i = 0; i < KI; ++i) {
-      const int k = i * 32 + lane;
-      const bool there = d_gates != nullptr && t < last && k < d.K;
-      next_id[i] = there ? topk_idx[(size_t)t * d.K + k] : -1;
-      next_dg[i] = there ? d_gates[(size_t)t * d.K + k] : 0.f;
-    }
-  };
-  fetch(first + warp);
-  for (int t = first + warp; t < last; t += W) {
-#pragma unroll
-    for (int i = 0; i < KI; ++i) {
-      id[i] = next_id[i] < d.E ? next_id[i] : -1;
-      dg[i] = next_dg[i];
-    }
-    fetch(t + W);
-    const T* row = logits + (size_t)t * d.E;
-    T* drow = d_logits + (size_t)t * d.E;
-    const bool live = mask == nullptr || mask[t] != 0;
-    float l[N];
-    if (live) {
-      load_row<T, N, VEC>(row, d.E, lane, l);
-      float s[KI];
-#pragma unroll
-      for (int i = 0; i < KI; ++i) s[i] = id[i] >= 0 ? to_f32(row[id[i]]) : 0.f;
-      if (d_loss != nullptr && t / d.segment != seg) {
-        seg = t / d.segment;
-        const float n = (float)seg_tokens[seg];
-        const float coef = n > 0.f ? *d_loss * ((float)d.E / ((float)d.G * (float)d.K * n)) / n : 0.f;
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-          const int e = place<N, VEC>(j, lane);
-          w[j] = e < d.E ? coef * (float)__ldg(counts + (size_t)seg * d.E + e) : 0.f;
-        }
+      for (int i = 0; i < KI; ++i) {
+        const int k = i * 32 + lane;
+        const bool there = d_gates != nullptr && t < end && k < d.K;
+        next_id[i] = there ? topk_idx[(size_t)t * d.K + k] : -1;
+        next_dg[i] = there ? d_gates[(size_t)t * d.K + k] : 0.f;
       }
-      float m = -INFINITY;
+    };
+    auto is_live = [&](int t) { return t < end && (mask == nullptr || mask[t] != 0); };
+    fetch(begin + warp);
+    bool live = is_live(begin + warp);
+    if (VEC && live) fetch_row<T, N>(s_row, logits + (size_t)(begin + warp) * d.E, d.E, lane);
+    for (int t = begin + warp; t < end; t += W) {
 #pragma unroll
-      for (int j = 0; j < N; ++j) m = fmaxf(m, l[j]);
-      const Scores<KIND> score(d.score, warp_max(m));
-      // the scores (up to their common factor), their sum and that with w
-      float rest[N];  // sigmoid: 1 - s
-      float sum = 0.f, dot = 0.f;
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        if (score.softmax()) {
-          l[j] = score(l[j]);
-        } else {
-          const float x = fast_exp(score.shift - l[j]);
-          const float v = fast_rcp(x + score.one);
-          // near s = 1 (then the shift is 0) without cancellation
-          rest[j] = l[j] > 0.f ? x * v : fmaf(-v, score.one, 1.f);
-          l[j] = v;
-        }
-        sum += l[j];
-        dot = fmaf(l[j], w[j], dot);
+      for (int i = 0; i < KI; ++i) {
+        id[i] = next_id[i] < d.E ? next_id[i] : -1;
+        dg[i] = next_dg[i];
       }
-      sum = warp_sum(sum);
-      const float inv = sum == 0.f ? 0.f : fast_rcp(sum);
-      dot = warp_sum(dot) * inv;
+      fetch(t + W);
+      const bool next_live = is_live(t + W);
+      const T* next_row = logits + (size_t)(t + W) * d.E;
+      T* drow = d_logits + (size_t)t * d.E;
+      float l[N];
+      if (live) {
+        const T* row = VEC ? s_row : logits + (size_t)t * d.E;
+        if constexpr (VEC) await_row();
+        load_row<T, N, VEC>(row, d.E, lane, l);
+        float s[KI];
+#pragma unroll
+        for (int i = 0; i < KI; ++i) s[i] = id[i] >= 0 ? to_f32(row[id[i]]) : 0.f;
+        float m = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < N; ++j) m = fmaxf(m, l[j]);
+        const Scores<KIND> score(d.score, warp_max(m));
+        // the scores (up to their common factor), their sum and that with w.  A
+        // sigmoid's place keeps the smaller of s and 1 - s without cancellation (where
+        // that is 1 - s, l > 0, the factor is 1): the other follows, and their product
+        // is all that the gradient needs
+        float sum = 0.f, dot = 0.f;
+#pragma unroll
+        for (int c = 0; c < N / V; ++c) {
+          const int at = place<N, VEC>(c * V, lane);
+          float wv[V] = {};
+          if (inside<N, VEC>(c, lane, d.E)) values(w + at, wv);
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            float& v = l[c * V + i];
+            float q;
+            if (score.softmax()) {
+              v = q = score(v);
+            } else {
+              const float x = fast_exp(score.shift - v);
+              q = fast_rcp(x + score.one);
+              v = v > 0.f ? x * q : q;
+            }
+            sum += q;
+            dot = fmaf(q, wv[i], dot);
+          }
+        }
+        sum = warp_sum(sum);
+        const float inv = sum == 0.f ? 0.f : fast_rcp(sum);
+        dot = warp_sum(dot) * inv;
 
-      if (d_gates != nullptr) {
-        float total = 0.f, with = 0.f;
+        if (d_gates != nullptr) {
+          float total = 0.f, with = 0.f;
+          float rest[KI];  // sigmoid: 1 - s
 #pragma unroll
-        for (int i = 0; i < KI; ++i) {
-          s[i] = id[i] >= 0 ? score(s[i]) : 0.f;
-          total += s[i];
-          with = fmaf(s[i], dg[i], with);
+          for (int i = 0; i < KI; ++i) {
+            rest[i] = 1.f;
+            if (!score.softmax()) {
+              const float x = fast_exp(score.shift - s[i]), q = fast_rcp(x + score.one);
+              rest[i] = s[i] > 0.f ? x * q : fmaf(-q, score.one, 1.f);
+            }
+            s[i] = id[i] >= 0 ? score(s[i]) : 0.f;
+            total += s[i];
+            with = fmaf(s[i], dg[i], with);
+          }
+          float factor = score.softmax() ? inv : score.one, mean = 0.f;
+          if (d.normalise) {
+            total = warp_sum(total);
+            factor = total == 0.f ? 0.f : fast_rcp(total);
+            mean = warp_sum(with) * factor;
+          } else if (score.softmax()) {
+            dot = fmaf(warp_sum(with), d.scale * inv, dot);
+          }
+#pragma unroll
+          for (int i = 0; i < KI; ++i)
+            if (id[i] >= 0) a[id[i]] = d.scale * (s[i] * factor) * (dg[i] - mean) * rest[i];
         }
-        float factor = score.softmax() ? inv : score.one, mean = 0.f;
-        if (d.normalise) {
-          total = warp_sum(total);
-          factor = total == 0.f ? 0.f : fast_rcp(total);
-          mean = warp_sum(with) * factor;
-        } else if (score.softmax()) {
-          dot = fmaf(warp_sum(with), d.scale * inv, dot);
+        __syncwarp();
+        // all that was read of this row has been used: the next one's way from memory
+        // is behind what is left of this one
+        if (VEC && next_live) fetch_row<T, N>(s_row, next_row, d.E, lane);
+        const float dot_inv = dot * inv;
+#pragma unroll
+        for (int c = 0; c < N / V; ++c) {
+          const int at = place<N, VEC>(c * V, lane);
+          float wv[V] = {}, av[V] = {};
+          if (inside<N, VEC>(c, lane, d.E)) values(w + at, wv), values(a + at, av);
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            float& v = l[c * V + i];
+            if (!score.softmax()) v *= fmaf(-v, score.one, 1.f);
+            v = fmaf(v, fmaf(wv[i], inv, -dot_inv), av[i]);
+          }
         }
+        if (d_gates != nullptr) {
+          __syncwarp();
 #pragma unroll
-        for (int i = 0; i < KI; ++i)
-          if (id[i] >= 0) a[id[i]] = d.scale * (s[i] * factor) * (dg[i] - mean);
-        __syncwarp();
+          for (int i = 0; i < KI; ++i)
+            if (id[i] >= 0) a[id[i]] = 0.f;
+          __syncwarp();
+        }
+      } else {
+        if (VEC && next_live) fetch_row<T, N>(s_row, next_row, d.E, lane);
+#pragma unroll
+        for (int j = 0; j < N; ++j) l[j] = 0.f;
       }
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const int e = place<N, VEC>(j, lane);
-        l[j] = fmaf(l[j] * inv, w[j] - dot, e < E4 ? a[e] : 0.f);
-        if (!score.softmax()) l[j] *= rest[j];
-      }
-      if (d_gates != nullptr) {
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < KI; ++i)
-          if (id[i] >= 0) a[id[i]] = 0.f;
-        __syncwarp();
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < N; ++j) l[j] = 0.f;
+      store_row<T, N, VEC>(drow, d.E, lane, l);
+      live = next_live;
     }
-    store_row<T, N, VEC>(drow, d.E, lane, l);
+    begin = end;
   }
 }
 
@@ -734,7 +823,7 @@ RouterScratch router_scratch(const RouterDims& d, void* ws) {
 // is kept for each device and size of shared memory (the last one asked for): the
 // three questions take longer than a small launch.
 template <auto kernel, int N, int W>
-static cudaError_t blocks_at_once(size_t smem, int64_t* blocks) {
+static cudaError_t blocks_at_once(size_t smem, size_t most, int64_t* blocks) {
   constexpr int kDevices = 64;
   static std::atomic<uint64_t> known[kDevices];  // shared memory, blocks
   int dev = 0;
@@ -746,9 +835,8 @@ static cudaError_t blocks_at_once(size_t smem, int64_t* blocks) {
     *blocks = (uint32_t)k;
     return cudaSuccess;
   }
-  constexpr int most = 32 * N * 4 * (W + 1);  // of the longest row that this kernel takes
   if (most > (32 << 10)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
     if (e != cudaSuccess) return e;
   }
   int sms = 0, per_sm = 0;
@@ -763,9 +851,9 @@ static cudaError_t blocks_at_once(size_t smem, int64_t* blocks) {
 // Launch shape: one round of blocks with equally many tokens: whole rounds of the
 // block's warps, and at most 64 tokens a warp, so that a warp's fp32 sums stay short.
 template <auto kernel, int N, int W>
-static cudaError_t plan_blocks(size_t smem, RouterDims& d) {
+static cudaError_t plan_blocks(size_t smem, size_t most, RouterDims& d) {
   int64_t blocks = 0;
-  const cudaError_t e = blocks_at_once<kernel, N, W>(smem, &blocks);
+  const cudaError_t e = blocks_at_once<kernel, N, W>(smem, most, &blocks);
   if (e != cudaSuccess) return e;
   const int64_t each = ((int64_t)d.T + blocks * W - 1) / (blocks * W);  // tokens a warp
   d.per_block = (int)std::min<int64_t>(each, 64) * W;
@@ -787,8 +875,9 @@ static cudaError_t forward(RouterDims d, const void* logits, const uint8_t* mask
                            int* launches) {
   constexpr int W = router_warps<N>();
   constexpr auto kernel = k_router<T, N, VEC, LOSS, SHORT, KIND>;
-  const size_t smem = LOSS ? (size_t)d.E * 4 * (W + 1) : 0;
-  cudaError_t e = plan_blocks<kernel, N, W>(smem, d);
+  const size_t per_expert = (LOSS ? 4 * (W + 1) : 0) + (rows_ahead<N, VEC>() ? sizeof(T) * W : 0);
+  const size_t smem = d.E * per_expert;
+  cudaError_t e = plan_blocks<kernel, N, W>(smem, 32 * N * per_expert, d);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -876,9 +965,10 @@ struct BackwardCall {
   cudaError_t operator()() const {
     constexpr int W = router_warps<N>();
     constexpr auto kernel = k_router_backward<T, N, VEC, SHORT, KIND>;
-    const size_t smem = (size_t)W * ((d.E + 3) & ~3) * 4;
+    const size_t per_expert = 4 * (W + 1) + (VEC ? sizeof(T) * W : 0);
+    const size_t smem = ((d.E + 3) & ~3) * per_expert;
     RouterDims r = d;
-    const cudaError_t e = plan_blocks<kernel, N, W>(smem, r);
+    const cudaError_t e = plan_blocks<kernel, N, W>(smem, 32 * N * per_expert, r);
     if (e != cudaSuccess) return e;
     kernel<<<r.blocks, W * 32, smem, st>>>(r, (const T*)logits, mask, topk_idx, d_gates, counts,
                                            seg_tokens, d_loss, (T*)d_logits);
