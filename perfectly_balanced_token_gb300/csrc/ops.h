@@ -17,8 +17,7 @@ struct RouterDims {
 // The router's scratch: what is zeroed before a launch comes first.
 struct RouterScratch {
   int32_t* done;          // [1] segments finished
-  int32_t* seg_done;      // [G] blocks finished of each segment
-  int32_t* tokens;        // [G] unmasked tokens
+  unsigned long long* joined;  // [G] blocks finished, above unmasked tokens (32 bits)
   int32_t* bad;           // [G] set where a sum met a value that is not finite
   int32_t* counts;        // [G][E]
   unsigned long long* q;  // [G][E] fixed-point probability sums

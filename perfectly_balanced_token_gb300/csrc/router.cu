@@ -342,6 +342,18 @@ template <int N>
 constexpr int router_blocks() {
   return N <= 8 ? 5 : N <= 16 ? 4 : N <= 32 ? 3 : 1;
 }
+// The same for the router with balance outputs.  A block ends with up to two atomics an
+// expert: for rows of more than 512 all warps of a multiprocessor are one block (65536 x
+// 896: 77 us, in blocks of 8 warps 79.5); for shorter ones that gains 0.6 us at 65536 x
+// 384 (51.8, 52.4) and costs as much on eight tokens.
+template <int N, bool LOSS>
+constexpr int forward_warps() {
+  return LOSS && N > 16 && N <= 32 ? 24 : router_warps<N>();
+}
+template <int N, bool LOSS>
+constexpr int forward_blocks() {
+  return LOSS && N > 16 && N <= 32 ? 1 : router_blocks<N>();
+}
 // Rows of more than 512 keep the warp's probability sums in shared memory: in
 // registers, next to the row, they cost a third of the warps that fit.
 template <int N>
@@ -370,64 +382,50 @@ __device__ __forceinline__ float block_sum(float v, float* s) {
   return threadIdx.x < 32 ? warp_sum(v) : 0.f;
 }
 
-// A block is done with segment g: its warps' probability sums s_q [W][E], counts s_cnt
-// [E] and tokens go to the segment's; the last block of a segment writes the
-// segment's outputs, the last segment the loss.
-template <int W>
-__device__ __forceinline__ void join_blocks(const RouterDims& d, const RouterOut& out,
-                                            const RouterScratch& ws, int g, const float* s_q,
-                                            const int32_t* s_cnt, int& s_tokens, int& s_bad) {
-  __shared__ int s_last;
-  // the blocks that take tokens of this segment
-  const int from = (int)((int64_t)g * d.segment / d.per_block);
-  const int to = (int)((min((int64_t)(g + 1) * d.segment, (int64_t)d.T) - 1) / d.per_block);
-  const bool alone = from == to;
-  if (!alone) {
-    // Joined across blocks as integers (steps of 2^-shift), so the order of the
-    // atomics changes nothing; what is not finite is only noted (q of such a token is
-    // NaN for every expert).
-    const float one = ldexpf(1.f, d.shift);
-    for (int e = threadIdx.x; e < d.E; e += blockDim.x) {
-      float q = 0.f;
-#pragma unroll
-      for (int w = 0; w < W; ++w) q += s_q[(size_t)w * d.E + e];
-      if (!isfinite(q)) s_bad = 1;
-      else if (q != 0.f) atomicAdd(&ws.q[(size_t)g * d.E + e], __float2ull_rn(q * one));
-      if (s_cnt[e]) atomicAdd(&ws.counts[(size_t)g * d.E + e], s_cnt[e]);
-    }
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      atomicAdd(&ws.tokens[g], s_tokens);
-      if (s_bad) atomicOr(&ws.bad[g], 1);
-      __threadfence();
-      s_last = atomicAdd(&ws.seg_done[g], 1) == to - from;
-      __threadfence();
-      if (s_last) {
-        s_tokens = __ldcg(&ws.tokens[g]);
-        s_bad = __ldcg(&ws.bad[g]);
-      }
-    }
-    __syncthreads();
-    if (!s_last) return;
-  }
+// An expert's sum over the warps that had a token.
+__device__ __forceinline__ float sum_of_warps(const float* s_q, int E, int e, int warps) {
+  float q = 0.f;
+#pragma unroll 8
+  for (int w = 0; w < warps; ++w) q += s_q[(size_t)w * E + e];
+  return q;
+}
 
-  // the segment's outputs and its part of the loss
+// A block's part of a segment that several blocks share: its warps' probability sums
+// s_q [warps][E] and counts s_cnt [E] are added to the segment's as integers (steps of
+// 2^-shift), so the order of the atomics changes nothing; what is not finite is only
+// noted (q of such a token is NaN for every expert).
+__device__ __forceinline__ void add_to_segment(const RouterDims& d, const RouterScratch& ws, int g,
+                                               const float* s_q, const int32_t* s_cnt, int warps) {
+  const float one = ldexpf(1.f, d.shift);
+  for (int e = threadIdx.x; e < d.E; e += blockDim.x) {
+    const float q = sum_of_warps(s_q, d.E, e, warps);
+    if (!isfinite(q)) atomicOr(&ws.bad[g], 1);
+    else if (q != 0.f) atomicAdd(&ws.q[(size_t)g * d.E + e], __float2ull_rn(q * one));
+    if (s_cnt[e]) atomicAdd(&ws.counts[(size_t)g * d.E + e], s_cnt[e]);
+  }
+}
+
+// The outputs of a segment of `tokens` tokens and its part of the loss, from the block's
+// own sums (ALONE) or the joined ones.  All threads.
+template <bool ALONE>
+__device__ __forceinline__ void finish_segment(const RouterDims& d, const RouterOut& out,
+                                               const RouterScratch& ws, int g, int tokens,
+                                               const float* s_q = nullptr,
+                                               const int32_t* s_cnt = nullptr, int warps = 0) {
   __shared__ float s_red[32];
   const float step = ldexpf(1.f, -d.shift);
+  const bool bad = !ALONE && __ldcg(&ws.bad[g]);
   float part = 0.f;
   for (int e = threadIdx.x; e < d.E; e += blockDim.x) {
     const size_t at = (size_t)g * d.E + e;
     int32_t c;
     float q;
-    if (alone) {
-      q = 0.f;
-#pragma unroll
-      for (int w = 0; w < W; ++w) q += s_q[(size_t)w * d.E + e];
+    if constexpr (ALONE) {
+      q = sum_of_warps(s_q, d.E, e, warps);
       c = s_cnt[e];
     } else {
       c = __ldcg(&ws.counts[at]);
-      q = s_bad ? NAN : __ull2float_rn(__ldcg(&ws.q[at])) * step;
+      q = bad ? NAN : __ull2float_rn(__ldcg(&ws.q[at])) * step;
     }
     out.counts[at] = c;
     out.prob_sum[at] = q;
@@ -435,21 +433,51 @@ __device__ __forceinline__ void join_blocks(const RouterDims& d, const RouterOut
   }
   part = block_sum(part, s_red);
   if (threadIdx.x == 0) {
-    const float n = (float)s_tokens;
-    const float seg = s_tokens ? part / n * ((float)d.E / ((float)d.K * n)) : 0.f;
-    out.seg_tokens[g] = s_tokens;
-    if (d.G > 1) {
-      ws.seg_loss[g] = seg;
-      __threadfence();
-      s_last = atomicAdd(ws.done, 1) == d.G - 1;
-      __threadfence();
-    } else {
-      *out.loss = seg;
-    }
+    const float n = (float)tokens;
+    const float seg = tokens ? part / n * ((float)d.E / ((float)d.K * n)) : 0.f;
+    out.seg_tokens[g] = tokens;
+    *(d.G > 1 ? &ws.seg_loss[g] : out.loss) = seg;
   }
-  if (d.G == 1) return;
   __syncthreads();
-  if (!s_last) return;
+}
+
+// A block's end.  Its `joined` (0 to 2) segments shared with other blocks are told off;
+// the last block of a segment writes its outputs, and the block that finishes the last
+// segment the loss.  `finished`: segments that this block has had to itself.
+__device__ __forceinline__ void join_blocks(const RouterDims& d, const RouterOut& out,
+                                            const RouterScratch& ws, int first_seg, int last_seg,
+                                            int joined, int* s_tokens, int finished) {
+  __shared__ int s_last[2];
+  if (joined) {
+    // (the barrier before this orders the block's additions before these fences)
+    if ((int)threadIdx.x < joined) {
+      const int g = threadIdx.x ? last_seg : first_seg;
+      const int from = (int)((int64_t)g * d.segment / d.per_block);
+      const int to = (int)((min((int64_t)(g + 1) * d.segment, (int64_t)d.T) - 1) / d.per_block);
+      __threadfence();
+      // the blocks so far above the tokens so far
+      const unsigned long long before =
+          atomicAdd(&ws.joined[g], 1ull << 32 | (uint32_t)s_tokens[threadIdx.x]);
+      __threadfence();
+      s_last[threadIdx.x] = (int)(before >> 32) == to - from;
+      s_tokens[threadIdx.x] += (int)(uint32_t)before;
+    }
+    __syncthreads();
+    for (int i = 0; i < joined; ++i)
+      if (s_last[i]) {
+        finish_segment<false>(d, out, ws, i ? last_seg : first_seg, s_tokens[i]);
+        ++finished;
+      }
+  }
+  if (d.G == 1 || finished == 0) return;
+  if (threadIdx.x == 0) {
+    __threadfence();
+    s_last[0] = atomicAdd(ws.done, finished) + finished == d.G;
+    __threadfence();
+  }
+  __syncthreads();
+  if (!s_last[0]) return;
+  __shared__ float s_red[32];
   float mean = 0.f;
   for (int i = threadIdx.x; i < d.G; i += blockDim.x) mean += __ldcg(&ws.seg_loss[i]);
   mean = block_sum(mean, s_red);
@@ -459,10 +487,10 @@ __device__ __forceinline__ void join_blocks(const RouterDims& d, const RouterOut
 // A block takes per_block consecutive tokens, a warp every W-th of them; with the
 // loss, segment by segment.  SHORT: K <= 32.
 template <typename T, int N, bool VEC, bool LOSS, bool SHORT, int KIND>
-__global__ void __launch_bounds__(router_warps<N>() * 32, router_blocks<N>())
+__global__ void __launch_bounds__(forward_warps<N, LOSS>() * 32, forward_blocks<N, LOSS>())
 k_router(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__ mask,
          RouterOut out, RouterScratch ws) {
-  constexpr int W = router_warps<N>();
+  constexpr int W = forward_warps<N, LOSS>();
   constexpr bool kSmemSums = LOSS && sums_in_smem<N>(), kRegSums = LOSS && !kSmemSums;
   constexpr bool kAhead = rows_ahead<N, VEC>();
   constexpr int KI = SHORT ? 1 : kRouterMaxK / 32;
@@ -470,12 +498,13 @@ k_router(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__
   __shared__ unsigned long long s_list[SHORT ? 1 : W][kRouterMaxK];
   // LOSS: the warps' sums [W][E], then counts [E]; rows ahead: the warps' [W][E]
   extern __shared__ __align__(16) float s_dyn[];
-  __shared__ int s_tokens, s_bad;
+  __shared__ int s_tokens[2];  // of the shared segments, and of the one at work
   int32_t* s_cnt = reinterpret_cast<int32_t*>(s_dyn + (size_t)W * d.E);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   T* s_row = reinterpret_cast<T*>(s_dyn + (LOSS ? (size_t)(W + 1) * d.E : 0)) + (size_t)warp * d.E;
   const uint32_t keep = sort_directions(lane);
   float guess = -INFINITY;
+  int joined = 0, finished = 0, first_seg = 0, last_seg = 0;
 
   const int first = blockIdx.x * d.per_block;
   const int last = min(first + d.per_block, d.T);
@@ -494,7 +523,7 @@ k_router(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__
           if (place<N, VEC>(j, lane) < d.E) sums[place<N, VEC>(j, lane)] = 0.f;
       }
       for (int e = threadIdx.x; e < d.E; e += blockDim.x) s_cnt[e] = 0;
-      if (threadIdx.x == 0) s_tokens = s_bad = 0;
+      if (threadIdx.x == 0) s_tokens[joined] = 0;
       __syncthreads();
     }
 
@@ -607,13 +636,29 @@ k_router(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__
         for (int j = 0; j < N; ++j)
           if (place<N, VEC>(j, lane) < d.E) sums[place<N, VEC>(j, lane)] = acc[j];
       }
-      if (lane == 0) atomicAdd(&s_tokens, live_tokens);
+      if (lane == 0) atomicAdd(&s_tokens[joined], live_tokens);
       __syncthreads();
-      cudaGridDependencySynchronize();  // the scratch is zero
-      join_blocks<W>(d, out, ws, g, s_dyn, s_cnt, s_tokens, s_bad);
+      // A segment with a token in another block: at most the block's first one and its
+      // last.  Only the additions are made here, and waited for at the block's end
+      // (waiting for them twice in a block: 1.1 us more at 65536 x 896).
+      const bool alone = first <= (int64_t)g * d.segment &&
+                         min((int64_t)(g + 1) * d.segment, (int64_t)d.T) <= (int64_t)first + d.per_block;
+      if (alone) {
+        finish_segment<true>(d, out, ws, g, s_tokens[joined], s_dyn, s_cnt, min(W, end - begin));
+        ++finished;
+      } else {
+        cudaGridDependencySynchronize();  // the scratch is zero
+        add_to_segment(d, ws, g, s_dyn, s_cnt, min(W, end - begin));
+        *(joined ? &last_seg : &first_seg) = g;
+        ++joined;
+      }
       __syncthreads();  // the next segment uses the sums' memory
     }
     begin = end;
+  }
+  if constexpr (LOSS) {
+    cudaGridDependencySynchronize();
+    join_blocks(d, out, ws, first_seg, last_seg, joined, s_tokens, finished);
   }
 }
 
@@ -808,8 +853,7 @@ RouterScratch router_scratch(const RouterDims& d, void* ws) {
   RouterScratch r{};
   const size_t G = d.G, GE = (size_t)d.G * d.E;
   r.done = (int32_t*)take(4);
-  r.seg_done = (int32_t*)take(4 * G);
-  r.tokens = (int32_t*)take(4 * G);
+  r.joined = (unsigned long long*)take(8 * G);
   r.bad = (int32_t*)take(4 * G);
   r.counts = (int32_t*)take(4 * GE);
   r.q = (unsigned long long*)take(8 * GE);
@@ -873,7 +917,7 @@ template <typename T, int N, bool VEC, bool LOSS, bool SHORT, int KIND>
 static cudaError_t forward(RouterDims d, const void* logits, const uint8_t* mask,
                            const RouterOut& out, const RouterScratch& ws, cudaStream_t st,
                            int* launches) {
-  constexpr int W = router_warps<N>();
+  constexpr int W = forward_warps<N, LOSS>();
   constexpr auto kernel = k_router<T, N, VEC, LOSS, SHORT, KIND>;
   const size_t per_expert = (LOSS ? 4 * (W + 1) : 0) + (rows_ahead<N, VEC>() ? sizeof(T) * W : 0);
   const size_t smem = d.E * per_expert;
