@@ -16,7 +16,7 @@ struct RouterDims {
 
 // The router's scratch: what is zeroed before a launch comes first.
 struct RouterScratch {
-  int32_t* done;          // [1] segments finished
+  unsigned long long* done;    // [1] segments finished
   unsigned long long* joined;  // [G] blocks finished, above unmasked tokens (32 bits)
   int32_t* bad;           // [G] set where a sum met a value that is not finite
   int32_t* counts;        // [G][E]

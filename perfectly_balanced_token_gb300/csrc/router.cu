@@ -441,6 +441,15 @@ __device__ __forceinline__ void finish_segment(const RouterDims& d, const Router
   __syncthreads();
 }
 
+// Adds to a counter of the GPU, after all that this thread has written or, over a
+// barrier, has seen written; what other threads wrote before theirs is seen after it.
+__device__ __forceinline__ unsigned long long add_in_order(unsigned long long* at,
+                                                           unsigned long long v) {
+  unsigned long long before;
+  asm volatile("atom.acq_rel.gpu.global.add.u64 %0, [%1], %2;" : "=l"(before) : "l"(at), "l"(v) : "memory");
+  return before;
+}
+
 // A block's end.  Its `joined` (0 to 2) segments shared with other blocks are told off;
 // the last block of a segment writes its outputs, and the block that finishes the last
 // segment the loss.  `finished`: segments that this block has had to itself.
@@ -449,16 +458,14 @@ __device__ __forceinline__ void join_blocks(const RouterDims& d, const RouterOut
                                             int joined, int* s_tokens, int finished) {
   __shared__ int s_last[2];
   if (joined) {
-    // (the barrier before this orders the block's additions before these fences)
+    // (the barrier before this orders the block's additions before these)
     if ((int)threadIdx.x < joined) {
       const int g = threadIdx.x ? last_seg : first_seg;
       const int from = (int)((int64_t)g * d.segment / d.per_block);
       const int to = (int)((min((int64_t)(g + 1) * d.segment, (int64_t)d.T) - 1) / d.per_block);
-      __threadfence();
       // the blocks so far above the tokens so far
       const unsigned long long before =
-          atomicAdd(&ws.joined[g], 1ull << 32 | (uint32_t)s_tokens[threadIdx.x]);
-      __threadfence();
+          add_in_order(&ws.joined[g], 1ull << 32 | (uint32_t)s_tokens[threadIdx.x]);
       s_last[threadIdx.x] = (int)(before >> 32) == to - from;
       s_tokens[threadIdx.x] += (int)(uint32_t)before;
     }
@@ -471,9 +478,7 @@ __device__ __forceinline__ void join_blocks(const RouterDims& d, const RouterOut
   }
   if (d.G == 1 || finished == 0) return;
   if (threadIdx.x == 0) {
-    __threadfence();
-    s_last[0] = atomicAdd(ws.done, finished) + finished == d.G;
-    __threadfence();
+    s_last[0] = (int)add_in_order(ws.done, finished) + finished == d.G;
   }
   __syncthreads();
   if (!s_last[0]) return;
@@ -852,7 +857,7 @@ RouterScratch router_scratch(const RouterDims& d, void* ws) {
   };
   RouterScratch r{};
   const size_t G = d.G, GE = (size_t)d.G * d.E;
-  r.done = (int32_t*)take(4);
+  r.done = (unsigned long long*)take(8);
   r.joined = (unsigned long long*)take(8 * G);
   r.bad = (int32_t*)take(4 * G);
   r.counts = (int32_t*)take(4 * GE);
