@@ -85,6 +85,83 @@ __device__ __forceinline__ void load_row(const T* row, int E, int lane, float (&
   }
 }
 
+// A row as choosing sees it: its values, the largest of this lane's (NaN passed over),
+// a bit for each that reaches a bound, and the expert that a bit stands for.
+template <typename T, int N, bool VEC>
+struct Row {
+  static constexpr int kWords = (N + 31) / 32;
+  float l[N];
+  __device__ __forceinline__ void load(const T* row, int E, int lane) {
+    load_row<T, N, VEC>(row, E, lane, l);
+  }
+  __device__ __forceinline__ float operator()(int j) const { return l[j]; }
+  __device__ __forceinline__ float most() const {
+    float m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < N; ++j) m = fmaxf(m, l[j]);
+    return m;
+  }
+  __device__ __forceinline__ bool nan() const {
+    bool n = false;
+#pragma unroll
+    for (int j = 0; j < N; ++j) n |= l[j] != l[j];
+    return n;
+  }
+  __device__ __forceinline__ void reach(float bound, uint32_t (&bits)[kWords]) const {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (l[j] >= bound) bits[j / 32] |= 1u << (j & 31);
+  }
+  __device__ __forceinline__ static int expert(int word, int bit, int lane) {
+    return place<N, VEC>(word * 32 + bit, lane);
+  }
+};
+// bf16 vectors stay as they are, two values a register: an instruction takes both
+// (bits p and p + 16 for pair p).
+template <int N>
+struct Row<__nv_bfloat16, N, true> {
+  static constexpr int kWords = 1;
+  static_assert(N % 4 == 0 && N <= 32);
+  uint32_t pair[N / 2];
+  __device__ __forceinline__ void load(const __nv_bfloat16* row, int E, int lane) {
+#pragma unroll
+    for (int c = 0; c < N / 4; ++c) {
+      uint2 u = make_uint2(0xff80ff80u, 0xff80ff80u);  // -inf
+      if (inside<N, true>(c, lane, E)) u = *reinterpret_cast<const uint2*>(row + c * 128 + lane * 4);
+      pair[2 * c] = u.x, pair[2 * c + 1] = u.y;
+    }
+  }
+  __device__ __forceinline__ static __nv_bfloat162 both(uint32_t u) {
+    return *reinterpret_cast<const __nv_bfloat162*>(&u);
+  }
+  __device__ __forceinline__ float operator()(int j) const {
+    const uint32_t u = pair[j >> 1];
+    return __uint_as_float(j & 1 ? u & 0xffff0000u : u << 16);
+  }
+  __device__ __forceinline__ float most() const {
+    __nv_bfloat162 m = both(pair[0]);
+#pragma unroll
+    for (int p = 1; p < N / 2; ++p) m = __hmax2(m, both(pair[p]));
+    const float a = __low2float(m), b = __high2float(m);
+    return fmaxf(fmaxf(a, b), -INFINITY);
+  }
+  __device__ __forceinline__ bool nan() const {
+    unsigned n = 0;
+#pragma unroll
+    for (int p = 0; p < N / 2; ++p) n |= __hneu2_mask(both(pair[p]), both(pair[p]));
+    return n != 0;
+  }
+  __device__ __forceinline__ void reach(float bound, uint32_t (&bits)[1]) const {
+    const __nv_bfloat162 b = __bfloat162bfloat162(__float2bfloat16_ru(bound));
+#pragma unroll
+    for (int p = 0; p < N / 2; ++p) bits[0] |= __hge2_mask(both(pair[p]), b) & (0x00010001u << p);
+  }
+  __device__ __forceinline__ static int expert(int, int bit, int lane) {
+    const int p = bit & 15;
+    return (p >> 1) * 128 + lane * 4 + (p & 1) * 2 + (bit >> 4);
+  }
+};
+
 template <typename T, int N, bool VEC>
 __device__ __forceinline__ void store_row(T* __restrict__ row, int E, int lane,
                                           const float (&l)[N]) {
@@ -183,8 +260,9 @@ struct Scores {
 // The K largest of a token, one after the other; f(k, logit, expert) for each.
 // (Compared as logits and experts, not as keys: keys of a whole row would be kept
 // in registers through the kernel.)
-template <int N, bool VEC, typename F>
-__device__ __forceinline__ void select_in_turn(const float (&l)[N], int E, int K, int lane, F&& f) {
+template <typename T, int N, bool VEC, typename F>
+__device__ __forceinline__ void select_in_turn(const Row<T, N, VEC>& l, int E, int K, int lane,
+                                               F&& f) {
   float last = INFINITY;
   int last_e = -1;
   bool nans = false;  // all that is left is NaN
@@ -196,8 +274,9 @@ __device__ __forceinline__ void select_in_turn(const float (&l)[N], int E, int K
     for (int j = 0; j < N; ++j) {
       const int e = place<N, VEC>(j, lane);
       const bool later = e > last_e;
-      const bool left = nans ? (l[j] != l[j] && later) : (l[j] < last || (l[j] == last && later));
-      if (left && e < E && (best_e == 0x7fffffff || l[j] > best)) best = l[j], best_e = e;
+      const float v = l(j);
+      const bool left = nans ? (v != v && later) : (v < last || (v == last && later));
+      if (left && e < E && (best_e == 0x7fffffff || v > best)) best = v, best_e = e;
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
@@ -241,11 +320,11 @@ struct __align__(16) Candidates {
 // in on.  What no bound tells apart (ties) and a bound of -inf (which the places past
 // the row's end reach too) take the K largest one after the other.
 template <typename T, int N, bool VEC>
-__device__ __forceinline__ void select_top(const float (&l)[N], const T* row, int E, int K,
+__device__ __forceinline__ void select_top(const Row<T, N, VEC>& l, const T* row, int E, int K,
                                            int lane, float most, float m, uint32_t keep,
                                            float& guess, Candidates& list, int& rank, float& value,
                                            int& expert) {
-  constexpr int NW = (N + 31) / 32;
+  constexpr int NW = Row<T, N, VEC>::kWords;
   rank = 32;
   value = 0.f, expert = 0;
   const float target = (float)min(K + 8, (K + 30) / 2);
@@ -256,9 +335,7 @@ __device__ __forceinline__ void select_top(const float (&l)[N], const T* row, in
 #pragma unroll 1
   for (int tries = 0; tries < 8 && bound > -INFINITY; ++tries) {
     uint32_t reach[NW] = {};
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-      if (l[j] >= bound) reach[j / 32] |= 1u << (j & 31);
+    l.reach(bound, reach);
     int mine = 0;
 #pragma unroll
     for (int w = 0; w < NW; ++w) mine += __popc(reach[w]);
@@ -291,7 +368,7 @@ __device__ __forceinline__ void select_top(const float (&l)[N], const T* row, in
       while (const unsigned who = __ballot_sync(kAll, reach[w] != 0)) {
         if (reach[w])
           list.expert[base + __popc(who & ((1u << lane) - 1u))] =
-              place<N, VEC>(w * 32 + __ffs(reach[w]) - 1, lane);
+              Row<T, N, VEC>::expert(w, __ffs(reach[w]) - 1, lane);
         reach[w] &= reach[w] - 1;
         base += __popc(who);
       }
@@ -325,7 +402,7 @@ __device__ __forceinline__ void select_top(const float (&l)[N], const T* row, in
     if (lane < total) rank = r;
     return;
   }
-  select_in_turn<N, VEC>(l, E, K, lane, [&](int k, float v, int e) {
+  select_in_turn<T, N, VEC>(l, E, K, lane, [&](int k, float v, int e) {
     if (lane == k) value = v, expert = e, rank = k;
   });
 }
@@ -535,14 +612,12 @@ k_router(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__
     if (kAhead && begin + warp < end)
       fetch_row<T, N>(s_row, logits + (size_t)(begin + warp) * d.E, d.E, lane);
     for (int t = begin + warp; t < end; t += W) {
-      float l[N];
+      Row<T, N, VEC> logit;
       const T* row = kAhead ? s_row : logits + (size_t)t * d.E;
       if constexpr (kAhead) await_row();
-      load_row<T, N, VEC>(row, d.E, lane, l);
+      logit.load(row, d.E, lane);
       const bool live = mask == nullptr || mask[t] != 0;
-      float most = -INFINITY;
-#pragma unroll
-      for (int j = 0; j < N; ++j) most = fmaxf(most, l[j]);  // passes NaN over
+      const float most = logit.most();
       const float m = warp_max(most);
       const Scores<KIND> score(d.score, m);
 
@@ -550,10 +625,10 @@ k_router(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__
       float value[KI];
       int expert[KI], rank[KI];
       if constexpr (SHORT) {
-        select_top<T, N, VEC>(l, row, d.E, d.K, lane, most, m, keep, guess, s_cand[warp],
+        select_top<T, N, VEC>(logit, row, d.E, d.K, lane, most, m, keep, guess, s_cand[warp],
                               rank[0], value[0], expert[0]);
       } else {
-        select_in_turn<N, VEC>(l, d.E, d.K, lane, [&](int k, float v, int e) {
+        select_in_turn<T, N, VEC>(logit, d.E, d.K, lane, [&](int k, float v, int e) {
           if (lane == 0)
             s_list[warp][k] = ((unsigned long long)__float_as_uint(v) << 32) | (uint32_t)e;
         });
@@ -575,19 +650,19 @@ k_router(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__
       // every softmax score, shows in it
       float inv = 1.f;
       bool nan = score.softmax() && m == INFINITY;
+      float l[N];
       if (LOSS || (score.softmax() && !d.normalise)) {
         float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-          l[j] = score(l[j]);
+          l[j] = score(logit(j));
           sum += l[j];
         }
         sum = warp_sum(sum);
         inv = sum == 0.f ? 0.f : fast_rcp(sum);
         nan |= score.softmax() && sum != sum;
       } else if (score.softmax()) {
-#pragma unroll
-        for (int j = 0; j < N; ++j) nan |= l[j] != l[j];
+        nan |= logit.nan();
       }
       if (LOSS && live) {
         ++live_tokens;
