@@ -339,3 +339,57 @@ def test_gradient_against_differences_on_the_gpu():
             seen += 1
             assert abs((a - b) / (2 * h) - float(got[t, e])) <= 6 * RTOL / (2 * h) + 10 * h * h
     assert seen > T * E // 2
+
+
+# Several tokens a warp, blocks with whole segments and parts of others, and rows that
+# lie in vectors, short and long.
+@pytest.mark.parametrize("T,E,K,segment", [(2000, 896, 16, 7), (2000, 896, 16, 24),
+                                           (5000, 640, 8, 37), (12000, 516, 6, 1000),
+                                           (16000, 384, 8, 900)])
+@pytest.mark.parametrize("score,dtype", [("sigmoid", torch.bfloat16), ("softmax", torch.float32)])
+def test_many_tokens_and_segment_borders(T, E, K, segment, score, dtype):
+    rd = mx.router_dims(T, E, K, segment, score, True, 1.5, dtype)
+    logits = draw(T, E, T + segment, dtype)
+    live = np.random.default_rng(E).random(T) > 0.2
+    fwd = check(rd, logits, live.astype(np.uint8), score)
+    dg = np.random.default_rng(K).standard_normal((T, K)).astype(np.float32)
+    dl = float(T)
+    got = torch.full((T, E), 7.0, dtype=dtype, device="cuda")
+    cuda = {k: torch.from_numpy(fwd[k]).cuda() for k in ("topk_idx", "counts", "seg_tokens")}
+    mx.moonep_router_backward(rd, logits.cuda(), cuda["topk_idx"], got,
+                              token_mask=torch.from_numpy(live.astype(np.uint8)).cuda(),
+                              d_gates=torch.from_numpy(dg).cuda(), counts=cuda["counts"],
+                              seg_tokens=cuda["seg_tokens"],
+                              d_loss=torch.tensor([dl], device="cuda"))
+    want, size = ops.router_backward(logits.double().numpy(), fwd["topk_idx"], segment, score, True,
+                                     1.5, live, dg, dl)
+    tol = 3 * RTOL * size + 1e-12 + (2.0 ** -8 * np.abs(want) if dtype == torch.bfloat16 else 0)
+    err = np.abs(got.double().cpu().numpy() - want)
+    assert (err <= tol).all(), (err.max(), (err / tol).max())
+    assert not got[torch.from_numpy(~live).cuda()].any()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [24, 384, 900])
+def test_bf16_rows_of_infinities_nan_and_ties(score, E):
+    T, K = 14, 6
+    l = draw(T, E, 6, torch.bfloat16)
+    l[1] = -np.inf
+    l[3, 4] = np.nan
+    l[4] = np.nan
+    l[5] = -np.inf
+    l[5, 7] = np.nan
+    l[6] = torch.finfo(torch.bfloat16).min
+    l[7] = torch.finfo(torch.bfloat16).max
+    l[8, 2] = torch.finfo(torch.bfloat16).max
+    l[9] = torch.finfo(torch.bfloat16).tiny
+    l[10, E - 3:] = 7.0
+    l[11] = 2.0 ** -133
+    l[11, 5] = 0.0
+    l[11, 9] = 2 * 2.0 ** -133
+    check(mx.router_dims(T, E, K, 4, score, True, 1.0, torch.bfloat16), l, score=score)
+    rd = mx.router_dims(50, E, K, 0, score, True, 1.0, torch.bfloat16)
+    check(rd, draw(50, E, 1, torch.bfloat16, ties=True), score=score)
+    check(rd, torch.zeros(50, E, dtype=torch.bfloat16), score=score)
+    check(rd, draw(50, E, 2, torch.bfloat16, off=E // 2), score=score)
+    check(rd, draw(50, E, 3, torch.bfloat16, off=E - 3), score=score)
