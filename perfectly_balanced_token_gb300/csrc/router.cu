@@ -533,7 +533,8 @@ __device__ __forceinline__ unsigned long long add_in_order(unsigned long long* a
 __device__ __forceinline__ void join_blocks(const RouterDims& d, const RouterOut& out,
                                             const RouterScratch& ws, int first_seg, int last_seg,
                                             int joined, int* s_tokens, int finished) {
-  __shared__ int s_last[2];
+  // (s_all is a word of its own: a warp may still be reading s_last when thread 0 writes it)
+  __shared__ int s_last[2], s_all;
   if (joined) {
     // (the barrier before this orders the block's additions before these)
     if ((int)threadIdx.x < joined) {
@@ -555,10 +556,10 @@ __device__ __forceinline__ void join_blocks(const RouterDims& d, const RouterOut
   }
   if (d.G == 1 || finished == 0) return;
   if (threadIdx.x == 0) {
-    s_last[0] = (int)add_in_order(ws.done, finished) + finished == d.G;
+    s_all = (int)add_in_order(ws.done, finished) + finished == d.G;
   }
   __syncthreads();
-  if (!s_last[0]) return;
+  if (!s_all) return;
   __shared__ float s_red[32];
   float mean = 0.f;
   for (int i = threadIdx.x; i < d.G; i += blockDim.x) mean += __ldcg(&ws.seg_loss[i]);

@@ -393,3 +393,27 @@ def test_bf16_rows_of_infinities_nan_and_ties(score, E):
     check(rd, torch.zeros(50, E, dtype=torch.bfloat16), score=score)
     check(rd, draw(50, E, 2, torch.bfloat16, off=E // 2), score=score)
     check(rd, draw(50, E, 3, torch.bfloat16, off=E - 3), score=score)
+
+
+# Blocks that have several short segments to themselves and share their first and last one
+# with a neighbour: whole segments, joins and the last block's loss in the same block.
+@pytest.mark.parametrize("E,K,score,dtype", [(384, 8, "softmax", torch.float32),
+                                             (896, 16, "sigmoid", torch.bfloat16),
+                                             (64, 4, "softmax", torch.float32)])
+@pytest.mark.parametrize("segment", [5, 37])
+def test_short_segments_launch_after_launch(E, K, score, dtype, segment):
+    T = 20000
+    rd = mx.router_dims(T, E, K, segment, score, True, 1.0, dtype)
+    l = draw(T, E, 13, dtype)
+    check(rd, l, score=score)
+    l = l.cuda()
+    want = forward(rd, l)
+    got = {k: torch.zeros_like(v) for k, v in want.items()}
+    ws = torch.empty(mx.moonep_router_workspace_bytes(rd), dtype=torch.uint8, device="cuda")
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(300):
+        mx.moonep_router_forward(rd, l, got["topk_idx"], got["gates"], ws=ws,
+                                 **{k: got[k] for k in ("counts", "prob_sum", "seg_tokens", "loss")})
+        for k in want:
+            differ += (got[k] != want[k]).any()
+    assert int(differ) == 0
