@@ -77,7 +77,8 @@ int moonep_router_forward(const moonep_router_dims* dims, const void* logits,
  * counts and seg_tokens as the forward pass wrote them (an id outside [0, E)
  * contributes nothing).  d_gates fp32 [T][K] or NULL; counts, seg_tokens and
  * d_loss (fp32 [1] on the device, 4-byte aligned) all given or all NULL; at
- * least one of the two gradients is given. */
+ * least one of the two gradients is given.  Sigmoid without d_loss: a token's
+ * gradient depends on its chosen logits alone, whatever the others hold. */
 int moonep_router_backward(const moonep_router_dims* dims, const void* logits,
                            const uint8_t* token_mask, const int32_t* topk_idx,
                            const float* d_gates, const int32_t* counts,

@@ -123,6 +123,10 @@ def router_backward(logits, ids, segment, kind, normalise, scale, live, d_gates,
             grad[t] = s[t] * (1 - s[t]) * (ds + inner)
             size[t] = s[t] * (1 - s[t]) * (np.abs(ds) + np.abs(w) / max(total, 1e-300)
                                            + (q[t] * np.abs(w)).sum() / max(total, 1e-300))
+            if not d_loss:  # the gates are functions of the chosen logits alone
+                chosen = np.isin(np.arange(E), ids[t])
+                grad[t] = np.where(chosen, s[t] * (1 - s[t]) * ds, 0.0)
+                size[t] = np.where(chosen, s[t] * (1 - s[t]) * np.abs(ds), 0.0)
         if d_gates is not None and normalise:  # what cancels inside a normalised gate's gradient
             sk = s[t, ids[t]]
             n = sk / sk.sum() if sk.sum() else sk

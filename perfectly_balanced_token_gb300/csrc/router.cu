@@ -755,6 +755,7 @@ k_router(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__
 //   sigmoid:  dl_e = (1 - s_e) (q_e (w_e - dot) + a_e)
 //   a_k = scale n_k (d_gate_k - sum_j n_j d_gate_j), n = chosen s / their sum, when
 //   normalised; else scale s_k d_gate_k
+// (sigmoid without the loss, w = 0: dl_e = (1 - s_e) a_e, and 0 where e is not chosen)
 // The chosen experts' a lie in a row of shared memory that is zero elsewhere; w, one for
 // a segment, lies there too, as three rows in registers left a third of the warps.
 //
@@ -844,10 +845,14 @@ k_router_backward(RouterDims d, const T* __restrict__ logits, const uint8_t* __r
         // the scores (up to their common factor), their sum and that with w.  A
         // sigmoid's place keeps the smaller of s and 1 - s without cancellation (where
         // that is 1 - s, l > 0, the factor is 1): the other follows, and their product
-        // is all that the gradient needs
+        // is all that the gradient needs.
+        // A sigmoid's gates without the loss depend on the chosen logits alone: the row's
+        // sums are left out, with what a NaN at another expert would make of them
+        const bool row_sums = score.softmax() || d_loss != nullptr;
         float sum = 0.f, dot = 0.f;
 #pragma unroll
         for (int c = 0; c < N / V; ++c) {
+          if (!row_sums) break;
           const int at = place<N, VEC>(c * V, lane);
           float wv[V] = {};
           if (inside<N, VEC>(c, lane, d.E)) values(w + at, wv);
@@ -910,7 +915,7 @@ k_router_backward(RouterDims d, const T* __restrict__ logits, const uint8_t* __r
           for (int i = 0; i < V; ++i) {
             float& v = l[c * V + i];
             if (!score.softmax()) v *= fmaf(-v, score.one, 1.f);
-            v = fmaf(v, fmaf(wv[i], inv, -dot_inv), av[i]);
+            v = row_sums ? fmaf(v, fmaf(wv[i], inv, -dot_inv), av[i]) : av[i];
           }
         }
         if (d_gates != nullptr) {

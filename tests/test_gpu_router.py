@@ -308,6 +308,59 @@ def test_backward_of_rows_without_weight():
         assert torch.isfinite(got).all() and not got[2].any()
 
 
+# Rows with NaN and infinities at chosen and at unchosen experts: NaN where the formula has it
+# (sigmoid gates without the loss depend on the chosen logits alone) and nowhere else.
+@pytest.mark.parametrize("E,K,dtype", [(24, 6, torch.float32), (71, 5, torch.bfloat16),
+                                       (384, 8, torch.float32), (896, 16, torch.bfloat16),
+                                       (1500, 10, torch.float32), (64, 40, torch.float32)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("normalise", [True, False])
+@pytest.mark.parametrize("parts", ["both", "gates", "loss"])
+def test_backward_of_rows_of_infinities_and_nan(E, K, dtype, score, normalise, parts):
+    T = 16
+    l = draw(T, E, 15, dtype)
+    top = l[:, :].float().argsort(1, descending=True)
+    l[1, top[1, E - 1]] = np.nan            # never chosen
+    l[2, top[2, [K + 1, E - 2]]] = np.nan   # just below the chosen ones
+    l[3] = np.nan
+    l[4] = np.nan
+    l[4, 7] = 1.0                           # NaN among the chosen
+    l[5, : E - K + 1] = np.nan              # one chosen NaN
+    l[6, top[6, 0]] = np.inf                # chosen
+    l[7, top[7, : K + 1]] = np.inf          # one of them not chosen
+    l[8, top[8, E // 2:]] = -np.inf
+    l[9] = -np.inf
+    l[9, 3] = 2.0                           # -inf among the chosen
+    l[10] = -np.inf
+    l[10, 5] = np.nan
+    l[11, 0], l[11, E - 1] = np.inf, -np.inf
+    rd = mx.router_dims(T, E, K, 5, score, normalise, 1.5, dtype)
+    live = np.ones(T, bool)
+    live[2] = parts != "both"               # a masked token's gradient is 0, whatever its row holds
+    mask = torch.from_numpy(live.astype(np.uint8)).cuda()
+    fwd = forward(rd, l.cuda(), mask)
+    rng = np.random.default_rng(E)
+    dg = rng.standard_normal((T, K)).astype(np.float32) if parts != "loss" else None
+    dl = 3.0 if parts != "gates" else 0.0
+    extra = {}
+    if dg is not None:
+        extra["d_gates"] = torch.from_numpy(dg).cuda()
+    if dl:
+        extra.update(counts=fwd["counts"], seg_tokens=fwd["seg_tokens"],
+                     d_loss=torch.tensor([dl], device="cuda"))
+    got = torch.full((T, E), 7.0, dtype=dtype, device="cuda")
+    mx.moonep_router_backward(rd, l.cuda(), fwd["topk_idx"], got, token_mask=mask, **extra)
+    with np.errstate(invalid="ignore"):
+        want, size = ops.router_backward(l.double().numpy(), fwd["topk_idx"].cpu().numpy(), 5, score,
+                                         normalise, 1.5, live, dg, dl)
+    got = got.double().cpu().numpy()
+    nan = np.isnan(want)
+    assert np.array_equal(np.isnan(got), nan), np.nonzero((np.isnan(got) != nan).any(1))[0]
+    tol = 3 * RTOL * size + 1e-12 + (2.0 ** -8 * np.abs(want) if dtype == torch.bfloat16 else 0)
+    err = np.abs(got - want)
+    assert (err <= tol)[~nan].all(), err[~nan].max()
+
+
 def test_gradient_against_differences_on_the_gpu():
     """d_logits against differences of the forward pass's own fp32 gates and loss.  Their
     rounding is RTOL of values below 3, so a difference over 2 h is off by 6 RTOL / (2 h),

@@ -72,6 +72,24 @@ def test_gradient_against_differences(kind, normalise):
     assert (np.abs(grad) <= size * (1 + 1e-9)).all()
 
 
+def test_gradient_of_rows_with_nan():
+    # a sigmoid gate depends on its own logit (normalised: on the chosen ones), the loss and
+    # every softmax on the whole row
+    l = np.array([[1.0, np.nan, 2.0, 0.5], [np.nan, 1.0, np.nan, np.nan]])
+    ids = ops.top_k(l, 2)
+    assert ids.tolist() == [[2, 0], [1, 0]]
+    dg = np.array([[1.0, 3.0], [1.0, 3.0]])
+    slope = lambda x: np.exp(-x) / (1 + np.exp(-x)) ** 2  # noqa: E731
+    grad, _ = ops.router_backward(l, ids, 2, "sigmoid", False, 2.0, None, dg, 0.0)
+    assert np.allclose(grad[0], [6 * slope(1.0), 0, 2 * slope(2.0), 0])
+    assert np.allclose(grad[1], [np.nan, 2 * slope(1.0), 0, 0], equal_nan=True)
+    grad, _ = ops.router_backward(l, ids, 2, "sigmoid", True, 2.0, None, dg, 0.0)
+    assert np.isfinite(grad[0]).all() and grad[0][[1, 3]].tolist() == [0, 0] and grad[0][0] > 0
+    assert np.isnan(grad[1][:2]).all() and grad[1][2:].tolist() == [0, 0]
+    for kind, d_loss in (("sigmoid", 1.0), ("softmax", 0.0), ("softmax", 1.0)):
+        assert np.isnan(ops.router_backward(l, ids, 2, kind, True, 2.0, None, dg, d_loss)[0]).all()
+
+
 def test_mxfp4_by_hand():
     x = np.zeros((1, 32))
     # largest 7 = 1.75 2^2: scale 1; ties go to the even code, 7 is cut to 6
