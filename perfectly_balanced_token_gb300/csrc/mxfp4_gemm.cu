@@ -648,8 +648,9 @@ static cudaError_t launch_mx(const Dims& d, const PlanPtrs& p, const MxMaps& m,
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  static int grid = 0;
-  if (grid == 0) {
+  static PerDevice kept;
+  int grid = 0;
+  const cudaError_t e = kept(&grid, [&](int* found) {
     cudaError_t e = cudaFuncSetAttribute(k_mxfp4_gemm<CG>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
     if (e != cudaSuccess) return e;
@@ -657,10 +658,11 @@ static cudaError_t launch_mx(const Dims& d, const PlanPtrs& p, const MxMaps& m,
     if (CG == 2) {  // one CTA pair per co-resident cluster
       cfg.gridDim = dim3(2 * std::max(1, n / 2));
       e = cudaOccupancyMaxActiveClusters(&n, (void*)k_mxfp4_gemm<CG>, &cfg);
-      if (e != cudaSuccess) return e;
     }
-    grid = CG * std::max(1, n);
-  }
+    *found = CG * std::max(1, n);
+    return e;
+  });
+  if (e != cudaSuccess) return e;
   const long long items = (long long)d.max_mtiles * ((d.Hp + kMxBN - 1) / kMxBN);
   if (grid > kMaxGemmCtas) return cudaErrorInvalidConfiguration;  // tensor-map scratch per CTA
   cfg.gridDim = dim3((unsigned)std::min<long long>(grid, CG * items));

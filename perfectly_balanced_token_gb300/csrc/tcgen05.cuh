@@ -5,6 +5,8 @@
 
 #include <cuda.h>
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace moonep {
@@ -393,6 +395,25 @@ inline EncodeTiledFn get_encode() {
   }
   return fn;
 }
+
+// What a launcher finds out (and sets up) once for each device: `find(&value)` gives a
+// positive number for the current one, which is kept once all of it has succeeded there.
+constexpr int kDevices = 64;
+struct PerDevice {
+  std::atomic<int> known[kDevices] = {};
+  template <typename F>
+  cudaError_t operator()(int* value, F&& find) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
+    *value = known[dev].load(std::memory_order_acquire);
+    if (*value > 0) return cudaSuccess;
+    e = find(value);
+    if (e == cudaSuccess) known[dev].store(*value, std::memory_order_release);
+    return e;
+  }
+};
 
 inline int sm_count_gemm() {
   int dev = 0, sms = 0;
