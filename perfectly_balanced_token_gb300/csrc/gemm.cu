@@ -1502,13 +1502,14 @@ static bool encode_2d_f32_tile(CUtensorMap* m, const void* base, uint64_t inner,
 }
 
 template <typename Cfg, typename KernelT, typename... Args>
-static cudaError_t launch_cfg(KernelT kernel, bool& attr_set, int grid, cudaStream_t st,
+static cudaError_t launch_cfg(KernelT kernel, PerDevice& kept, int grid, cudaStream_t st,
                               Args... args) {
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  int set = 0;
+  const cudaError_t e = kept(&set, [&](int* done) {
+    *done = 1;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
+  });
+  if (e != cudaSuccess) return e;
   kernel<<<grid, kGemmThreads, Cfg::kSmem, st>>>(args...);
   return cudaGetLastError();
 }
@@ -1519,7 +1520,7 @@ static cudaError_t launch_bn(const Dims& d, GemmShape sh, const PlanPtrs& p, con
                              cudaStream_t st, int* launches) {
   // With the height left to the plan both variants are launched; the one the
   // plan did not choose returns at once (the choice is only on the device).
-  static bool set128 = false, set256 = false;
+  static PerDevice set128, set256;
   int n = 0;
   if (d.tile_m != 2 * kMmaM) {
     const cudaError_t e = launch_cfg<GemmCfgM128<BN, S128>>(k_ggemm_m128<BN, S128, BKM>, set128,
@@ -1539,7 +1540,7 @@ static cudaError_t launch_bn(const Dims& d, GemmShape sh, const PlanPtrs& p, con
 
 static int pick_bn(int n) { return (n % 256 == 0) ? 256 : (n % 128 == 0 ? 128 : 64); }
 
-static bool set_fwd128 = false, set_dx128 = false;
+static PerDevice set_fwd128, set_dx128;
 
 // The CTA-pair kernel on two CTAs per co-resident cluster.
 template <bool BKM>
@@ -1549,8 +1550,9 @@ static cudaError_t launch_pair_gemm(const Dims& d, GemmShape sh, const PlanPtrs&
   using Cfg = GemmCfgPair<kPairStages>;
   CUtensorMap ty;  // the output as TMA store target, 32-row boxes of 64 columns
   if (!encode_2d(&ty, y, (uint64_t)sh.N, (uint64_t)d.R * d.C, 32)) return cudaErrorInvalidValue;
-  static int grid = 0;
-  if (grid == 0) {
+  static PerDevice kept;
+  int grid = 0;
+  const cudaError_t e = kept(&grid, [&](int* found) {
     cudaError_t e = cudaFuncSetAttribute(k_ggemm_2sm<kPairStages, BKM>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
     if (e != cudaSuccess) return e;
@@ -1560,9 +1562,10 @@ static cudaError_t launch_pair_gemm(const Dims& d, GemmShape sh, const PlanPtrs&
     cfg.dynamicSmemBytes = Cfg::kSmem;
     int ncl = 0;
     e = cudaOccupancyMaxActiveClusters(&ncl, (void*)k_ggemm_2sm<kPairStages, BKM>, &cfg);
-    if (e != cudaSuccess) return e;
-    grid = 2 * std::max(1, ncl);
-  }
+    *found = 2 * std::max(1, ncl);
+    return e;
+  });
+  if (e != cudaSuccess) return e;
   if (grid > kMaxGemmCtas) return cudaErrorInvalidConfiguration;  // tensor-map scratch per CTA
   k_ggemm_2sm<kPairStages, BKM><<<grid, kGemmThreads, Cfg::kSmem, st>>>(a, wh, ws, ty, d, sh, p, y);
   return cudaGetLastError();
@@ -1573,8 +1576,9 @@ static cudaError_t launch_pair_dw(const Dims& d, const PlanPtrs& p, const CUtens
                                   const CUtensorMap& tdy, const CUtensorMap& tgh,
                                   const CUtensorMap& tgs, cudaStream_t st) {
   using Cfg = GemmCfgDWPair<kDwPairStages>;
-  static int grid = 0;
-  if (grid == 0) {
+  static PerDevice kept;
+  int grid = 0;
+  const cudaError_t e = kept(&grid, [&](int* found) {
     cudaError_t e = cudaFuncSetAttribute(k_ggemm_dw_2sm<kDwPairStages>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
     if (e != cudaSuccess) return e;
@@ -1584,9 +1588,10 @@ static cudaError_t launch_pair_dw(const Dims& d, const PlanPtrs& p, const CUtens
     cfg.dynamicSmemBytes = Cfg::kSmem;
     int ncl = 0;
     e = cudaOccupancyMaxActiveClusters(&ncl, (void*)k_ggemm_dw_2sm<kDwPairStages>, &cfg);
-    if (e != cudaSuccess) return e;
-    grid = 2 * std::max(1, ncl);
-  }
+    *found = 2 * std::max(1, ncl);
+    return e;
+  });
+  if (e != cudaSuccess) return e;
   if (grid > kMaxGemmCtas) return cudaErrorInvalidConfiguration;  // tensor-map scratch per CTA
   k_ggemm_dw_2sm<kDwPairStages><<<grid, kGemmThreads, Cfg::kSmem, st>>>(tx, tdy, tgh, tgs, d, p);
   return cudaGetLastError();
@@ -1717,13 +1722,13 @@ cudaError_t launch_grouped_gemm_dw(const Dims& d, const PlanPtrs& p, const void*
   const long long max_items = (long long)d.max_groups * (d.H / kMmaM) * (d.Hp / bn);
   const int grid = (int)std::min<long long>(sm_count_gemm(), std::max<long long>(1, max_items));
   if (bn == 256) {
-    static bool set = false;
+    static PerDevice set;
     e = launch_cfg<GemmCfgDW<256, 4>>(k_ggemm_dw<256, 4>, set, grid, st, tx, tdy, tgh, tgs, tghp, tgsp, d, p);
   } else if (bn == 128) {
-    static bool set = false;
+    static PerDevice set;
     e = launch_cfg<GemmCfgDW<128, 5>>(k_ggemm_dw<128, 5>, set, grid, st, tx, tdy, tgh, tgs, tghp, tgsp, d, p);
   } else {
-    static bool set = false;
+    static PerDevice set;
     e = launch_cfg<GemmCfgDW<64, 7>>(k_ggemm_dw<64, 7>, set, grid, st, tx, tdy, tgh, tgs, tghp, tgsp, d, p);
   }
   if (e == cudaSuccess) *launches += 1;

@@ -33,10 +33,13 @@ def fake(tmp_path_factory):
     return run
 
 
-def test_each_device_is_set_up(fake):
+@pytest.mark.parametrize("call", ["mxfp4_grouped_gemm", "grouped_gemm", "grouped_gemm_dx",
+                                  "grouped_gemm_dw"])
+def test_each_device_is_set_up(fake, call):
     # the second device has half the multiprocessors and an opt-in of its own
-    lines = fake("mxfp4_grouped_gemm", 0, 1, 0)
+    lines = fake(call, 0, 1, 0)
     assert [ln for ln in lines if ln.startswith("returned")] == ["returned 0"] * 3, lines
     grids = [(int(m[1]), int(m[2])) for m in (re.match(r"device (\d) \S+ grid (\d+) ok", ln)
                                               for ln in lines) if m]
-    assert grids == [(0, 152)] * 2 + [(1, 76)] * 2 + [(0, 152)] * 2, lines
+    n = 1 if call.endswith("dw") else 2  # a kernel for each height of the plan's tiles
+    assert grids == [(0, 152)] * n + [(1, 76)] * n + [(0, 152)] * n, lines
