@@ -19,10 +19,11 @@ constexpr int kMmaM = 128;          // rows of one tcgen05.mma (cta_group::1)
 constexpr int kHistWarps = 8;
 // Tensor-map scratch of the grouped weight-gradient kernel: per CTA, a ring of
 // kTmapSlots pairs of 128-byte tensor maps (recv and dY views whose row extent
-// ends at the current group's end); sized for up to kMaxGemmCtas CTAs.
-constexpr int kMaxGemmCtas = 256;
+// ends at the current group's end); sized for up to kMaxGemmCtas CTAs and the bytes
+// up to a 128-byte boundary, where tensor maps have to lie and a workspace need not.
+constexpr int kMaxGemmCtas = 255;
 constexpr int kTmapSlots = 8;
-static_assert((size_t)kMaxGemmCtas * kTmapSlots * 2 * 128 == MOONEP_GEMM_SCRATCH_BYTES,
+static_assert((size_t)kMaxGemmCtas * kTmapSlots * 2 * 128 + 128 <= MOONEP_GEMM_SCRATCH_BYTES,
               "the GEMM scratch at the end of the plan workspace");
 
 // Per-expert migrated range of global ordinals [lo, hi) and where it goes.

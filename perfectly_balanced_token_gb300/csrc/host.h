@@ -122,7 +122,7 @@ inline PlanPtrs resolve(const Layout& L, void* ws) {
   q.mtiles = (MTile*)(b + p.mtiles);
   q.rank_groups = (int32_t*)(b + L.rank_groups);
   q.groups = (MTile*)(b + p.groups);
-  q.tmaps = (uint8_t*)(b + L.tmaps);
+  q.tmaps = (uint8_t*)(((uintptr_t)b + L.tmaps + 127) & ~(uintptr_t)127);
   return q;
 }
 

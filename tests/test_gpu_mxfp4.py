@@ -342,3 +342,31 @@ def test_a_failed_plan_writes_nothing():
     assert mx.moonep_read_status(d, ws.buf) == mx._lib.ERR_ROUTING
     for t in (sq, ss, rq, rs, y):
         assert bool((t == 9).all())
+
+
+@pytest.mark.parametrize("gemm_rows", [128, 256])
+def test_workspace_at_any_multiple_of_16(gemm_rows):
+    # groups that end inside tiles, so tensor maps are edited in the workspace
+    w = syn.Workload("offset", R=2, E=8, B=4, K=2, S=500, H=512, Hp=512)
+    idx = routed(w, 9)
+    r = run_layer(w, idx, gemm_rows)
+    d, n = r["d"], r["ws"].buf.numel()
+    x = r["x"].cuda()
+    for offset in (16, 112):
+        ws = torch.zeros(n + 256, dtype=torch.uint8, device="cuda")[offset:offset + n]
+        mx.moonep_plan(d, torch.from_numpy(np.ascontiguousarray(idx)).cuda(), ws)
+        y = torch.full_like(r["y"], 7.0)
+        mx.moonep_mxfp4_grouped_gemm(d, ws, r["rq"], r["rs"], r["home_q"], r["home_s"], r["slot_q"],
+                                     r["slot_s"], y)
+        assert torch.equal(y, r["y"])
+        # the bf16 weight gradient, on the same plan in both workspaces
+        recv = torch.empty(w.N * w.H, dtype=torch.bfloat16, device="cuda")
+        mx.moonep_dispatch(d, ws, x, recv)
+        got = []
+        for buf in (r["ws"].buf, ws):
+            g_home = torch.zeros(w.E * w.H * w.Hp, device="cuda")
+            g_slot = torch.zeros(w.R * w.B * w.H * w.Hp, device="cuda")
+            mx.moonep_grouped_gemm_dw(d, buf, recv, y, g_home, g_slot)
+            got.append((g_home, g_slot))
+        assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+        assert mx.moonep_read_status(d, ws) == 0

@@ -43,3 +43,20 @@ def test_each_device_is_set_up(fake, call):
                                               for ln in lines) if m]
     n = 1 if call.endswith("dw") else 2  # a kernel for each height of the plan's tiles
     assert grids == [(0, 152)] * n + [(1, 76)] * n + [(0, 152)] * n, lines
+
+
+@pytest.mark.parametrize("call", ["mxfp4_grouped_gemm", "grouped_gemm", "grouped_gemm_dx",
+                                  "grouped_gemm_dw"])
+@pytest.mark.parametrize("offset", [0, 16, 112, 240])
+def test_tensor_maps_lie_on_128_bytes(fake, call, offset):
+    # the workspace may begin at any multiple of 16; the copies stay in its last bytes
+    import perfectly_balanced_token_gb300 as mx
+    d = mx.dims(2, 8, 4, 2, 4096, 512, 512)
+    end = 0x10000000 + offset + mx.moonep_plan_workspace_bytes(d)
+    lines = fake("offset", call, offset)
+    maps = [(int(m[1]), int(m[2])) for m in (re.search(r"grid (\d+) ok maps (\d+)", ln)
+                                             for ln in lines) if m]
+    assert maps and lines[-1] == "returned 0", lines
+    for ctas, at in maps:
+        assert at % 128 == 0, lines
+        assert end - mx.GEMM_SCRATCH_BYTES <= at and at + ctas * 8 * 2 * 128 <= end, lines
