@@ -64,6 +64,10 @@ struct MxCfg {
                                16 * kMxQueue + kNumBars * 8 + 16;
 };
 static_assert(MxCfg<1>::kSmem <= 232448 && MxCfg<2>::kSmem <= 232448, "shared memory of a CTA");
+// (an item takes a copy at most and a stage at least, and a stage is filled again only when
+// its last loads have been used)
+static_assert(kTmapSlots > MxCfg<1>::kStages && kTmapSlots > MxCfg<2>::kStages,
+              "a tensor-map copy must outlive the loads in flight");
 
 // Instruction descriptor, kind::mxf4: A and B E2M1 (bits 7-9 and 10-11 = 1), both
 // K-major, N >> 3 in bits 17-22, E8M0 scales (bit 23), M >> 7 in bits 27-28; the
