@@ -163,6 +163,16 @@ def _ptr(t, dtype, numel, name, allow_none=False):
     return t.data_ptr()
 
 
+_KEPT = 1024  # sizes kept at a time: a server's token counts vary without end
+
+
+def _keep(kept: dict, key, value):
+    if len(kept) >= _KEPT:
+        kept.clear()
+    kept[key] = value
+    return value
+
+
 _workspace_bytes: dict = {}  # of dims already asked for, by their fields
 
 
@@ -173,7 +183,7 @@ def moonep_plan_workspace_bytes(d: moonep_dims) -> int:
         n = ctypes.c_size_t(0)
         _check(lib.moonep_plan_workspace_bytes(ctypes.byref(d), ctypes.byref(n)),
                "moonep_plan_workspace_bytes")
-        size = _workspace_bytes[key] = n.value
+        size = _keep(_workspace_bytes, key, n.value)
     return size
 
 

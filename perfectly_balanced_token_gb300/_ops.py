@@ -10,7 +10,7 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import _check, _ptr, _stream, _ws, moonep_dims
+from ._lib import _check, _keep, _ptr, _stream, _ws, moonep_dims
 
 SCORES = {"softmax": 0, "sigmoid": 1}
 DTYPES = {torch.float32: 0, torch.bfloat16: 1}
@@ -83,7 +83,8 @@ def _router_sizes(rd):
         n = ctypes.c_size_t(0)
         _check(lib.moonep_router_workspace_bytes(ctypes.byref(rd), ctypes.byref(n)),
                "moonep_router_workspace_bytes")
-        got = _sizes[key] = (n.value, rd.T * rd.E, rd.T * rd.K, rd.G * rd.E, rd.G, rd.torch_dtype)
+        got = _keep(_sizes, key, (n.value, rd.T * rd.E, rd.T * rd.K, rd.G * rd.E, rd.G,
+                                  rd.torch_dtype))
     return got
 
 

@@ -159,6 +159,21 @@ def test_binding_checks_its_tensors(lib):
         mx.moonep_mxfp4_quantize_weights(torch.zeros(64, 64, dtype=torch.bfloat16), None, None)
 
 
+def test_kept_sizes_do_not_pile_up(lib):
+    # a program whose token count never repeats
+    sizes = [(mx.moonep_router_workspace_bytes(mx.router_dims(64, 64, 4, n)),
+              mx.moonep_plan_workspace_bytes(mx.dims(1, 8, 0, 2, 100 + n, 64, 64, 1)))
+             for n in range(1, 65)]
+    for n in range(3000):
+        mx.moonep_router_workspace_bytes(mx.router_dims(100 + n, 64, 4))
+        mx.moonep_plan_workspace_bytes(mx.dims(1, 8, 0, 2, 200 + n, 64, 64, 1))
+    assert len(_ops._sizes) <= 1024 and len(_lib._workspace_bytes) <= 1024
+    # and the answers stay what they were
+    assert sizes == [(mx.moonep_router_workspace_bytes(mx.router_dims(64, 64, 4, n)),
+                      mx.moonep_plan_workspace_bytes(mx.dims(1, 8, 0, 2, 100 + n, 64, 64, 1)))
+                     for n in range(1, 65)]
+
+
 C_CLIENT = r"""
 #include <stdio.h>
 #include <string.h>
