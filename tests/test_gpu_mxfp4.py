@@ -370,3 +370,52 @@ def test_workspace_at_any_multiple_of_16(gemm_rows):
             got.append((g_home, g_slot))
         assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
         assert mx.moonep_read_status(d, ws) == 0
+
+
+def test_whole_layer_repeats_itself_between_other_inputs():
+    # from the router's logits to the combined output, on the same buffers with other inputs
+    # between: bit for bit, and the gated sum of its own y to within the rounding of the output
+    # (K + 1 fp32 roundings of the sum of magnitudes and 2^-9 of the value)
+    w = syn.Workload("layer", R=4, E=16, B=4, K=3, S=300, H=512, Hp=320)
+    T, pitch = w.R * w.S, mx.mxfp4_scale_pitch(w.H)
+    d, rd = mx.dims(w.R, w.E, w.B, w.K, w.S, w.H, w.Hp), mx.router_dims(T, w.E, w.K, w.S)
+    ws = mx.PlanWorkspace(d)
+    u8 = dict(dtype=torch.uint8, device="cuda")
+    home = torch.empty(w.E * w.Hp, w.H // 2, **u8), torch.empty(w.E * w.Hp, pitch, **u8)
+    mx.moonep_mxfp4_quantize_weights(syn.normal_bf16((w.E, w.H, w.Hp), 0.05, 4).cuda(), *home)
+    nb = w.R * w.B * w.Hp
+    slot = torch.empty(nb, w.H // 2, **u8), torch.empty(nb, pitch, **u8)
+    recv = torch.empty(w.N, w.H // 2, **u8), torch.empty(w.N, pitch, **u8)
+    rws = torch.empty(mx.moonep_router_workspace_bytes(rd), **u8)
+    idx = torch.empty(T, w.K, dtype=torch.int32, device="cuda")
+    gates = torch.empty(T, w.K, device="cuda")
+    balance = dict(counts=torch.empty(w.R, w.E, dtype=torch.int32, device="cuda"),
+                   prob_sum=torch.empty(w.R, w.E, device="cuda"),
+                   seg_tokens=torch.empty(w.R, dtype=torch.int32, device="cuda"),
+                   loss=torch.empty(1, device="cuda"))
+    y = torch.empty(w.N, w.Hp, dtype=torch.bfloat16, device="cuda")
+    out = torch.empty(T, w.Hp, dtype=torch.bfloat16, device="cuda")
+
+    def layer(seed):
+        g = torch.Generator().manual_seed(seed)
+        skew = 0.7 * torch.log1p(torch.arange(w.E).float())
+        logits = (torch.randn(T, w.E, generator=g) - skew).cuda()
+        x = syn.normal_bf16((T, w.H), 1.0, seed).cuda()
+        mx.moonep_router_forward(rd, logits, idx, gates, ws=rws, **balance)
+        mx.moonep_plan(d, idx, ws.buf)
+        mx.moonep_mxfp4_prefetch_weights(d, ws.buf, *home, *slot)
+        mx.moonep_mxfp4_dispatch(d, ws.buf, x, *recv)
+        mx.moonep_mxfp4_grouped_gemm(d, ws.buf, *recv, *home, *slot, y)
+        mx.moonep_combine(d, ws.buf, y, gates, out)
+        return [t.clone() for t in (idx, gates, *balance.values(), y, out)]
+
+    first = layer(1)
+    rows = ws.tables()["dst"].reshape(T, w.K)
+    terms = y.double().cpu().numpy()[rows] * gates.double().cpu().numpy()[..., None]
+    want, size = terms.sum(1), np.abs(terms).sum(1)
+    err = np.abs(out.double().cpu().numpy() - want)
+    assert (err <= 2.0 ** -8 * np.abs(want) + (w.K + 1) * 2.0 ** -24 * size).all()
+    for other in (2, 3):
+        layer(other)
+        assert all(torch.equal(a, b) for a, b in zip(first, layer(1)))
+    assert mx.moonep_read_status(d, ws.buf) == 0

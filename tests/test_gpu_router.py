@@ -470,3 +470,55 @@ def test_short_segments_launch_after_launch(E, K, score, dtype, segment):
         for k in want:
             differ += (got[k] != want[k]).any()
     assert int(differ) == 0
+
+
+# So many tokens that the blocks run in several rounds (a block takes 64 tokens a warp, a
+# multiprocessor holds 64 warps at most): the same few rows again and again, so that all that
+# repeats has to be equal and the sums are those of one turn times the turns.
+# Sums: a warp's 64 tokens in fp32 add 64 2^-24 to RTOL, 24 warps half as much; a block rounds
+# once to steps of 2^-41 at up to 2^21 tokens.
+@pytest.mark.parametrize("E,K,turns,score,dtype", [(64, 4, 1304, "softmax", torch.float32),
+                                                   (71, 5, 1304, "sigmoid", torch.bfloat16),
+                                                   (384, 8, 700, "softmax", torch.float32),
+                                                   (896, 16, 500, "sigmoid", torch.bfloat16)])
+@pytest.mark.parametrize("segment_turns", [0, 37])
+def test_blocks_in_several_rounds(E, K, turns, score, dtype, segment_turns):
+    n = 997
+    T = n * turns
+    few = draw(n, E, 31, dtype)
+    live = np.random.default_rng(3).random(n) > 0.2
+    rd = mx.router_dims(T, E, K, segment_turns * n, score, True, 1.5, dtype)
+    l = few.cuda().repeat(turns, 1)
+    mask = torch.from_numpy(live.astype(np.uint8)).cuda().repeat(turns)
+    fwd = forward(rd, l, mask)
+    ids, gates, counts, sums, tokens, loss = ops.router(few.double().numpy(), K, n, score, True, 1.5,
+                                                        live)
+    idx, g = fwd["topk_idx"].view(turns, n, K), fwd["gates"].view(turns, n, K)
+    assert np.array_equal(idx[0].cpu().numpy(), ids) and bool((idx == idx[0]).all())
+    close(g[0].cpu().numpy(), gates, "gates")
+    assert bool((g == g[0]).all())
+    per = segment_turns or turns
+    r = np.minimum(per, turns - np.arange(rd.G) * per)[:, None]  # turns of each segment
+    assert np.array_equal(fwd["counts"].cpu().numpy(), r * counts)
+    assert np.array_equal(fwd["seg_tokens"].cpu().numpy(), r[:, 0] * tokens)
+    close(fwd["prob_sum"].cpu().numpy(), r * sums, "prob_sum", RTOL + 96 * 2.0 ** -24,
+          (T / 512 + 1) * 2.0 ** -42)
+    close(fwd["loss"][0].cpu().numpy(), loss, "loss", RTOL + 96 * 2.0 ** -24)
+    again = forward(rd, l, mask)
+    assert all(torch.equal(fwd[k], again[k]) for k in fwd)
+    if segment_turns:
+        return
+    dg = torch.randn(n, K, generator=torch.Generator().manual_seed(2))
+    got = torch.full((T, E), 7.0, dtype=dtype, device="cuda")
+    mx.moonep_router_backward(rd, l, fwd["topk_idx"], got, token_mask=mask,
+                              d_gates=dg.cuda().repeat(turns, 1), counts=fwd["counts"],
+                              seg_tokens=fwd["seg_tokens"],
+                              d_loss=torch.tensor([float(T)], device="cuda"))
+    got = got.view(turns, n, E)
+    assert bool((got == got[0]).all())
+    # counts and tokens of all turns: the weights of one turn's over the turns
+    want, size = ops.router_backward(few.double().numpy(), ids, n, score, True, 1.5, live,
+                                     dg.numpy(), float(T) / turns)
+    tol = 3 * RTOL * size + 1e-12 + (2.0 ** -8 * np.abs(want) if dtype == torch.bfloat16 else 0)
+    err = np.abs(got[0].double().cpu().numpy() - want)
+    assert (err <= tol).all(), (err.max(), (err / tol).max())
