@@ -132,9 +132,14 @@ int moonep_mxfp4_dispatch(const moonep_dims* dims, void* plan_ws, const uint16_t
  * above, products and sums in the block-scaled tensor-core instruction with
  * fp32 accumulation, y bf16 [R][C][Hp] (round to nearest even).  Slot pointers
  * may be NULL when B == 0.  N, R*B*Hp and E*Hp must stay below 2^31 - 512
- * (MOONEP_ERR_SHAPE).  Uses the plan's work tiles; training keeps its
- * gradients in bf16 through moonep_grouped_gemm_dx / _dw on the unquantised
- * (or dequantised) operands. */
+ * (MOONEP_ERR_SHAPE).  Uses the plan's work tiles.
+ * The gradients stay in bf16, on the same plan: moonep_grouped_gemm_dx takes
+ * bf16 weights [E][H][Hp] with their slots (moonep_prefetch_weights), and
+ * moonep_grouped_gemm_dw bf16 rows (H a multiple of 128).  These are the
+ * caller's weights and moonep_dispatch's rows; or, for the gradients of the
+ * product as it was computed, what moonep_mxfp4_dequantize makes of the codes:
+ * recv as it stands, the weights turned by the caller from [E][Hp][H] to
+ * [E][H][Hp] first. */
 int moonep_mxfp4_grouped_gemm(const moonep_dims* dims, void* plan_ws, const uint8_t* recv_codes,
                               const uint8_t* recv_scales, const uint8_t* home_codes,
                               const uint8_t* home_scales, const uint8_t* slot_codes,

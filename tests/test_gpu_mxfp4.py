@@ -419,3 +419,48 @@ def test_whole_layer_repeats_itself_between_other_inputs():
         layer(other)
         assert all(torch.equal(a, b) for a, b in zip(first, layer(1)))
     assert mx.moonep_read_status(d, ws.buf) == 0
+
+
+@pytest.mark.parametrize("name,R,E,B,K,S,H,Hp", [("narrow", 2, 6, 3, 3, 67, 384, 320),
+                                                 ("wide", 4, 16, 4, 2, 300, 512, 256)])
+def test_gradients_of_the_quantised_product(name, R, E, B, K, S, H, Hp):
+    """moonep_grouped_gemm_dx and _dw on the dequantised operands, as the header describes, against
+    the chain rule in 64 bits through y = recv_q W_q^T.  fp32 sums of n terms: n 2^-24 of the sum
+    of magnitudes (twice that is allowed), the bf16 input gradient 2^-8 of itself."""
+    w = syn.Workload(name, R=R, E=E, B=B, K=K, S=S, H=H, Hp=Hp)
+    idx = routed(w, 4)
+    r = run_layer(w, idx, 0)
+    d, ws, bf = r["d"], r["ws"].buf, torch.bfloat16
+    recv = torch.empty(w.N, H, dtype=bf, device="cuda")
+    mx.moonep_mxfp4_dequantize(r["rq"], r["rs"], recv)
+    turned = torch.empty(E, Hp, H, dtype=bf, device="cuda")
+    mx.moonep_mxfp4_dequantize(r["home_q"], r["home_s"], turned)
+    w_home = turned.transpose(1, 2).contiguous()
+    w_slot = torch.zeros(R * B * H * Hp, dtype=bf, device="cuda")
+    mx.moonep_prefetch_weights(d, ws, w_home, w_slot)
+    rng = np.random.default_rng(1)
+    gates = torch.from_numpy(rng.random(w.N).astype(np.float32)).cuda()
+    d_out = syn.normal_bf16((R * S, Hp), 1.0, 8).cuda()
+    d_y, d_gates = torch.empty_like(r["y"]).contiguous(), torch.empty(w.N, device="cuda")
+    mx.moonep_combine_backward(d, ws, r["y"], gates, d_out, d_y, d_gates)
+    d_recv = torch.empty(w.N, H, dtype=bf, device="cuda")
+    mx.moonep_grouped_gemm_dx(d, ws, d_y, w_home, w_slot, d_recv)
+    g_home = torch.zeros(E, H, Hp, device="cuda")
+    g_slot = torch.zeros(R * B * H * Hp, device="cuda")
+    mx.moonep_grouped_gemm_dw(d, ws, recv, d_y, g_home, g_slot)
+    mx.moonep_reduce_grad(d, ws, g_home, g_slot)
+    assert mx.moonep_read_status(d, ws) == 0
+    inv = r["tabs"]["inverse"]
+    token, expert = inv // K, idx.reshape(-1)[inv]
+    xv = ops.mxfp4_values(*ops.mxfp4_quantize(r["x"].double().numpy()))[token]
+    dy = d_y.double().cpu().numpy().reshape(w.N, Hp)
+    want_dy = gates.double().cpu().numpy()[inv, None] * d_out.double().cpu().numpy()[token]
+    assert (np.abs(dy - want_dy) <= 2.0 ** -8 * np.abs(want_dy)).all()
+    dx, dw = d_recv.double().cpu().numpy(), g_home.double().cpu().numpy()
+    for e in range(E):
+        at = np.nonzero(expert == e)[0]
+        wv = ops.mxfp4_values(*ops.mxfp4_quantize(r["wt"][e].double().numpy().T.copy()))
+        want, size = dy[at] @ wv, np.abs(dy[at]) @ np.abs(wv)
+        assert (np.abs(dx[at] - want) <= 2.0 ** -8 * np.abs(want) + Hp * 2.0 ** -23 * size).all(), e
+        want, size = xv[at].T @ dy[at], np.abs(xv[at].T) @ np.abs(dy[at])
+        assert (np.abs(dw[e] - want) <= (len(at) + 8) * 2.0 ** -23 * size).all(), e
