@@ -48,7 +48,10 @@ extern "C" {
  * A row that holds only -inf has q = 0 and gates 0.  Other rows with NaN (softmax:
  * or +inf) give NaN where the formulas do.  Gates, sums and the loss are computed
  * in fp32 or wider; the result is the same in every run (sums across blocks are
- * integer sums of fixed-point values). */
+ * integer sums of fixed-point values).  Smallest values: scores below 2^-126
+ * read 0, and where several blocks share a segment each rounds its part of
+ * prob_sum to a multiple of 2^-46 (of 2^(b - 62) for segments of more than 2^16
+ * tokens, 2^b the power of two at or above their length). */
 typedef struct moonep_router_dims {
   int32_t T, E, K;
   int32_t segment;    /* tokens per segment of the balance loss, 1 .. T (0: T) */

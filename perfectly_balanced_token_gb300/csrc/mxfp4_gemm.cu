@@ -117,7 +117,8 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[
 // a thread that does nothing else.  With the claims and the tile list read by the TMA
 // producer, between one item's loads and the next's, the first two stages of an item
 // came some 2500 clocks late: 1193 -> 1117 us at 262144 rows x 7168 x 2048, 459 -> 379 us
-// at 262144 rows x 4096 x 1024 in 224 groups.  A slot is filled when it is free and not
+// at 262144 rows x 4096 x 1024 in 224 groups (short runs; call after call the power limit
+// sets the time, 1311 us at 1450 MHz).  A slot is filled when it is free and not
 // before: an item claimed earlier is one that no idle CTA can take (decoding 16
 // tokens: 125 us with the next item claimed ahead, 117 without).
 struct __align__(16) MxItem {
@@ -338,7 +339,7 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     }
   } else if (warp == 1) {
     // ---------------- MMA issuer (leader only) ----------------
-    // (elect_one instead of lane 0: 1355 -> 1229 us at 262144 rows x 7168 x 2048)
+    // (elect_one instead of lane 0: 1355 -> 1229 us at 262144 rows x 7168 x 2048, short runs)
     if (leader && elect_one()) {
       constexpr uint32_t idesc[2] = {mx_idesc(CG * kMmaM, kMxBN, 0), mx_idesc(CG * kMmaM, kMxBN, 2)};
       int stage = 0, slot = 0;
@@ -426,6 +427,9 @@ k_mxfp4_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         for (int c = 0; c < 2; ++c) {
           const int n = c0 + c * 64;
           if (n0 + n >= N) break;  // N is a multiple of 64
+          // The one rounding of the fp32 sums: bf16 is the type that moonep_combine reads,
+          // as in the bf16 product (layer of 8192 tokens x 1024 x 512, K 4: 2.35e-3 from 64
+          // bits; with fp32 kept up to the combined output 1.66e-3)
           uint4 o[8];
 #pragma unroll
           for (int v = 0; v < 8; ++v) {

@@ -570,10 +570,15 @@ __device__ __forceinline__ void join_blocks(const RouterDims& d, const RouterOut
 // A block takes per_block consecutive tokens, a warp every W-th of them; with the
 // loss, segment by segment.  SHORT: K <= 32.
 //
-// Bound by instructions: about 290 a token to choose the experts and place them, and per
-// logit 1 to 4 more there and 7 in scores and sums.  Measured with the loss: 65536 x 384
-// fp32, K 8: 49.2 us (without 35.3; its bytes 15.6); 65536 x 896 bf16, K 16, sigmoid:
-// 69.7 us (without 45; its bytes 18.8, its 2 special functions a score 25).
+// Bound by instructions and by the latency of a token's own chain (test the bound, gather,
+// rank, score): about 290 instructions a token to choose the experts and place them, and
+// per logit 1 to 4 more there and 7 in scores and sums.  While blocks run, 66 % (384
+// experts) and 74 % (896) of the issue slots are used, 55 and 61 % of the launch with its
+// start and end; of the 10.5 clocks between two instructions of a warp at 384, 2.6 are
+// waits for the row, 1.4 for shared memory and shuffles, 1.9 for results of fixed latency,
+// 0.75 for the block.  Measured with the loss: 65536 x 384 fp32, K 8: 49.2 us (without
+// 35.3; its bytes 15.6); 65536 x 896 bf16, K 16, sigmoid: 69.7 us (without 45; its bytes
+// 18.8, its 2 special functions a score 25).
 template <typename T, int N, bool VEC, bool LOSS, bool SHORT, int KIND>
 __global__ void __launch_bounds__(forward_warps<N, LOSS>() * 32, forward_blocks<N, LOSS>())
 k_router(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__ mask,
@@ -760,7 +765,8 @@ k_router(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__
 // a segment, lies there too, as three rows in registers left a third of the warps.
 //
 // Bound by bytes at 65536 x 384 fp32 (37.9 us, 5.4 TB/s; its bytes 30.5), by instructions
-// at 65536 x 896 bf16 (58 us; with w in registers 79; its bytes 35).
+// and their latency at 65536 x 896 bf16 (58 us, 69 % of the issue slots while blocks run;
+// with w in registers 79 us; its bytes 35).
 template <typename T, int N, bool VEC, bool SHORT, int KIND>
 __global__ void __launch_bounds__(router_warps<N>() * 32, router_blocks<N>())
 k_router_backward(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__ mask,
