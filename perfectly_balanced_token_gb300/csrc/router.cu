@@ -912,16 +912,27 @@ k_router_backward(RouterDims d, const T* __restrict__ logits, const uint8_t* __r
         // is behind what is left of this one
         if (VEC && next_live) fetch_row<T, N>(s_row, next_row, d.E, lane);
         const float dot_inv = dot * inv;
+        // (two loops: a choice for each element costs 1 us at 65536 x 896)
+        if (row_sums) {
 #pragma unroll
-        for (int c = 0; c < N / V; ++c) {
-          const int at = place<N, VEC>(c * V, lane);
-          float wv[V] = {}, av[V] = {};
-          if (inside<N, VEC>(c, lane, d.E)) values(w + at, wv), values(a + at, av);
+          for (int c = 0; c < N / V; ++c) {
+            const int at = place<N, VEC>(c * V, lane);
+            float wv[V] = {}, av[V] = {};
+            if (inside<N, VEC>(c, lane, d.E)) values(w + at, wv), values(a + at, av);
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            float& v = l[c * V + i];
-            if (!score.softmax()) v *= fmaf(-v, score.one, 1.f);
-            v = row_sums ? fmaf(v, fmaf(wv[i], inv, -dot_inv), av[i]) : av[i];
+            for (int i = 0; i < V; ++i) {
+              float& v = l[c * V + i];
+              if (!score.softmax()) v *= fmaf(-v, score.one, 1.f);
+              v = fmaf(v, fmaf(wv[i], inv, -dot_inv), av[i]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < N / V; ++c) {
+            float av[V] = {};
+            if (inside<N, VEC>(c, lane, d.E)) values(a + place<N, VEC>(c * V, lane), av);
+#pragma unroll
+            for (int i = 0; i < V; ++i) l[c * V + i] = av[i];
           }
         }
         if (d_gates != nullptr) {
