@@ -522,3 +522,24 @@ def test_blocks_in_several_rounds(E, K, turns, score, dtype, segment_turns):
     tol = 3 * RTOL * size + 1e-12 + (2.0 ** -8 * np.abs(want) if dtype == torch.bfloat16 else 0)
     err = np.abs(got[0].double().cpu().numpy() - want)
     assert (err <= tol).all(), (err.max(), (err / tol).max())
+
+
+# Logits within 4 of 0, so that exponents are at most 8 long: an exponential is then within
+# 2 2^-23 + 8 2^-24 + 8 2^-25 (instruction, product, constant) = 9.6e-7 of itself, a sum over the
+# row within 17 2^-24 (12 values a lane, 5 steps over the warp) = 1e-6 more.  Gate: two
+# exponentials, the chosen scores in steps of 2^-24 (8 halves of a step over 1/2: 4.8e-7), a
+# reciprocal and four products (3.6e-7): 2.8e-6.  prob_sum: the score (sigmoid: and a reciprocal,
+# 1.2e-6), the row's sum of such scores (2.2e-6), a reciprocal and up to 13 additions (9e-7): 4.3e-6.
+@pytest.mark.parametrize("E", [64, 384])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("normalise", [True, False])
+def test_rounding_of_moderate_logits(E, score, normalise):
+    T, K, tight = 300, 8, 5e-6
+    l = torch.from_numpy(np.random.default_rng(E).uniform(-4, 4, (T, E)).astype(np.float32))
+    rd = mx.router_dims(T, E, K, 100, score, normalise, 1.0)
+    out = {k: v.cpu().numpy() for k, v in forward(rd, l.cuda()).items()}
+    ids, gates, counts, sums, _, loss = ops.router(l.double().numpy(), K, 100, score, normalise, 1.0)
+    assert np.array_equal(out["topk_idx"], ids) and np.array_equal(out["counts"], counts)
+    close(out["gates"], gates, "gates", tight, 0)
+    close(out["prob_sum"], sums, "prob_sum", tight)
+    close(out["loss"][0], loss, "loss", tight)
