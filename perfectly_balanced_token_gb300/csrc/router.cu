@@ -765,7 +765,7 @@ k_router(RouterDims d, const T* __restrict__ logits, const uint8_t* __restrict__
 // a segment, lies there too, as three rows in registers left a third of the warps.
 //
 // Bound by bytes at 65536 x 384 fp32 (37.9 us, 5.4 TB/s; its bytes 30.5), by instructions
-// and their latency at 65536 x 896 bf16 (58 us, 69 % of the issue slots while blocks run;
+// and their latency at 65536 x 896 bf16 (58 us, 68 % of the issue slots while blocks run;
 // with w in registers 79 us; its bytes 35).
 template <typename T, int N, bool VEC, bool SHORT, int KIND>
 __global__ void __launch_bounds__(router_warps<N>() * 32, router_blocks<N>())
