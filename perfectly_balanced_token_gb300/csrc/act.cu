@@ -1,0 +1,243 @@
+// Gradient of the feed-forward network's activation, with that of the bias.  Bound by memory:
+// 16-byte accesses, each value read and written once, four rows of loads in flight in every thread.
+#include <algorithm>
+
+#include "activation.cuh"
+#include "ffn.h"
+#include "vec.cuh"
+
+namespace moonep {
+
+// ---------------------------------------------------------------------------
+// d_z = act'(z) d_out, with column sums of d_z (in fp32, before d_z is rounded).
+//
+// An item is a chunk of rows (128, or a work tile of the plan: rows of one expert) by 256 columns;
+// a warp's lanes cover the columns and its rows are every eighth of the chunk.  The chunk's sums go
+// to scratch, one row a chunk, and a second kernel adds them in ascending order: the same bits in
+// every run, whatever runs when.
+// ---------------------------------------------------------------------------
+constexpr int kActThreads = 256;
+constexpr int kActWarps = kActThreads / 32;
+constexpr int kActRows = 128;
+constexpr int kActCols = 256;
+
+struct ActArgs {
+  int64_t rows;
+  int cols;  // of z
+  const uint16_t *z, *d_out;
+  uint16_t* d_z;
+  float* sums;  // [chunks][cols] or null
+};
+
+// slope[i] = d act / d z at z[i]
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z) {
+  if (ACT == kActRelu) return z > 0.f ? 1.f : (z <= 0.f ? 0.f : z);  // (a NaN stays one)
+  if (ACT == kActGelu)
+    return fmaf(z, 0.3989422804f * expf(-0.5f * z * z), normal_cdf(z));
+  if (ACT == kActSilu) {
+    const float s = sigmoid_f(z);
+    return s * fmaf(z, 1.f - s, 1.f);
+  }
+  return 1.f;
+}
+
+template <int ACT>
+__global__ void __launch_bounds__(kActThreads) k_act_backward(ActArgs a, PlanPtrs p, int plan) {
+  constexpr bool GATED = ACT == kActSwiglu;
+  __shared__ float part[GATED ? 2 : 1][kActWarps][kActCols];
+  // plan: 0 = none, 1 = chunks are its work tiles, 2 = only its status counts
+  if (plan && plan_failed(p.status)) return;
+  const bool grouped = plan == 1;
+  const int ocols = GATED ? a.cols / 2 : a.cols;
+  const int nct = (ocols + kActCols - 1) / kActCols;
+  const int64_t chunks = grouped ? p.counters[MOONEP_CNT_MTILES] : (a.rows + kActRows - 1) / kActRows;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int64_t item = blockIdx.x; item < chunks * nct; item += gridDim.x) {
+    const int64_t chunk = item / nct;
+    const int col = (int)(item % nct) * kActCols + lane * 8;
+    int64_t row0;
+    int rows;
+    if (grouped) {
+      const MTile mt = p.mtiles[chunk];
+      row0 = mt.row0;
+      rows = mt.rows;
+    } else {
+      row0 = chunk * kActRows;
+      rows = (int)min((int64_t)kActRows, a.rows - row0);
+    }
+    float sum[8] = {}, sum_up[8] = {};
+    if (col < ocols) {
+      constexpr int U = 4;  // rows in flight
+      for (int r0 = warp; r0 < rows; r0 += U * kActWarps) {
+        uint4 vz[U], vu[U], vd[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int r = r0 + u * kActWarps;
+          if (r < rows) {
+            const int64_t row = row0 + r;
+            vd[u] = __ldcs(reinterpret_cast<const uint4*>(a.d_out + row * ocols + col));
+            if (ACT != kActNone)
+              vz[u] = __ldcs(reinterpret_cast<const uint4*>(a.z + row * a.cols + col));
+            if (GATED)
+              vu[u] = __ldcs(reinterpret_cast<const uint4*>(a.z + row * a.cols + ocols + col));
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int r = r0 + u * kActWarps;
+          if (r < rows) {
+            const int64_t row = row0 + r;
+            float d[8], z[8], up[8];
+            unpack8(d, vd[u]);
+            if (ACT != kActNone) unpack8(z, vz[u]);
+            if (GATED) {
+              unpack8(up, vu[u]);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                // one sigmoid serves both: a = z s(z), a' = s (1 + z (1 - s))
+                const float s = sigmoid_f(z[i]);
+                const float du = d[i] * (z[i] * s);
+                z[i] = d[i] * up[i] * (s * fmaf(z[i], 1.f - s, 1.f));
+                up[i] = du;
+                sum_up[i] += du;
+              }
+              *reinterpret_cast<uint4*>(a.d_z + row * a.cols + ocols + col) = pack8(up);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) z[i] = ACT == kActNone ? d[i] : d[i] * act_slope<ACT>(z[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[i] += z[i];
+            if (a.d_z != nullptr) __stcs(reinterpret_cast<uint4*>(a.d_z + row * a.cols + col), pack8(z));
+          }
+        }
+      }
+    }
+    if (a.sums == nullptr) continue;
+    __syncthreads();  // the previous item's sums are read
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      part[0][warp][lane * 8 + i] = sum[i];
+      if (GATED) part[GATED ? 1 : 0][warp][lane * 8 + i] = sum_up[i];
+    }
+    __syncthreads();
+    const int c = (int)(item % nct) * kActCols + threadIdx.x;
+    if (c < ocols) {
+#pragma unroll
+      for (int h = 0; h < (GATED ? 2 : 1); ++h) {
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < kActWarps; ++w) s += part[h][w][threadIdx.x];
+        a.sums[chunk * a.cols + h * ocols + c] = s;
+      }
+    }
+  }
+}
+
+// d_bias[c] (+)= sum over chunks of sums[chunk][c]: 32 columns a block, 32 threads a column
+__global__ void __launch_bounds__(1024) k_sum_chunks(const float* __restrict__ sums, int64_t chunks,
+                                                     int cols, float* __restrict__ d_bias, int add) {
+  __shared__ float part[32][33];
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5, c = blockIdx.x * 32 + x;
+  float s = 0.f;
+  if (c < cols)
+    for (int64_t k = y; k < chunks; k += 32) s += sums[k * cols + c];
+  part[y][x] = s;
+  __syncthreads();
+  if (y == 0 && c < cols) {
+    float total = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) total += part[i][x];
+    d_bias[c] = add ? d_bias[c] + total : total;
+  }
+}
+
+// The same for each expert over its work tiles: a block an expert, which picks the expert's tiles
+// out of the plan's list, 1024 at a time and in order, and adds their rows of sums.
+constexpr int kPickThreads = 1024;
+__global__ void __launch_bounds__(kPickThreads)
+k_sum_tiles(PlanPtrs p, const float* __restrict__ sums, int cols, float* __restrict__ d_bias, int add) {
+  __shared__ int picked[kPickThreads];
+  __shared__ int count[kPickThreads / 32];
+  if (plan_failed(p.status)) return;
+  const int e = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tiles = p.counters[MOONEP_CNT_MTILES];
+  for (int c = tid; c < cols; c += kPickThreads)
+    if (!add) d_bias[(size_t)e * cols + c] = 0.f;
+  for (int t0 = 0; t0 < tiles; t0 += kPickThreads) {
+    const int t = t0 + tid;
+    bool mine = false;
+    if (t < tiles) {
+      const int w = p.mtiles[t].wsel;
+      mine = (w >= 0 ? w : p.slot_expert[-1 - w]) == e;
+    }
+    const uint32_t b = __ballot_sync(0xffffffffu, mine);
+    if (lane == 0) count[warp] = __popc(b);
+    __syncthreads();
+    int before = 0, n = 0;
+#pragma unroll
+    for (int w = 0; w < kPickThreads / 32; ++w) {
+      if (w < warp) before += count[w];
+      n += count[w];
+    }
+    if (mine) picked[before + __popc(b & ((1u << lane) - 1))] = t;
+    __syncthreads();
+    if (n > 0)
+      for (int c = tid; c < cols; c += kPickThreads) {
+        float s = d_bias[(size_t)e * cols + c];
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) s += sums[(size_t)picked[i] * cols + c];
+        d_bias[(size_t)e * cols + c] = s;
+      }
+    __syncthreads();
+  }
+}
+
+// -- host side ------------------------------------------------------------------
+int64_t act_chunks(int64_t rows) { return (rows + kActRows - 1) / kActRows; }
+
+static cudaError_t launch_act(int act, const ActArgs& a, const PlanPtrs& p, int plan,
+                              int64_t chunks, cudaStream_t st) {
+  const int ocols = act == kActSwiglu ? a.cols / 2 : a.cols;
+  const int64_t items = chunks * ((ocols + kActCols - 1) / kActCols);
+  const int grid = (int)std::min<int64_t>(items, (int64_t)sm_count_gemm() * 16);
+  if (act == kActNone) k_act_backward<kActNone><<<grid, kActThreads, 0, st>>>(a, p, plan);
+  else if (act == kActRelu) k_act_backward<kActRelu><<<grid, kActThreads, 0, st>>>(a, p, plan);
+  else if (act == kActGelu) k_act_backward<kActGelu><<<grid, kActThreads, 0, st>>>(a, p, plan);
+  else if (act == kActSilu) k_act_backward<kActSilu><<<grid, kActThreads, 0, st>>>(a, p, plan);
+  else k_act_backward<kActSwiglu><<<grid, kActThreads, 0, st>>>(a, p, plan);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_act_backward(int64_t rows, int cols, int act, const void* z, const void* d_out,
+                                void* d_z, float* d_bias, int add, float* scratch, cudaStream_t st,
+                                int* launches) {
+  const ActArgs a{rows, cols, (const uint16_t*)z, (const uint16_t*)d_out, (uint16_t*)d_z,
+                  d_bias ? scratch : nullptr};
+  cudaError_t e = cudaSuccess;
+  if (rows > 0) {
+    e = launch_act(act, a, PlanPtrs{}, 0, act_chunks(rows), st);
+    *launches += 1;
+  }
+  if (e != cudaSuccess || d_bias == nullptr) return e;
+  k_sum_chunks<<<(cols + 31) / 32, 1024, 0, st>>>(scratch, act_chunks(rows), cols, d_bias, add);
+  *launches += 1;
+  return cudaGetLastError();
+}
+
+cudaError_t launch_grouped_act_backward(const Dims& d, const PlanPtrs& p, int act, const void* z,
+                                        const void* d_y, void* d_z, float* d_bias, int add,
+                                        float* scratch, cudaStream_t st, int* launches) {
+  const ActArgs a{d.N, d.Hp, (const uint16_t*)z, (const uint16_t*)d_y, (uint16_t*)d_z,
+                  d_bias ? scratch : nullptr};
+  // rows of one expert matter to the sums alone
+  const cudaError_t e = launch_act(act, a, p, d_bias ? 1 : 2, d_bias ? d.max_mtiles : act_chunks(d.N), st);
+  *launches += 1;
+  if (e != cudaSuccess || d_bias == nullptr) return e;
+  k_sum_tiles<<<d.E, kPickThreads, 0, st>>>(p, scratch, d.Hp, d_bias, add);
+  *launches += 1;
+  return cudaGetLastError();
+}
+
+}  // namespace moonep
