@@ -17,7 +17,8 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libmoonep.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 SOURCES = ["moonep.cu", "plan.cu", "move.cu", "gemm.cu", "ops.cu", "router.cu", "mxfp4.cu",
-           "mxfp4_gemm.cu", "ffn.cu", "product.cu", "act.cu", "dropout.cu"]
+           "mxfp4_gemm.cu", "ffn.cu", "product.cu", "product_split.cu",
+           "act.cu", "dropout.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE,
          "--expt-relaxed-constexpr"]

@@ -29,19 +29,6 @@ struct ActArgs {
   float* sums;  // [chunks][cols] or null
 };
 
-// slope[i] = d act / d z at z[i]
-template <int ACT>
-__device__ __forceinline__ float act_slope(float z) {
-  if (ACT == kActRelu) return z > 0.f ? 1.f : (z <= 0.f ? 0.f : z);  // (a NaN stays one)
-  if (ACT == kActGelu)
-    return fmaf(z, 0.3989422804f * expf(-0.5f * z * z), normal_cdf(z));
-  if (ACT == kActSilu) {
-    const float s = sigmoid_f(z);
-    return s * fmaf(z, 1.f - s, 1.f);
-  }
-  return 1.f;
-}
-
 template <int ACT>
 __global__ void __launch_bounds__(kActThreads) k_act_backward(ActArgs a, PlanPtrs p, int plan) {
   constexpr bool GATED = ACT == kActSwiglu;

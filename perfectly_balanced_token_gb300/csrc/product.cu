@@ -22,32 +22,34 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "activation.cuh"
-#include "ffn.h"
-#include "tcgen05.cuh"
+#include "product.cuh"
 
 namespace moonep {
 
-constexpr int kDepth = 64;          // of a stage: 64 bf16 = one 128-byte swizzle row
-constexpr int kProductThreads = 192;
-constexpr int kPanelBytes = 64 * 128;  // 64 rows of 64 bf16
+// Blocks of the depth that one accumulator sums where C is fp32.  The instruction cuts off what its
+// fp32 sums do not hold, always towards zero, so a long sum drifts: against 64 bits, with the whole
+// depth in one accumulator, 7e-6 of C at a depth of 7168 and past 1e-5 at 32768.  The epilogue adds the
+// parts in registers, rounding to nearest.  (A bf16 C's own rounding is 250 times larger.)
+constexpr int kPartBlocks = 32;
 
-enum Kind { kForward, kInputGrad, kWeightGrad };
-
-template <bool PAIR>
+template <bool PAIR, bool F32>
 struct ProductCfg {
+  // fp32 sums of 128 columns a thread take eight epilogue warps
+  static constexpr int kEpilogueWarps = F32 ? 8 : 4;
+  static constexpr int kThreads = 64 + 32 * kEpilogueWarps;
   static constexpr int kStages = PAIR ? 6 : 4;
   static constexpr int kTileM = PAIR ? 256 : 128;
   static constexpr int kABytes = 128 * kDepth * 2;
   static constexpr int kBPanels = PAIR ? 2 : 4;  // of 64 columns, in one CTA
   static constexpr int kStageBytes = kABytes + kBPanels * kPanelBytes;
-  static constexpr int kOutWarpBytes = 2 * 4096;  // two buffers of 32 rows x 128 bytes
-  static constexpr int kOutBytes = 4 * kOutWarpBytes;
+  static constexpr int kOutBuffers = F32 ? 1 : 2;  // of 32 rows x 128 bytes, a warp
+  static constexpr int kOutBytes = kEpilogueWarps * kOutBuffers * 4096;
   static constexpr int kNumBars = 2 * kStages + 5 + 2 * kQueue;
   static constexpr int kBarBytes = kNumBars * 8 + 16 + 4 * kQueue;
   static constexpr int kSmem = kStages * kStageBytes + kOutBytes + 1024 + kBarBytes;
 };
-static_assert(ProductCfg<true>::kSmem <= 232448 && ProductCfg<false>::kSmem <= 232448,
+static_assert(ProductCfg<true, false>::kSmem <= 232448 && ProductCfg<true, true>::kSmem <= 232448 &&
+                  ProductCfg<false, false>::kSmem <= 232448,
               "shared memory of a CTA");
 
 struct ProductArgs {
@@ -55,7 +57,7 @@ struct ProductArgs {
   int wrows;       // grouped: rows of an expert's weight
   int act;         // Act
   int half;        // swiglu: N / 2, otherwise 0
-  int f32, add;    // C in fp32; added into (both for outputs without groups)
+  int add;         // fp32 C: added into
   const float* bias;  // [N], grouped [E][N]; or null
   const uint16_t* residual;  // [M][out columns] or null
   uint16_t *out, *z;         // for rows stored one by one; z null if not asked for
@@ -84,32 +86,26 @@ struct Issue {  // the forms of one CTA and of a pair
   }
 };
 
-// kind::f16: fp32 accumulator, bf16 operands; which of them run along M or N in memory
-__host__ __device__ constexpr uint32_t product_idesc(int M, int N, bool a_mn, bool b_mn) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
-         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-
-// Descriptor of the k-th 16 of a stage: rows of 128 bytes along the depth, or panels of 64 columns.
-__device__ __forceinline__ uint64_t stage_desc(uint32_t at, int k, bool mn) {
-  return mn ? sw128_desc(at + k * (16 * 128), kPanelBytes, 1024) : sw128_desc(at + k * 32, 16, 1024);
-}
-
-// A warp's two staging buffers of 32 rows x 128 bytes (128-byte swizzle) and the stores from them.
+// A warp's staging buffers of 32 rows x 128 bytes (128-byte swizzle) and the stores from them.
+template <int BUFFERS>
 struct OutRing {
   uint8_t* base;
   int n, lane;
+  static __device__ __forceinline__ uint32_t word(uint32_t v) { return v; }
+  static __device__ __forceinline__ uint32_t word(float v) { return __float_as_uint(v); }
   // writes this lane's row (32 words) and stores the box at column x, row y
-  __device__ __forceinline__ void put(const uint32_t (&v)[32], const CUtensorMap* m, int x, int y,
+  template <typename T>
+  __device__ __forceinline__ void put(const T (&v)[32], const CUtensorMap* m, int x, int y,
                                       bool add) {
-    uint8_t* buf = base + (n & 1) * 4096;
+    uint8_t* buf = base + (n % BUFFERS) * 4096;
     ++n;
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(BUFFERS - 1) : "memory");
     __syncwarp();
     uint4* row = reinterpret_cast<uint4*>(buf + lane * 128);
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      row[j ^ (lane & 7)] = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+      row[j ^ (lane & 7)] =
+          make_uint4(word(v[4 * j]), word(v[4 * j + 1]), word(v[4 * j + 2]), word(v[4 * j + 3]));
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
     if (lane == 0) {
@@ -183,20 +179,18 @@ __device__ __forceinline__ void load32(uint32_t taddr, float (&v)[32]) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// 32 columns of a lane's row from TMEM to the output's values: z and, for swiglu, the up half of z
-// packed into pz and pu on the way, the result in v.  x: the first column, cols: how many are left.
+// 32 columns of a lane's row from the sums (v and, for swiglu, u of the up half) to the output's
+// values in v; z, and its up half, packed into pz and pu on the way.  x: the first column, cols: how
+// many are left.
 template <int H>
 __device__ __forceinline__ void forward32(const ProductArgs& a, const float* bias,
-                                          const uint16_t* residual, uint32_t taddr, int x, int cols,
-                                          float (&v)[32], uint32_t (&pz)[32], uint32_t (&pu)[32]) {
-  load32(taddr + 32 * H, v);
+                                          const uint16_t* residual, int x, int cols, float (&v)[32],
+                                          float (&u)[32], uint32_t (&pz)[32], uint32_t (&pu)[32]) {
   x += 32 * H;
   cols -= 32 * H;
   if (bias != nullptr) add_bias(v, bias + x, cols);
   pack32<H>(pz, v);
   if (a.half) {
-    float u[32];
-    load32(taddr + 128 + 32 * H, u);
     if (bias != nullptr) add_bias(u, bias + a.half + x, cols);
     pack32<H>(pu, u);
 #pragma unroll
@@ -214,11 +208,12 @@ __device__ __forceinline__ void forward32(const ProductArgs& a, const float* bia
   if (residual != nullptr) add_residual(v, residual + x, cols);
 }
 
-template <bool PAIR, int KIND, bool DENSE>
-__global__ void __launch_bounds__(kProductThreads, 1)
+template <bool PAIR, int KIND, bool DENSE, bool F32>
+__global__ void __launch_bounds__(ProductCfg<PAIR, F32>::kThreads, 1)
 k_product(const __grid_constant__ ProductMaps tm, const __grid_constant__ ProductArgs a,
           const __grid_constant__ PlanPtrs p) {
-  using Cfg = ProductCfg<PAIR>;
+  static_assert(DENSE || !F32, "the grouped output is bf16");
+  using Cfg = ProductCfg<PAIR, F32>;
   using Op = Issue<PAIR>;
   constexpr int STAGES = Cfg::kStages;
   constexpr bool AMN = KIND == kWeightGrad;  // A = x^T: runs along M in memory
@@ -229,6 +224,7 @@ k_product(const __grid_constant__ ProductMaps tm, const __grid_constant__ Produc
   uint64_t* bars = (uint64_t*)(out_stage + Cfg::kOutBytes);
   uint32_t* tmem_slot = (uint32_t*)(bars + Cfg::kNumBars);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
+  volatile int* dead = (volatile int*)(tmem_slot + 2 + kQueue);  // the status was set
   const uint32_t bar0 = smem_u32(bars);
   auto full = [&](int s) { return bar0 + 8u * s; };
   auto empty = [&](int s) { return bar0 + 8u * (STAGES + s); };
@@ -244,7 +240,6 @@ k_product(const __grid_constant__ ProductMaps tm, const __grid_constant__ Produc
   const bool leader = crank == 0;
   const int nwork = PAIR ? gridDim.x >> 1 : gridDim.x;   // pairs or CTAs
   const int work = PAIR ? blockIdx.x >> 1 : blockIdx.x;  // this one
-  if (plan_failed(a.status)) return;  // uniform over the pair: before any barrier
   if (!DENSE && p.counters[MOONEP_CNT_TILE_ROWS] != Cfg::kTileM) return;
   const int NT = a.half ? (a.half + 127) / 128 : (a.N + 255) / 256;
   const int MT = DENSE ? (a.M + Cfg::kTileM - 1) / Cfg::kTileM : p.counters[MOONEP_CNT_MTILES];
@@ -259,11 +254,12 @@ k_product(const __grid_constant__ ProductMaps tm, const __grid_constant__ Produc
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull(b), 1);
-      mbar_init(tempty(b), PAIR ? 8 : 4);  // four epilogue warps in each CTA
+      mbar_init(tempty(b), (PAIR ? 2 : 1) * Cfg::kEpilogueWarps);
     }
     mbar_init(drain, 1);
     if (!DENSE) queue_init(q, PAIR ? kQueueConsumers : kQueueConsumersSolo);
     *abort_flag = 0;
+    *dead = plan_failed(a.status);
     fence_barrier_init();
   }
   if (warp == 0 && lane == 0) {
@@ -285,6 +281,15 @@ k_product(const __grid_constant__ ProductMaps tm, const __grid_constant__ Produc
   tc_fence_after();
   if (PAIR) pair_sync();  // the peer's barriers are initialised before anything reaches them
   const uint32_t tmem_base = *tmem_slot;
+  // both CTAs go by what either found in the status word: another pair may set it meanwhile
+  int skip = *dead;
+  if (PAIR) {
+    int other;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];"
+                 : "=r"(other)
+                 : "r"(pair_map(smem_u32((const void*)dead), crank ^ 1u)));
+    skip |= other;
+  }
 
   auto fail = [&]() {
     *abort_flag = 1;
@@ -302,7 +307,9 @@ k_product(const __grid_constant__ ProductMaps tm, const __grid_constant__ Produc
     n0 = (t % NT) * (a.half ? 128 : 256);
   };
 
-  if (warp == 0) {
+  if (skip) {
+    // (on to the end, where the pair meets)
+  } else if (warp == 0) {
     // ---------------- TMA producer (both CTAs) ----------------
     if (lane == 0) {
       int stage = 0, issued = 0;
@@ -393,23 +400,27 @@ k_product(const __grid_constant__ ProductMaps tm, const __grid_constant__ Produc
           if (!queue_take(q, i, true, true, t, abort_flag)) { ok = false; break; }
           if (t < 0) break;
         }
-        if (!mbar_wait(tempty(acc), acc_phase ^ 1u, abort_flag)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t dtm = tmem_base + (uint32_t)(acc * 256);
-        for (int kb = 0; kb < KB; ++kb) {
-          if (!mbar_wait(full(stage), phase, abort_flag)) { ok = false; break; }
+        const int part = F32 ? kPartBlocks : KB;  // what one accumulator sums
+        for (int kp = 0; kp < KB && ok; kp += part) {
+          if (!mbar_wait(tempty(acc), acc_phase ^ 1u, abort_flag)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t sa = smem_u32(smem + stage * Cfg::kStageBytes);
-          const uint32_t sb = sa + Cfg::kABytes;
+          const uint32_t dtm = tmem_base + (uint32_t)(acc * 256);
+          const int end = F32 ? min(kp + part, KB) : KB;
+          for (int kb = kp; kb < end; ++kb) {
+            if (!mbar_wait(full(stage), phase, abort_flag)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t sa = smem_u32(smem + stage * Cfg::kStageBytes);
+            const uint32_t sb = sa + Cfg::kABytes;
 #pragma unroll
-          for (int k = 0; k < kDepth / 16; ++k)
-            Op::mma(dtm, stage_desc(sa, k, AMN), stage_desc(sb, k, BMN), idesc, (kb | k) != 0);
-          Op::commit(empty(stage));
-          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+            for (int k = 0; k < kDepth / 16; ++k)
+              Op::mma(dtm, stage_desc(sa, k, AMN), stage_desc(sb, k, BMN), idesc, kb != kp || k != 0);
+            Op::commit(empty(stage));
+            if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+          }
+          if (!ok) break;
+          Op::commit(tfull(acc));
+          if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
         }
-        if (!ok) break;
-        Op::commit(tfull(acc));
-        if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
       }
       if (!ok) {
         fail();
@@ -419,22 +430,39 @@ k_product(const __grid_constant__ ProductMaps tm, const __grid_constant__ Produc
       }
     }
   } else {
-    // ---------------- epilogue (warps 2..5, both CTAs) ----------------
-    const int qw = warp & 3;  // TMEM lanes 32 qw .. are this warp's rows
-    OutRing ring{out_stage + qw * Cfg::kOutWarpBytes, 0, lane};
+    // ---------------- epilogue (warps 2.., both CTAs) ----------------
+    const int qw = warp & 3;         // TMEM lanes 32 qw .. are this warp's rows
+    const int hs = (warp - 2) >> 2;  // fp32: which half of the columns is this warp's
+    OutRing<Cfg::kOutBuffers> ring{out_stage + (warp - 2) * Cfg::kOutBuffers * 4096, 0, lane};
     const int ocols = a.half ? a.half : a.N;
+    const int parts = F32 ? (KB + kPartBlocks - 1) / kPartBlocks : 1;
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int i = 0;; ++i) {
+    auto take = [&]() {  // the next accumulator, once its sums are complete
+      const bool ok = mbar_wait(tfull(acc), acc_phase, abort_flag);
+      tc_fence_after();
+      return __all_sync(0xffffffffu, ok) != 0;
+    };
+    auto release = [&]() {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (PAIR) mbar_arrive_remote(pair_map(tempty(acc), 0));
+        else mbar_arrive(tempty(acc));
+      }
+      if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+    };
+    auto lanes_at = [&]() {
+      return tmem_base + ((uint32_t)(qw * 32) << 16) + (uint32_t)(acc * 256);
+    };
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
       int t;
       if (DENSE) {
         t = work + i * nwork;
         if (t >= total) break;
       } else {
-        if (!queue_take_warp(q, i, leader, t, abort_flag)) {
-          if (lane == 0) fail();
-          break;
-        }
+        if (!queue_take_warp(q, i, leader, t, abort_flag)) { ok = false; break; }
         if (t < 0) break;
       }
       MTile mt;
@@ -445,65 +473,91 @@ k_product(const __grid_constant__ ProductMaps tm, const __grid_constant__ Produc
       const bool valid = first + lane < mt.rows;
       const bool whole = DENSE || first + 32 <= mt.rows;  // stored as boxes
       const float* bias = a.bias;
-      if (!DENSE && bias != nullptr) {
-        int e = mt.wsel >= 0 ? mt.wsel : p.slot_expert[-1 - mt.wsel];
-        bias += (size_t)e * a.N;
-      }
+      if (!DENSE && bias != nullptr)
+        bias += (size_t)(mt.wsel >= 0 ? mt.wsel : p.slot_expert[-1 - mt.wsel]) * a.N;
       // (lanes past the last row read that one: the warp stays together)
       const uint16_t* residual =
           a.residual != nullptr ? a.residual + (size_t)min(row, a.M - 1) * ocols : nullptr;
-      const bool ok = mbar_wait(tfull(acc), acc_phase, abort_flag);
-      if (!__all_sync(0xffffffffu, ok)) {
-        if (lane == 0) fail();
-        break;
-      }
-      tc_fence_after();
-      const uint32_t tbase = tmem_base + ((uint32_t)(qw * 32) << 16) + (uint32_t)(acc * 256);
+      const bool any = first < mt.rows;  // otherwise none of this warp's rows is stored
       auto put = [&](const uint32_t (&v)[32], const CUtensorMap* m, int x, uint16_t* plain, int pitch,
                      int cols) {
         if (whole) ring.put(v, m, x, mt.row0 + first, false);
         else if (valid) put_row(v, plain + (size_t)row * pitch + x, cols);
-      };
-      // (a warp all of whose rows lie past the last one has nothing to store)
-      const int chunks = first < mt.rows ? (a.half ? 2 : 4) : 0;
-#pragma unroll 1
-      for (int c = 0; c < chunks; ++c) {
-        const int x = n0 + 64 * c;  // first output column
-        const int cols = min(64, ocols - x);
-        if (cols <= 0) break;
         __syncwarp();
-        uint32_t pz[32], pu[32], po[32];
-        float v[32];
-        auto half = [&](auto h) {
-          constexpr int H = decltype(h)::value;
-          if (KIND == kForward)
-            forward32<H>(a, bias, residual, tbase + 64 * c, x, cols, v, pz, pu);
-          else
-            load32(tbase + 64 * c + 32 * H, v);
-          if (DENSE && a.f32) {  // 32 columns a store
+      };
+      auto put_z = [&](const uint32_t (&pz)[32], const uint32_t (&pu)[32], int x, int cols) {
+        if (KIND != kForward || !a.has_z) return;
+        put(pz, &tm.z, x, a.z, a.N, cols);
+        if (a.half) put(pu, &tm.z_up, x, a.z + a.half, a.N, cols);
+      };
+      if constexpr (F32) {
+        float sum[4][32];  // of 128 columns: 64 gates and the 64 up columns of the same numbers for swiglu
+        for (int k = 0; k < parts && ok; ++k) {
+          ok = take();
+          if (!ok) break;
+          // (16 columns at a time: the sums leave few registers)
 #pragma unroll
-            for (int j = 0; j < 32; ++j) po[j] = __float_as_uint(v[j]);
-            if (32 * H < cols) ring.put(po, &tm.out, x + 32 * H, mt.row0 + first, a.add);
-          } else {
-            pack32<H>(po, v);
+          for (int j = 0; j < 8; ++j) {
+            const int at = a.half ? 128 * (j >> 2) + 64 * hs + 16 * (j & 3) : 128 * hs + 16 * j;
+            uint32_t v[16];
+            tmem_ld_x16(lanes_at() + at, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              float& to = sum[j >> 1][16 * (j & 1) + c];
+              to = __uint_as_float(v[c]) + (k == 0 ? 0.f : to);
+            }
           }
-        };
-        half(std::integral_constant<int, 0>());
-        half(std::integral_constant<int, 1>());
-        if (!(DENSE && a.f32)) put(po, &tm.out, x, a.out, ocols, cols);
-        if (KIND == kForward && a.has_z) {
-          put(pz, &tm.z, x, a.z, a.N, cols);
-          if (a.half) put(pu, &tm.z_up, x, a.z + a.half, a.N, cols);
+          release();
         }
+        if (!ok || !any) continue;
+        auto unit = [&](auto number) {  // 64 output columns
+          constexpr int U = decltype(number)::value;
+          const int x = n0 + (a.half ? 64 * hs : 128 * hs + 64 * U);
+          const int cols = min(64, ocols - x);
+          if (cols <= 0) return;
+          uint32_t pz[32], pu[32];
+          auto half = [&](auto h) {
+            constexpr int H = decltype(h)::value;
+            if (KIND == kForward)
+              forward32<H>(a, bias, residual, x, cols, sum[2 * U + H], sum[2 + H], pz, pu);
+            if (32 * H < cols) ring.put(sum[2 * U + H], &tm.out, x + 32 * H, mt.row0 + first, a.add);
+          };
+          half(std::integral_constant<int, 0>());
+          half(std::integral_constant<int, 1>());
+          put_z(pz, pu, x, cols);
+        };
+        unit(std::integral_constant<int, 0>());
+        if (!a.half) unit(std::integral_constant<int, 1>());
+      } else {
+        ok = take();
+        if (!ok) break;
+        const int chunks = any ? (a.half ? 2 : 4) : 0;
+#pragma unroll 1
+        for (int c = 0; c < chunks; ++c) {
+          const int x = n0 + 64 * c;  // first output column
+          const int cols = min(64, ocols - x);
+          if (cols <= 0) break;
+          uint32_t pz[32], pu[32], po[32];
+          auto half = [&](auto h) {
+            constexpr int H = decltype(h)::value;
+            float v[32], u[32];
+            load32(lanes_at() + 64 * c + 32 * H, v);
+            if (KIND == kForward) {
+              if (a.half) load32(lanes_at() + 128 + 64 * c + 32 * H, u);
+              forward32<H>(a, bias, residual, x, cols, v, u, pz, pu);
+            }
+            pack32<H>(po, v);
+          };
+          half(std::integral_constant<int, 0>());
+          half(std::integral_constant<int, 1>());
+          put(po, &tm.out, x, a.out, ocols, cols);
+          put_z(pz, pu, x, cols);
+        }
+        release();
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (PAIR) mbar_arrive_remote(pair_map(tempty(acc), 0));
-        else mbar_arrive(tempty(acc));
-      }
-      if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
     }
+    if (!ok && lane == 0) fail();
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // this warp's stores
     __syncwarp();
   }
@@ -519,35 +573,18 @@ k_product(const __grid_constant__ ProductMaps tm, const __grid_constant__ Produc
 }
 
 // -- host side ------------------------------------------------------------------
-// A row-major matrix [rows][cols] with `pitch` elements a row; boxes of 128 bytes x `box` rows,
-// 128-byte swizzle.
-static bool encode(CUtensorMap* m, const void* base, int cols, int64_t rows, int64_t pitch, int box,
-                   bool f32 = false) {
-  EncodeTiledFn enc = get_encode();
-  if (!enc) return false;
-  const int size = f32 ? 4 : 2;
-  cuuint64_t dim[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  cuuint64_t stride[1] = {(cuuint64_t)(pitch * size)};
-  cuuint32_t b[2] = {(cuuint32_t)(128 / size), (cuuint32_t)box};
-  cuuint32_t one[2] = {1, 1};
-  return enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-             const_cast<void*>(base), dim, stride, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-template <bool PAIR, int KIND, bool DENSE>
+template <bool PAIR, int KIND, bool DENSE, bool F32>
 static cudaError_t launch_one(const ProductMaps& tm, const ProductArgs& a, const PlanPtrs& p,
                               int64_t tiles, cudaStream_t st) {
-  using Cfg = ProductCfg<PAIR>;
+  using Cfg = ProductCfg<PAIR, F32>;
   constexpr int CG = PAIR ? 2 : 1;
-  auto* kernel = k_product<PAIR, KIND, DENSE>;
+  auto* kernel = k_product<PAIR, KIND, DENSE, F32>;
   cudaLaunchAttribute cluster;
   cluster.id = cudaLaunchAttributeClusterDimension;
   cluster.val.clusterDim.x = CG;
   cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kProductThreads);
+  cfg.blockDim = dim3(Cfg::kThreads);
   cfg.dynamicSmemBytes = Cfg::kSmem;
   cfg.stream = st;
   cfg.attrs = &cluster;
@@ -579,34 +616,46 @@ static int64_t tiles_of(int64_t M, int N, int half, int rows) {
 cudaError_t launch_linear(const LinearDims& d, const void* x, const void* w, const float* bias,
                           const void* residual, void* out, void* z, int32_t* status, cudaStream_t st,
                           int* launches) {
+  const SplitPlan split = plan_split(d.T, d.N, d.half, d.K);
+  if (split.splits) {
+    *launches += 1;
+    return launch_split(kForward, d, split, x, w, bias, residual, out, z, status, st);
+  }
   ProductMaps tm;
   const int ocols = d.half ? d.half : d.N;
-  if (!encode(&tm.a, x, d.K, d.T, d.K, 128) || !encode(&tm.b, w, d.N, d.K, d.N, 64) ||
-      !encode(&tm.out, out, ocols, d.T, ocols, 32, d.f32))
+  if (!encode_matrix(&tm.a, x, d.K, d.T, d.K, 128) || !encode_matrix(&tm.b, w, d.N, d.K, d.N, 64) ||
+      !encode_matrix(&tm.out, out, ocols, d.T, ocols, 32, d.f32))
     return cudaErrorInvalidValue;
   tm.b_slots = tm.b;
   tm.z = tm.z_up = tm.out;
   if (z != nullptr) {  // the halves have maps of their own, so that either is clipped at its end
-    if (!encode(&tm.z, z, ocols, d.T, d.N, 32)) return cudaErrorInvalidValue;
-    if (d.half && !encode(&tm.z_up, (uint16_t*)z + d.half, ocols, d.T, d.N, 32))
+    if (!encode_matrix(&tm.z, z, ocols, d.T, d.N, 32)) return cudaErrorInvalidValue;
+    if (d.half && !encode_matrix(&tm.z_up, (uint16_t*)z + d.half, ocols, d.T, d.N, 32))
       return cudaErrorInvalidValue;
   }
   ProductArgs a = {};
   a.M = d.T, a.N = d.N, a.K = d.K;
-  a.act = d.act, a.half = d.half, a.f32 = d.f32;
+  a.act = d.act, a.half = d.half;
   a.bias = bias;
   a.residual = (const uint16_t*)residual;
   a.has_z = z != nullptr;
   a.status = status;
   *launches += 1;
-  return launch_one<true, kForward, true>(tm, a, PlanPtrs{}, tiles_of(d.T, d.N, d.half, 256), st);
+  const int64_t tiles = tiles_of(d.T, d.N, d.half, 256);
+  return d.f32 ? launch_one<true, kForward, true, true>(tm, a, PlanPtrs{}, tiles, st)
+               : launch_one<true, kForward, true, false>(tm, a, PlanPtrs{}, tiles, st);
 }
 
 cudaError_t launch_linear_dx(const LinearDims& d, const void* d_z, const void* w, void* d_x,
                              int32_t* status, cudaStream_t st, int* launches) {
+  const SplitPlan split = plan_split(d.T, d.K, 0, d.N);
+  if (split.splits) {
+    *launches += 1;
+    return launch_split(kInputGrad, d, split, d_z, w, nullptr, nullptr, d_x, nullptr, status, st);
+  }
   ProductMaps tm;
-  if (!encode(&tm.a, d_z, d.N, d.T, d.N, 128) || !encode(&tm.b, w, d.N, d.K, d.N, 128) ||
-      !encode(&tm.out, d_x, d.K, d.T, d.K, 32))
+  if (!encode_matrix(&tm.a, d_z, d.N, d.T, d.N, 128) || !encode_matrix(&tm.b, w, d.N, d.K, d.N, 128) ||
+      !encode_matrix(&tm.out, d_x, d.K, d.T, d.K, 32))
     return cudaErrorInvalidValue;
   tm.b_slots = tm.b;
   tm.z = tm.z_up = tm.out;
@@ -614,23 +663,23 @@ cudaError_t launch_linear_dx(const LinearDims& d, const void* d_z, const void* w
   a.M = d.T, a.N = d.K, a.K = d.N;
   a.status = status;
   *launches += 1;
-  return launch_one<true, kInputGrad, true>(tm, a, PlanPtrs{}, tiles_of(d.T, d.K, 0, 256), st);
+  return launch_one<true, kInputGrad, true, false>(tm, a, PlanPtrs{}, tiles_of(d.T, d.K, 0, 256), st);
 }
 
 cudaError_t launch_linear_dw(const LinearDims& d, const void* x, const void* d_z, float* d_w,
                              int add, int32_t* status, cudaStream_t st, int* launches) {
   ProductMaps tm;
-  if (!encode(&tm.a, x, d.K, d.T, d.K, 64) || !encode(&tm.b, d_z, d.N, d.T, d.N, 64) ||
-      !encode(&tm.out, d_w, d.N, d.K, d.N, 32, true))
+  if (!encode_matrix(&tm.a, x, d.K, d.T, d.K, 64) || !encode_matrix(&tm.b, d_z, d.N, d.T, d.N, 64) ||
+      !encode_matrix(&tm.out, d_w, d.N, d.K, d.N, 32, true))
     return cudaErrorInvalidValue;
   tm.b_slots = tm.b;
   tm.z = tm.z_up = tm.out;
   ProductArgs a = {};
   a.M = d.K, a.N = d.N, a.K = d.T;
-  a.f32 = 1, a.add = add;
+  a.add = add;
   a.status = status;
   *launches += 1;
-  return launch_one<true, kWeightGrad, true>(tm, a, PlanPtrs{}, tiles_of(d.K, d.N, 0, 256), st);
+  return launch_one<true, kWeightGrad, true, true>(tm, a, PlanPtrs{}, tiles_of(d.K, d.N, 0, 256), st);
 }
 
 cudaError_t launch_grouped_gemm_act(const Dims& d, const PlanPtrs& p, int act, const void* recv,
@@ -640,17 +689,17 @@ cudaError_t launch_grouped_gemm_act(const Dims& d, const PlanPtrs& p, int act, c
   const int half = act == kActSwiglu ? d.Hp / 2 : 0;
   const int ocols = half ? half : d.Hp;
   const bool slots = w_slot != nullptr && d.B > 0;
-  if (!encode(&tm.a, recv, d.H, d.N, d.H, 128) ||
-      !encode(&tm.b, w_home, d.Hp, (int64_t)d.E * d.H, d.Hp, 64) ||
-      !encode(&tm.out, y, ocols, d.N, ocols, 32))
+  if (!encode_matrix(&tm.a, recv, d.H, d.N, d.H, 128) ||
+      !encode_matrix(&tm.b, w_home, d.Hp, (int64_t)d.E * d.H, d.Hp, 64) ||
+      !encode_matrix(&tm.out, y, ocols, d.N, ocols, 32))
     return cudaErrorInvalidValue;
   tm.b_slots = tm.b;
-  if (slots && !encode(&tm.b_slots, w_slot, d.Hp, (int64_t)d.R * d.B * d.H, d.Hp, 64))
+  if (slots && !encode_matrix(&tm.b_slots, w_slot, d.Hp, (int64_t)d.R * d.B * d.H, d.Hp, 64))
     return cudaErrorInvalidValue;
   tm.z = tm.z_up = tm.out;
   if (z != nullptr) {
-    if (!encode(&tm.z, z, ocols, d.N, d.Hp, 32)) return cudaErrorInvalidValue;
-    if (half && !encode(&tm.z_up, (uint16_t*)z + half, ocols, d.N, d.Hp, 32))
+    if (!encode_matrix(&tm.z, z, ocols, d.N, d.Hp, 32)) return cudaErrorInvalidValue;
+    if (half && !encode_matrix(&tm.z_up, (uint16_t*)z + half, ocols, d.N, d.Hp, 32))
       return cudaErrorInvalidValue;
   }
   ProductArgs a = {};
@@ -664,12 +713,12 @@ cudaError_t launch_grouped_gemm_act(const Dims& d, const PlanPtrs& p, int act, c
   // with the height left to the plan both are launched; the one it did not choose returns at once
   const int64_t tiles = (int64_t)d.max_mtiles * (half ? (half + 127) / 128 : (d.Hp + 255) / 256);
   if (d.tile_m != 2 * kMmaM) {
-    const cudaError_t e = launch_one<false, kForward, false>(tm, a, p, tiles, st);
+    const cudaError_t e = launch_one<false, kForward, false, false>(tm, a, p, tiles, st);
     if (e != cudaSuccess) return e;
     *launches += 1;
   }
   if (d.tile_m != kMmaM) {
-    const cudaError_t e = launch_one<true, kForward, false>(tm, a, p, tiles, st);
+    const cudaError_t e = launch_one<true, kForward, false, false>(tm, a, p, tiles, st);
     if (e != cudaSuccess) return e;
     *launches += 1;
   }
