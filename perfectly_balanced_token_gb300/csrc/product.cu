@@ -26,12 +26,6 @@
 
 namespace moonep {
 
-// Blocks of the depth that one accumulator sums where C is fp32.  The instruction cuts off what its
-// fp32 sums do not hold, always towards zero, so a long sum drifts: against 64 bits, with the whole
-// depth in one accumulator, 7e-6 of C at a depth of 7168 and past 1e-5 at 32768.  The epilogue adds the
-// parts in registers, rounding to nearest.  (A bf16 C's own rounding is 250 times larger.)
-constexpr int kPartBlocks = 32;
-
 template <bool PAIR, bool F32>
 struct ProductCfg {
   // fp32 sums of 128 columns a thread take eight epilogue warps

@@ -10,6 +10,12 @@ namespace moonep {
 constexpr int kDepth = 64;             // of a stage: 64 bf16 = one 128-byte swizzle row
 constexpr int kPanelBytes = 64 * 128;  // 64 rows of 64 bf16
 
+// Blocks of the depth that one accumulator sums where C is fp32.  The instruction cuts off what its
+// fp32 sums do not hold, always towards zero, so a long sum drifts: against 64 bits, with the whole
+// depth in one accumulator, 7e-6 of C at a depth of 7168 and past 2e-5 at 32768.  The epilogues add
+// the parts in registers, rounding to nearest.  (A bf16 C's own rounding is 250 times larger.)
+constexpr int kPartBlocks = 16;
+
 enum Kind { kForward, kInputGrad, kWeightGrad };
 
 // kind::f16: fp32 accumulator, bf16 operands; which of them run along M or N in memory

@@ -15,7 +15,8 @@
 
 namespace moonep {
 
-constexpr int kSplitThreads = 256;
+// (the reduction is short chains of dependent instructions: eight warps took 2.2 times as long)
+constexpr int kSplitThreads = 512;
 constexpr int kSplitWarps = kSplitThreads / 32;
 constexpr int kSplitStages = 12;          // at most
 constexpr int kSplitRing = 204 * 1024;    // bytes of stages, at most
@@ -25,7 +26,7 @@ static_assert(kSplitSmem <= 232448, "shared memory of a CTA");
 struct SplitArgs {
   int T, columns, depth;  // rows of x, columns of w (or rows, input gradient), depth
   int half, act, f32;
-  int tokens, splits, stages;
+  int tokens, splits, stages, parts;
   const float* bias;
   const uint16_t* residual;
   void* out;
@@ -33,24 +34,27 @@ struct SplitArgs {
   int32_t* status;
 };
 
-// four columns' partial sums, added in rank order
-__device__ __forceinline__ void add_parts(float (&v)[4], const float* at, int stride, int splits) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = 0.f;
-#pragma unroll 4
-  for (int s = 0; s < splits; ++s) {
-    const float4 f = *reinterpret_cast<const float4*>(at + (size_t)s * stride);
-    v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
+// Four tokens' partial sums of a column, added in rank order.
+__device__ __forceinline__ float4 add_parts(const float4* at, int stride, int splits) {
+  float4 v = *at;
+#pragma unroll 2
+  for (int s = 1; s < splits; ++s) {
+    at += stride;
+    const float4 f = *at;
+    v.x += f.x, v.y += f.y, v.z += f.z, v.w += f.w;
   }
+  return v;
 }
-__device__ __forceinline__ void add_bias4(float (&v)[4], const float* bias) {
-  if (bias == nullptr) return;
-  const float4 f = __ldg(reinterpret_cast<const float4*>(bias));
-  v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
-}
-__device__ __forceinline__ void store4(uint16_t* at, const float (&v)[4]) {
-  *reinterpret_cast<uint2*>(at) = make_uint2(pack_bf16x2(__float_as_uint(v[0]), __float_as_uint(v[1])),
-                                             pack_bf16x2(__float_as_uint(v[2]), __float_as_uint(v[3])));
+
+// act of the two columns' four tokens
+__device__ __forceinline__ void act_pairs(int act, float (&v)[2][4]) {
+  auto each = [&](auto f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i >> 2][i & 3] = f(v[i >> 2][i & 3]);
+  };
+  if (act == kActRelu) each([](float z) { return act_value(kActRelu, z); });
+  else if (act == kActGelu) each([](float z) { return act_value(kActGelu, z); });
+  else if (act == kActSilu) each([](float z) { return act_value(kActSilu, z); });
 }
 
 template <int KIND>
@@ -79,7 +83,8 @@ k_product_split(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
   const int kb0 = (int)((int64_t)KB * rank / S), kb1 = (int)((int64_t)KB * (rank + 1) / S);
   const uint32_t stage_bytes = 2 * kPanelBytes + a.tokens * 128;
   const int stages = a.stages;
-  const uint32_t tmem_cols = a.tokens <= 32 ? 32 : (a.tokens <= 64 ? 64 : (a.tokens <= 128 ? 128 : 256));
+  const uint32_t span = a.tokens <= 32 ? 32 : (a.tokens <= 64 ? 64 : (a.tokens <= 128 ? 128 : 256));
+  const uint32_t tmem_cols = span * a.parts;  // a.parts is a power of two
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
@@ -140,15 +145,19 @@ k_product_split(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int kb = kb0; kb < kb1; ++kb) {
+      // the depth's parts, one after the other, have an accumulator each
+      const int blocks = kb1 - kb0, of_part = (blocks + a.parts - 1) / a.parts;
+      uint32_t acc = tmem_base;
+      for (int kb = 0, left = 0; kb < blocks; ++kb) {
         if (!mbar_wait(full(stage), phase, abort_flag)) { ok = false; break; }
         tc_fence_after();
+        if (left == 0 && kb != 0) acc += span;
         const uint32_t sa = smem_u32(smem) + stage * stage_bytes;
         const uint32_t sb = sa + 2 * kPanelBytes;
 #pragma unroll
         for (int k = 0; k < kDepth / 16; ++k)
-          umma_bf16(tmem_base, stage_desc(sa, k, AMN), stage_desc(sb, k, false), idesc,
-                    kb != kb0 || k != 0);
+          umma_bf16(acc, stage_desc(sa, k, AMN), stage_desc(sb, k, false), idesc, left != 0 || k != 0);
+        if (++left == of_part) left = 0;
         umma_commit(empty(stage));
         if (++stage == stages) { stage = 0; phase ^= 1u; }
       }
@@ -169,25 +178,36 @@ k_product_split(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
   tc_fence_after();
   if (S > 1) pair_sync();
 
-  const int valid = min(a.tokens, a.T - t0);  // rows of this tile
-  const int per = (valid + S - 1) / S;        // that a CTA owns
-  const uint32_t red = smem_u32(smem);        // [splits][per][128] partial sums
+  const int valid = min(a.tokens, a.T - t0);   // rows of this tile
+  const int fours = (valid + 3) / 4;           // in groups of four
+  const int per = (fours + S - 1) / S;         // groups that a CTA owns
+  const uint32_t red = smem_u32(smem);         // [splits][per][128 columns][4 tokens] partial sums
   if (ok) {
     const int qw = warp & 3;  // TMEM lanes 32 qw .. : columns of w
-#pragma unroll 1
-    for (int t = 16 * (warp >> 2); t < valid; t += 16 * (kSplitWarps / 4)) {
+    const int of_part = (kb1 - kb0 + a.parts - 1) / a.parts;
+    const int filled = (kb1 - kb0 + of_part - 1) / of_part;  // parts that hold a sum
+    const uint32_t own = red + (rank * per * 128 + qw * 32 + lane) * 16;
+    for (int g = 4 * (warp >> 2); g < fours; g += 4 * (kSplitWarps / 4)) {
+      const uint32_t at = tmem_base + ((uint32_t)(qw * 32) << 16) + (uint32_t)(4 * g);
       uint32_t r[16];
-      tmem_ld_x16(tmem_base + ((uint32_t)(qw * 32) << 16) + (uint32_t)t, r);
+      tmem_ld_x16(at, r);
       tmem_ld_wait();
-      int owner = t / per, local = t - owner * per;
+      for (int k = 1; k < filled; ++k) {
+        uint32_t more[16];
+        tmem_ld_x16(at + k * span, more);
+        tmem_ld_wait();
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        if (t + j < valid) {
-          const uint32_t at = red + (((rank * per + local) * 128) + qw * 32 + lane) * 4;
-          if (S > 1)
-            asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(pair_map(at, owner)), "r"(r[j]) : "memory");
-          else
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(r[j]) : "memory");
+        for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(more[j]));
+      }
+      int owner = S > 1 ? g / per : 0, local = g - owner * per;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (g + j < fours) {
+          uint32_t to = own + local * (128 * 16);
+          if (S > 1) to = pair_map(to, owner);
+          asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(r[4 * j]),
+                       "r"(r[4 * j + 1]), "r"(r[4 * j + 2]), "r"(r[4 * j + 3])
+                       : "memory");
         }
         if (++local == per) { local = 0; ++owner; }
       }
@@ -198,39 +218,84 @@ k_product_split(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
   if (S > 1) pair_sync();
 
   if (ok) {
-    const float* sums = reinterpret_cast<const float*>(smem);
-    const int mine = min(per, valid - rank * per);
-    const int width = a.half ? 16 : 32;  // lanes a row, four columns each
-    const int col = 4 * (lane & (width - 1)), x = c0 + col;
-    for (int l = (threadIdx.x / width); l < mine; l += kSplitThreads / width) {
-      if (x >= ncols) break;
-      const size_t row = (size_t)(t0 + rank * per + l);
-      float v[4];
-      add_parts(v, sums + l * 128 + col, per * 128, S);
-      if (KIND == kForward) {
-        add_bias4(v, a.bias ? a.bias + x : nullptr);
-        if (a.z != nullptr) store4(a.z + row * a.columns + x, v);
-        if (a.half) {
-          float u[4];
-          add_parts(u, sums + l * 128 + 64 + col, per * 128, S);
-          add_bias4(u, a.bias ? a.bias + a.half + x : nullptr);
-          if (a.z != nullptr) store4(a.z + row * a.columns + a.half + x, u);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = v[i] * sigmoid_f(v[i]) * u[i];
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = act_value(a.act, v[i]);
-        }
-        if (a.residual != nullptr) {
-          const uint2 r = __ldg(reinterpret_cast<const uint2*>(a.residual + row * ncols + x));
-          v[0] += __uint_as_float(r.x << 16), v[1] += __uint_as_float(r.x & 0xffff0000u);
-          v[2] += __uint_as_float(r.y << 16), v[3] += __uint_as_float(r.y & 0xffff0000u);
-        }
+    // a lane has two columns (and, for swiglu, the two of the same numbers in the up half), a warp
+    // 64 columns of every 8th (16th) group
+    const int mine = min(per, fours - rank * per);
+    const int c = 2 * lane + (a.half ? 0 : 64 * (warp & 1)), x = c0 + c;
+    const int step = a.half ? kSplitWarps : kSplitWarps / 2;
+    const int g0 = a.half ? warp : warp >> 1;
+    if (x < ncols && g0 < mine) {
+      const float4* sums = reinterpret_cast<const float4*>(smem) + g0 * 128 + c;
+      const int stride = per * 128;
+      const bool biased = KIND == kForward && a.bias != nullptr;
+      float2 bias = make_float2(0.f, 0.f), bias_up = bias;
+      if (biased) {
+        bias = __ldg(reinterpret_cast<const float2*>(a.bias + x));
+        if (a.half) bias_up = __ldg(reinterpret_cast<const float2*>(a.bias + a.half + x));
       }
-      if (a.f32)
-        *reinterpret_cast<float4*>((float*)a.out + row * ncols + x) = make_float4(v[0], v[1], v[2], v[3]);
-      else
-        store4((uint16_t*)a.out + row * ncols + x, v);
+      auto get = [&](float (&to)[2][4], int at, float2 b) {
+        const float4 p = add_parts(sums + at, stride, S), q = add_parts(sums + at + 1, stride, S);
+        to[0][0] = p.x, to[0][1] = p.y, to[0][2] = p.z, to[0][3] = p.w;
+        to[1][0] = q.x, to[1][1] = q.y, to[1][2] = q.z, to[1][3] = q.w;
+        if (biased) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) to[0][j] += b.x, to[1][j] += b.y;
+        }
+      };
+      const int first = 4 * (rank * per + g0);  // token of the tile
+      size_t at = (size_t)(t0 + first) * ncols + x, at_z = (size_t)(t0 + first) * a.columns + x;
+#pragma unroll 1
+      for (int left = valid - first, g = g0; g < mine; g += step, left -= 4 * step) {
+        auto put = [&](uint16_t* to, int pitch, const float (&f)[2][4]) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j, to += pitch)
+            if (j < left)
+              *reinterpret_cast<uint32_t*>(to) =
+                  pack_bf16x2(__float_as_uint(f[0][j]), __float_as_uint(f[1][j]));
+        };
+        float v[2][4];
+        get(v, 0, bias);
+        if (KIND == kForward) {
+          uint32_t res[4] = {};
+          if (a.residual != nullptr) {
+            const uint16_t* r = a.residual + at;
+#pragma unroll
+            for (int j = 0; j < 4; ++j, r += ncols)
+              if (j < left) res[j] = __ldg(reinterpret_cast<const uint32_t*>(r));
+          }
+          if (a.z != nullptr) put(a.z + at_z, a.columns, v);
+          if (a.half) {
+            float u[2][4];
+            get(u, 64, bias_up);
+            if (a.z != nullptr) put(a.z + at_z + a.half, a.columns, u);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float& z = v[i >> 2][i & 3];
+              z = z * sigmoid_f(z) * u[i >> 2][i & 3];
+            }
+          } else if (a.act != kActNone) {
+            act_pairs(a.act, v);
+          }
+          if (a.residual != nullptr) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              v[0][j] += __uint_as_float(res[j] << 16);
+              v[1][j] += __uint_as_float(res[j] & 0xffff0000u);
+            }
+          }
+        }
+        if (a.f32) {
+          float* o = (float*)a.out + at;
+#pragma unroll
+          for (int j = 0; j < 4; ++j, o += ncols)
+            if (j < left) *reinterpret_cast<float2*>(o) = make_float2(v[0][j], v[1][j]);
+        } else {
+          put((uint16_t*)a.out + at, ncols, v);
+        }
+        sums += step * 128;
+        at += (size_t)(4 * step) * ncols;
+        at_z += (size_t)(4 * step) * a.columns;
+      }
     }
   }
   __syncthreads();
@@ -322,6 +387,12 @@ cudaError_t launch_split(Kind kind, const LinearDims& d, SplitPlan plan, const v
   if (!encode_matrix(&tx, x, a.depth, d.T, a.depth, plan.tokens)) return cudaErrorInvalidValue;
   const int64_t CT = a.half ? (a.half + 63) / 64 : (a.columns + 127) / 128;
   const int64_t ctas = ((d.T + plan.tokens - 1) / plan.tokens) * CT * plan.splits;
+  a.parts = 1;
+  if (a.f32) {
+    const int blocks = ((a.depth + kDepth - 1) / kDepth + plan.splits - 1) / plan.splits;
+    const int span = plan.tokens <= 32 ? 32 : (plan.tokens <= 64 ? 64 : (plan.tokens <= 128 ? 128 : 256));
+    while (a.parts * kPartBlocks < blocks && a.parts * span < 512) a.parts *= 2;
+  }
   return kind == kForward ? launch_kind<kForward>(tw, tx, a, ctas, st)
                           : launch_kind<kInputGrad>(tw, tx, a, ctas, st);
 }
