@@ -4,6 +4,7 @@
 
 #include "activation.cuh"
 #include "ffn.h"
+#include "pdl.cuh"
 #include "vec.cuh"
 
 namespace moonep {
@@ -30,9 +31,11 @@ struct ActArgs {
 };
 
 template <int ACT>
-__global__ void __launch_bounds__(kActThreads) k_act_backward(ActArgs a, PlanPtrs p, int plan) {
+__global__ void __launch_bounds__(kActThreads, 2) k_act_backward(ActArgs a, PlanPtrs p, int plan) {
   constexpr bool GATED = ACT == kActSwiglu;
   __shared__ float part[GATED ? 2 : 1][kActWarps][kActCols];
+  grid_wait();
+  grid_trigger();
   // plan: 0 = none, 1 = chunks are its work tiles, 2 = only its status counts
   if (plan && plan_failed(p.status)) return;
   const bool grouped = plan == 1;
@@ -126,6 +129,8 @@ __global__ void __launch_bounds__(kActThreads) k_act_backward(ActArgs a, PlanPtr
 __global__ void __launch_bounds__(1024) k_sum_chunks(const float* __restrict__ sums, int64_t chunks,
                                                      int cols, float* __restrict__ d_bias, int add) {
   __shared__ float part[32][33];
+  grid_wait();
+  grid_trigger();
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5, c = blockIdx.x * 32 + x;
   float s = 0.f;
   if (c < cols)
@@ -140,20 +145,22 @@ __global__ void __launch_bounds__(1024) k_sum_chunks(const float* __restrict__ s
   }
 }
 
-// The same for each expert over its work tiles: a block an expert, which picks the expert's tiles
-// out of the plan's list, 1024 at a time and in order, and adds their rows of sums.
+// The same for each expert over its work tiles: a block an expert and 1024 columns, which picks the
+// expert's tiles out of the plan's list, 1024 at a time and in order, and adds their rows of sums.
 constexpr int kPickThreads = 1024;
 __global__ void __launch_bounds__(kPickThreads)
 k_sum_tiles(PlanPtrs p, const float* __restrict__ sums, int cols, float* __restrict__ d_bias, int add) {
   __shared__ int picked[kPickThreads];
   __shared__ int count[kPickThreads / 32];
+  grid_wait();
+  grid_trigger();
   if (plan_failed(p.status)) return;
-  const int e = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int e = blockIdx.x, c = blockIdx.y * kPickThreads + threadIdx.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int tiles = p.counters[MOONEP_CNT_MTILES];
-  for (int c = tid; c < cols; c += kPickThreads)
-    if (!add) d_bias[(size_t)e * cols + c] = 0.f;
+  float s = 0.f;
   for (int t0 = 0; t0 < tiles; t0 += kPickThreads) {
-    const int t = t0 + tid;
+    const int t = t0 + threadIdx.x;
     bool mine = false;
     if (t < tiles) {
       const int w = p.mtiles[t].wsel;
@@ -170,14 +177,15 @@ k_sum_tiles(PlanPtrs p, const float* __restrict__ sums, int cols, float* __restr
     }
     if (mine) picked[before + __popc(b & ((1u << lane) - 1))] = t;
     __syncthreads();
-    if (n > 0)
-      for (int c = tid; c < cols; c += kPickThreads) {
-        float s = d_bias[(size_t)e * cols + c];
+    if (c < cols) {
 #pragma unroll 4
-        for (int i = 0; i < n; ++i) s += sums[(size_t)picked[i] * cols + c];
-        d_bias[(size_t)e * cols + c] = s;
-      }
+      for (int i = 0; i < n; ++i) s += sums[(size_t)picked[i] * cols + c];
+    }
     __syncthreads();
+  }
+  if (c < cols) {
+    float* to = d_bias + (size_t)e * cols + c;
+    *to = add ? *to + s : s;
   }
 }
 
@@ -189,12 +197,12 @@ static cudaError_t launch_act(int act, const ActArgs& a, const PlanPtrs& p, int 
   const int ocols = act == kActSwiglu ? a.cols / 2 : a.cols;
   const int64_t items = chunks * ((ocols + kActCols - 1) / kActCols);
   const int grid = (int)std::min<int64_t>(items, (int64_t)sm_count_gemm() * 16);
-  if (act == kActNone) k_act_backward<kActNone><<<grid, kActThreads, 0, st>>>(a, p, plan);
-  else if (act == kActRelu) k_act_backward<kActRelu><<<grid, kActThreads, 0, st>>>(a, p, plan);
-  else if (act == kActGelu) k_act_backward<kActGelu><<<grid, kActThreads, 0, st>>>(a, p, plan);
-  else if (act == kActSilu) k_act_backward<kActSilu><<<grid, kActThreads, 0, st>>>(a, p, plan);
-  else k_act_backward<kActSwiglu><<<grid, kActThreads, 0, st>>>(a, p, plan);
-  return cudaGetLastError();
+  auto go = [&](auto kernel) { return launch_after(kernel, grid, kActThreads, 0, st, 1, a, p, plan); };
+  if (act == kActNone) return go(k_act_backward<kActNone>);
+  if (act == kActRelu) return go(k_act_backward<kActRelu>);
+  if (act == kActGelu) return go(k_act_backward<kActGelu>);
+  if (act == kActSilu) return go(k_act_backward<kActSilu>);
+  return go(k_act_backward<kActSwiglu>);
 }
 
 cudaError_t launch_act_backward(int64_t rows, int cols, int act, const void* z, const void* d_out,
@@ -208,9 +216,9 @@ cudaError_t launch_act_backward(int64_t rows, int cols, int act, const void* z, 
     *launches += 1;
   }
   if (e != cudaSuccess || d_bias == nullptr) return e;
-  k_sum_chunks<<<(cols + 31) / 32, 1024, 0, st>>>(scratch, act_chunks(rows), cols, d_bias, add);
   *launches += 1;
-  return cudaGetLastError();
+  return launch_after(k_sum_chunks, (cols + 31) / 32, 1024, 0, st, 1, scratch, act_chunks(rows), cols,
+                      d_bias, add);
 }
 
 cudaError_t launch_grouped_act_backward(const Dims& d, const PlanPtrs& p, int act, const void* z,
@@ -222,9 +230,9 @@ cudaError_t launch_grouped_act_backward(const Dims& d, const PlanPtrs& p, int ac
   const cudaError_t e = launch_act(act, a, p, d_bias ? 1 : 2, d_bias ? d.max_mtiles : act_chunks(d.N), st);
   *launches += 1;
   if (e != cudaSuccess || d_bias == nullptr) return e;
-  k_sum_tiles<<<d.E, kPickThreads, 0, st>>>(p, scratch, d.Hp, d_bias, add);
   *launches += 1;
-  return cudaGetLastError();
+  return launch_after(k_sum_tiles, dim3(d.E, (d.Hp + kPickThreads - 1) / kPickThreads), kPickThreads, 0,
+                      st, 1, p, scratch, d.Hp, d_bias, add);
 }
 
 }  // namespace moonep

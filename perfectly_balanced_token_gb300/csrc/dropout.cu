@@ -3,6 +3,7 @@
 #include <algorithm>
 
 #include "ffn.h"
+#include "pdl.cuh"
 #include "vec.cuh"
 
 namespace moonep {
@@ -54,6 +55,8 @@ template <int KC, bool DROP, bool RES>
 __global__ void __launch_bounds__(kRowThreads)
 k_combine_dropout(Dims d, PlanPtrs p, const uint4* __restrict__ y, const float* __restrict__ gates,
                   const uint4* __restrict__ residual, uint4* __restrict__ out, Dropout drop) {
+  grid_wait();
+  grid_trigger();
   if (plan_failed(p.status)) return;
   const int hv = d.Hp / 8;
   const int ntok = d.R * d.S;
@@ -108,6 +111,8 @@ k_combine_dropout_bwd(Dims d, PlanPtrs p, const uint4* __restrict__ y,
                       const float* __restrict__ gates, const uint4* __restrict__ dout,
                       uint4* __restrict__ dy, float* __restrict__ dgates, Dropout drop) {
   __shared__ float part[kRowThreads / 32][kDropMaxK];
+  grid_wait();
+  grid_trigger();
   if (plan_failed(p.status)) return;
   const int hv = d.Hp / 8;
   const int ntok = d.R * d.S;
@@ -189,9 +194,10 @@ cudaError_t launch_combine_dropout(const Dims& d, const PlanPtrs& p, const void*
                                    const void* residual, void* out, const Dropout& drop,
                                    cudaStream_t st, int* launches) {
   const int grid = std::min(d.R * d.S, sm_count_gemm() * 16);
+  cudaError_t e = cudaSuccess;
   auto go = [&](auto kernel) {
-    kernel<<<grid, kRowThreads, 0, st>>>(d, p, (const uint4*)y, gates, (const uint4*)residual,
-                                         (uint4*)out, drop);
+    e = launch_after(kernel, grid, kRowThreads, 0, st, 1, d, p, (const uint4*)y, gates,
+                     (const uint4*)residual, (uint4*)out, drop);
   };
   const bool r = residual != nullptr;
   if (drop.cut) {
@@ -202,7 +208,7 @@ cudaError_t launch_combine_dropout(const Dims& d, const PlanPtrs& p, const void*
     else r ? go(k_combine_dropout<4, false, true>) : go(k_combine_dropout<4, false, false>);
   }
   *launches += 1;
-  return cudaGetLastError();
+  return e;
 }
 
 cudaError_t launch_combine_dropout_backward(const Dims& d, const PlanPtrs& p, const void* y,
@@ -211,9 +217,10 @@ cudaError_t launch_combine_dropout_backward(const Dims& d, const PlanPtrs& p, co
                                             int* launches) {
   const int grid = std::min(d.R * d.S, sm_count_gemm() * 16);
   const int vpt = (d.Hp / 8 + kRowThreads - 1) / kRowThreads;
+  cudaError_t e = cudaSuccess;
   auto go = [&](auto kernel) {
-    kernel<<<grid, kRowThreads, 0, st>>>(d, p, (const uint4*)y, gates, (const uint4*)d_out,
-                                         (uint4*)d_y, d_gates, drop);
+    e = launch_after(kernel, grid, kRowThreads, 0, st, 1, d, p, (const uint4*)y, gates,
+                     (const uint4*)d_out, (uint4*)d_y, d_gates, drop);
   };
   const bool m = drop.cut != 0;
   // KC x VPT row vectors in flight in a thread: 8 for every row width
@@ -223,7 +230,7 @@ cudaError_t launch_combine_dropout_backward(const Dims& d, const PlanPtrs& p, co
   else if (vpt <= 8) m ? go(k_combine_dropout_bwd<8, 1, true>) : go(k_combine_dropout_bwd<8, 1, false>);
   else return cudaErrorInvalidValue;
   *launches += 1;
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace moonep

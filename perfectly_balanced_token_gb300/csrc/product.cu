@@ -234,7 +234,10 @@ k_product(const __grid_constant__ ProductMaps tm, const __grid_constant__ Produc
   const bool leader = crank == 0;
   const int nwork = PAIR ? gridDim.x >> 1 : gridDim.x;   // pairs or CTAs
   const int work = PAIR ? blockIdx.x >> 1 : blockIdx.x;  // this one
-  if (!DENSE && p.counters[MOONEP_CNT_TILE_ROWS] != Cfg::kTileM) return;
+  if (!DENSE) {
+    grid_wait();
+    if (p.counters[MOONEP_CNT_TILE_ROWS] != Cfg::kTileM) return;
+  }
   const int NT = a.half ? (a.half + 127) / 128 : (a.N + 255) / 256;
   const int MT = DENSE ? (a.M + Cfg::kTileM - 1) / Cfg::kTileM : p.counters[MOONEP_CNT_MTILES];
   const int total = MT * NT;
@@ -253,8 +256,9 @@ k_product(const __grid_constant__ ProductMaps tm, const __grid_constant__ Produc
     mbar_init(drain, 1);
     if (!DENSE) queue_init(q, PAIR ? kQueueConsumers : kQueueConsumersSolo);
     *abort_flag = 0;
-    *dead = plan_failed(a.status);
     fence_barrier_init();
+    if (DENSE) grid_wait();
+    *dead = plan_failed(a.status);
   }
   if (warp == 0 && lane == 0) {
     prefetch_tmap(&tm.a);
@@ -275,6 +279,8 @@ k_product(const __grid_constant__ ProductMaps tm, const __grid_constant__ Produc
   tc_fence_after();
   if (PAIR) pair_sync();  // the peer's barriers are initialised before anything reaches them
   const uint32_t tmem_base = *tmem_slot;
+  if (DENSE) grid_wait();  // (what is above runs while the kernel before this one ends)
+  grid_trigger();
   // both CTAs go by what either found in the status word: another pair may set it meanwhile
   int skip = *dead;
   if (PAIR) {
@@ -573,16 +579,6 @@ static cudaError_t launch_one(const ProductMaps& tm, const ProductArgs& a, const
   using Cfg = ProductCfg<PAIR, F32>;
   constexpr int CG = PAIR ? 2 : 1;
   auto* kernel = k_product<PAIR, KIND, DENSE, F32>;
-  cudaLaunchAttribute cluster;
-  cluster.id = cudaLaunchAttributeClusterDimension;
-  cluster.val.clusterDim.x = CG;
-  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(Cfg::kThreads);
-  cfg.dynamicSmemBytes = Cfg::kSmem;
-  cfg.stream = st;
-  cfg.attrs = &cluster;
-  cfg.numAttrs = PAIR ? 1 : 0;
   static PerDevice kept;
   int most = 0;  // CTAs (pairs) that run at once
   const cudaError_t e = kept(&most, [&](int* found) {
@@ -590,17 +586,24 @@ static cudaError_t launch_one(const ProductMaps& tm, const ProductArgs& a, const
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
     if (e != cudaSuccess) return e;
     if (!PAIR) return *found = sm_count_gemm(), cudaSuccess;
+    cudaLaunchAttribute cluster;
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim.x = CG;
+    cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * std::max(1, sm_count_gemm() / 2));
+    cfg.blockDim = dim3(Cfg::kThreads);
+    cfg.dynamicSmemBytes = Cfg::kSmem;
+    cfg.attrs = &cluster;
+    cfg.numAttrs = 1;
     int n = 0;
     const cudaError_t e2 = cudaOccupancyMaxActiveClusters(&n, (void*)kernel, &cfg);
     *found = std::max(1, n);
     return e2;
   });
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(CG * (unsigned)std::max<int64_t>(1, std::min<int64_t>(most, tiles)));
-  void* args[] = {const_cast<ProductMaps*>(&tm), const_cast<ProductArgs*>(&a),
-                  const_cast<PlanPtrs*>(&p)};
-  return cudaLaunchKernelExC(&cfg, (const void*)kernel, args);
+  const unsigned grid = CG * (unsigned)std::max<int64_t>(1, std::min<int64_t>(most, tiles));
+  return launch_after(kernel, grid, Cfg::kThreads, Cfg::kSmem, st, CG, tm, a, p);
 }
 
 static int64_t tiles_of(int64_t M, int N, int half, int rows) {

@@ -3,6 +3,7 @@
 
 #include "activation.cuh"
 #include "ffn.h"
+#include "pdl.cuh"
 #include "tcgen05.cuh"
 
 namespace moonep {

@@ -92,9 +92,7 @@ k_product_split(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
       mbar_init(empty(s), 1);
     }
     mbar_init(done, 1);
-    // (a CTA that finds the status set does nothing but take part in its cluster's barriers: one that
-    // started earlier may not have seen it, and stores to this one's shared memory)
-    *abort_flag = plan_failed(a.status) ? 1 : 0;
+    *abort_flag = 0;
     fence_barrier_init();
     prefetch_tmap(&tm_w);
     prefetch_tmap(&tm_x);
@@ -107,11 +105,10 @@ k_product_split(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const bool live = *abort_flag == 0;
-  __syncthreads();  // read by all before a role may raise it
+  grid_wait();  // (what is above runs while the kernel before this one ends)
 
   if (warp == 0) {
-    if (live && elect_one()) {
+    if (elect_one()) {
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -140,7 +137,7 @@ k_product_split(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
       }
     }
   } else if (warp == 1) {
-    if (live && elect_one()) {
+    if (elect_one()) {
       const uint32_t idesc = product_idesc(128, a.tokens, AMN, false);
       int stage = 0;
       uint32_t phase = 0;
@@ -169,11 +166,14 @@ k_product_split(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
     }
   }
   __syncwarp();
+  grid_trigger();
   // every thread waits for the sums: the stages are then free, here and, past the cluster's barrier,
-  // in its other CTAs.  A CTA that gave up still takes part in the barriers.
-  const bool here = !live || mbar_wait(done, 0, nullptr, 3 * kWaitNs);
+  // in its other CTAs.  A CTA that gave up still takes part in the barriers; so does one that finds
+  // the status set, which stops the stores alone (the rest harms nobody).
+  const bool live = !plan_failed(a.status);
+  const bool here = mbar_wait(done, 0, nullptr, 3 * kWaitNs);
   const bool ok = __syncthreads_and(here) && !*abort_flag;
-  if (live && !ok && threadIdx.x == 0) set_error(a.status, MOONEP_ERR_TIMEOUT);
+  if (!ok && threadIdx.x == 0) set_error(a.status, MOONEP_ERR_TIMEOUT);
   __syncwarp();
   tc_fence_after();
   if (S > 1) pair_sync();
@@ -217,7 +217,7 @@ k_product_split(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
   __syncthreads();
   if (S > 1) pair_sync();
 
-  if (ok) {
+  if (ok && live) {
     // a lane has two columns (and, for swiglu, the two of the same numbers in the up half), a warp
     // 64 columns of every 8th (16th) group
     const int mine = min(per, fours - rank * per);
@@ -346,20 +346,7 @@ static cudaError_t launch_kind(const CUtensorMap& w, const CUtensorMap& x, const
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSplitSmem);
   });
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute cluster;
-  cluster.id = cudaLaunchAttributeClusterDimension;
-  cluster.val.clusterDim.x = a.splits;
-  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(kSplitThreads);
-  cfg.dynamicSmemBytes = kSplitSmem;
-  cfg.stream = st;
-  cfg.attrs = &cluster;
-  cfg.numAttrs = a.splits > 1 ? 1 : 0;
-  void* args[] = {const_cast<CUtensorMap*>(&w), const_cast<CUtensorMap*>(&x),
-                  const_cast<SplitArgs*>(&a)};
-  return cudaLaunchKernelExC(&cfg, (const void*)kernel, args);
+  return launch_after(kernel, (unsigned)ctas, kSplitThreads, kSplitSmem, st, a.splits, w, x, a);
 }
 
 cudaError_t launch_split(Kind kind, const LinearDims& d, SplitPlan plan, const void* x, const void* w,
