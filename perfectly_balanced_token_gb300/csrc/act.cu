@@ -12,14 +12,14 @@ namespace moonep {
 // ---------------------------------------------------------------------------
 // d_z = act'(z) d_out, with column sums of d_z (in fp32, before d_z is rounded).
 //
-// An item is a chunk of rows (128, or a work tile of the plan: rows of one expert) by 256 columns;
+// An item is a chunk of rows (64, or a work tile of the plan: rows of one expert) by 256 columns;
 // a warp's lanes cover the columns and its rows are every eighth of the chunk.  The chunk's sums go
 // to scratch, one row a chunk, and a second kernel adds them in ascending order: the same bits in
 // every run, whatever runs when.
 // ---------------------------------------------------------------------------
 constexpr int kActThreads = 256;
 constexpr int kActWarps = kActThreads / 32;
-constexpr int kActRows = 128;
+constexpr int kActRows = 64;
 constexpr int kActCols = 256;
 
 struct ActArgs {
@@ -31,7 +31,7 @@ struct ActArgs {
 };
 
 template <int ACT>
-__global__ void __launch_bounds__(kActThreads, 2) k_act_backward(ActArgs a, PlanPtrs p, int plan) {
+__global__ void __launch_bounds__(kActThreads, 3) k_act_backward(ActArgs a, PlanPtrs p, int plan) {
   constexpr bool GATED = ACT == kActSwiglu;
   __shared__ float part[GATED ? 2 : 1][kActWarps][kActCols];
   grid_wait();
@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(kActThreads, 2) k_act_backward(ActArgs a, Plan
     }
     float sum[8] = {}, sum_up[8] = {};
     if (col < ocols) {
-      constexpr int U = 4;  // rows in flight
+      constexpr int U = 2;  // rows in flight
       for (int r0 = warp; r0 < rows; r0 += U * kActWarps) {
         uint4 vz[U], vu[U], vd[U];
 #pragma unroll
@@ -84,18 +84,23 @@ __global__ void __launch_bounds__(kActThreads, 2) k_act_backward(ActArgs a, Plan
             if (GATED) {
               unpack8(up, vu[u]);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
+              for (int i = 0; i < 8; i += 2) {
                 // one sigmoid serves both: a = z s(z), a' = s (1 + z (1 - s))
-                const float s = sigmoid_f(z[i]);
-                const float du = d[i] * (z[i] * s);
-                z[i] = d[i] * up[i] * (s * fmaf(z[i], 1.f - s, 1.f));
-                up[i] = du;
-                sum_up[i] += du;
+                const F2 zz(z[i], z[i + 1]), dd(d[i], d[i + 1]), uu(up[i], up[i + 1]);
+                const F2 s = sigmoid2(zz);
+                const F2 du = dd * (zz * s);
+                const F2 dz = dd * uu * (s * fma2(zz, fma2(s, F2(-1.f), F2(1.f)), F2(1.f)));
+                dz.get(z[i], z[i + 1]);
+                du.get(up[i], up[i + 1]);
+                (F2(sum_up[i], sum_up[i + 1]) + du).get(sum_up[i], sum_up[i + 1]);
               }
-              *reinterpret_cast<uint4*>(a.d_z + row * a.cols + ocols + col) = pack8(up);
+              __stcs(reinterpret_cast<uint4*>(a.d_z + row * a.cols + ocols + col), pack8(up));
             } else {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) z[i] = ACT == kActNone ? d[i] : d[i] * act_slope<ACT>(z[i]);
+              for (int i = 0; i < 8; i += 2) {
+                const F2 dd(d[i], d[i + 1]);
+                (ACT == kActNone ? dd : dd * act_slope2<ACT>(F2(z[i], z[i + 1]))).get(z[i], z[i + 1]);
+              }
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) sum[i] += z[i];

@@ -126,6 +126,15 @@ __device__ __forceinline__ void put_row(const uint32_t (&v)[32], uint16_t* at, i
     if (8 * j < cols) p[j] = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
 }
 
+// The same of 32 values, rounded.
+__device__ __forceinline__ void put_z32(const float (&v)[32], uint16_t* at, int cols) {
+  uint4* p = reinterpret_cast<uint4*>(at);
+  auto two = [&](int i) { return pack_bf16x2(__float_as_uint(v[i]), __float_as_uint(v[i + 1])); };
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (8 * j < cols) p[j] = make_uint4(two(8 * j), two(8 * j + 2), two(8 * j + 4), two(8 * j + 6));
+}
+
 // v += bias[0 .. 31], of which the first `cols` (a multiple of 8) are there; every lane has the same
 __device__ __forceinline__ void add_bias(float (&v)[32], const float* bias, int cols) {
   const float4* b = reinterpret_cast<const float4*>(bias);
@@ -174,30 +183,20 @@ __device__ __forceinline__ void load32(uint32_t taddr, float (&v)[32]) {
 }
 
 // 32 columns of a lane's row from the sums (v and, for swiglu, u of the up half) to the output's
-// values in v; z, and its up half, packed into pz and pu on the way.  x: the first column, cols: how
+// values in v; keep_z(v, false) and keep_z(u, true) see z on the way.  x: the first column, cols: how
 // many are left.
-template <int H>
+template <typename Z>
 __device__ __forceinline__ void forward32(const ProductArgs& a, const float* bias,
                                           const uint16_t* residual, int x, int cols, float (&v)[32],
-                                          float (&u)[32], uint32_t (&pz)[32], uint32_t (&pu)[32]) {
-  x += 32 * H;
-  cols -= 32 * H;
+                                          float (&u)[32], Z&& keep_z) {
   if (bias != nullptr) add_bias(v, bias + x, cols);
-  pack32<H>(pz, v);
+  keep_z(v, false);
   if (a.half) {
     if (bias != nullptr) add_bias(u, bias + a.half + x, cols);
-    pack32<H>(pu, u);
-#pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = v[j] * sigmoid_f(v[j]) * u[j];
-  } else if (a.act == kActRelu) {  // one loop for each, so that the choice is not made 32 times
-#pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = act_value(kActRelu, v[j]);
-  } else if (a.act == kActGelu) {
-#pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = act_value(kActGelu, v[j]);
-  } else if (a.act == kActSilu) {
-#pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = act_value(kActSilu, v[j]);
+    keep_z(u, true);
+    swiglu_each(v, u);
+  } else {
+    act_each(a.act, v);
   }
   if (residual != nullptr) add_residual(v, residual + x, cols);
 }
@@ -516,16 +515,22 @@ k_product(const __grid_constant__ ProductMaps tm, const __grid_constant__ Produc
           const int x = n0 + (a.half ? 64 * hs : 128 * hs + 64 * U);
           const int cols = min(64, ocols - x);
           if (cols <= 0) return;
-          uint32_t pz[32], pu[32];
           auto half = [&](auto h) {
             constexpr int H = decltype(h)::value;
+            const int xh = x + 32 * H, left = cols - 32 * H;
+            if (left <= 0) return;
             if (KIND == kForward)
-              forward32<H>(a, bias, residual, x, cols, sum[2 * U + H], sum[2 + H], pz, pu);
-            if (32 * H < cols) ring.put(sum[2 * U + H], &tm.out, x + 32 * H, mt.row0 + first, a.add);
+              // (z in bf16 goes row by row: the sums leave no registers to collect 64 columns in)
+              forward32(a, bias, residual, xh, left, sum[2 * U + H], sum[2 + H],
+                        [&](const float(&z)[32], bool up) {
+                          if (a.has_z && valid)
+                            put_z32(z, a.z + (size_t)row * a.N + (up ? a.half : 0) + xh, left);
+                          __syncwarp();
+                        });
+            ring.put(sum[2 * U + H], &tm.out, xh, mt.row0 + first, a.add);
           };
           half(std::integral_constant<int, 0>());
           half(std::integral_constant<int, 1>());
-          put_z(pz, pu, x, cols);
         };
         unit(std::integral_constant<int, 0>());
         if (!a.half) unit(std::integral_constant<int, 1>());
@@ -545,7 +550,8 @@ k_product(const __grid_constant__ ProductMaps tm, const __grid_constant__ Produc
             load32(lanes_at() + 64 * c + 32 * H, v);
             if (KIND == kForward) {
               if (a.half) load32(lanes_at() + 128 + 64 * c + 32 * H, u);
-              forward32<H>(a, bias, residual, x, cols, v, u, pz, pu);
+              forward32(a, bias, residual, x + 32 * H, cols - 32 * H, v, u,
+                        [&](const float(&z)[32], bool up) { pack32<H>(up ? pu : pz, z); });
             }
             pack32<H>(po, v);
           };
@@ -613,10 +619,10 @@ static int64_t tiles_of(int64_t M, int N, int half, int rows) {
 cudaError_t launch_linear(const LinearDims& d, const void* x, const void* w, const float* bias,
                           const void* residual, void* out, void* z, int32_t* status, cudaStream_t st,
                           int* launches) {
-  const SplitPlan split = plan_split(d.T, d.N, d.half, d.K);
+  const SplitPlan split = plan_split(d.T, d.N, d.half, d.K, d.f32);
   if (split.splits) {
     *launches += 1;
-    return launch_split(kForward, d, split, x, w, bias, residual, out, z, status, st);
+    return launch_split(kForward, d, split, x, w, bias, residual, out, z, 0, status, st);
   }
   ProductMaps tm;
   const int ocols = d.half ? d.half : d.N;
@@ -635,6 +641,7 @@ cudaError_t launch_linear(const LinearDims& d, const void* x, const void* w, con
   a.act = d.act, a.half = d.half;
   a.bias = bias;
   a.residual = (const uint16_t*)residual;
+  a.z = (uint16_t*)z;
   a.has_z = z != nullptr;
   a.status = status;
   *launches += 1;
@@ -645,10 +652,10 @@ cudaError_t launch_linear(const LinearDims& d, const void* x, const void* w, con
 
 cudaError_t launch_linear_dx(const LinearDims& d, const void* d_z, const void* w, void* d_x,
                              int32_t* status, cudaStream_t st, int* launches) {
-  const SplitPlan split = plan_split(d.T, d.K, 0, d.N);
+  const SplitPlan split = plan_split(d.T, d.K, 0, d.N, false);
   if (split.splits) {
     *launches += 1;
-    return launch_split(kInputGrad, d, split, d_z, w, nullptr, nullptr, d_x, nullptr, status, st);
+    return launch_split(kInputGrad, d, split, d_z, w, nullptr, nullptr, d_x, nullptr, 0, status, st);
   }
   ProductMaps tm;
   if (!encode_matrix(&tm.a, d_z, d.N, d.T, d.N, 128) || !encode_matrix(&tm.b, w, d.N, d.K, d.N, 128) ||
@@ -665,6 +672,11 @@ cudaError_t launch_linear_dx(const LinearDims& d, const void* d_z, const void* w
 
 cudaError_t launch_linear_dw(const LinearDims& d, const void* x, const void* d_z, float* d_w,
                              int add, int32_t* status, cudaStream_t st, int* launches) {
+  const SplitPlan split = plan_split(d.K, d.N, 0, d.T, true);
+  if (split.splits) {
+    *launches += 1;
+    return launch_split(kWeightGrad, d, split, x, d_z, nullptr, nullptr, d_w, nullptr, add, status, st);
+  }
   ProductMaps tm;
   if (!encode_matrix(&tm.a, x, d.K, d.T, d.K, 64) || !encode_matrix(&tm.b, d_z, d.N, d.T, d.N, 64) ||
       !encode_matrix(&tm.out, d_w, d.N, d.K, d.N, 32, true))

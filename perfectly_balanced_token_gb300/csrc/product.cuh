@@ -15,7 +15,7 @@ constexpr int kPanelBytes = 64 * 128;  // 64 rows of 64 bf16
 // fp32 sums do not hold, always towards zero, so a long sum drifts: against 64 bits, with the whole
 // depth in one accumulator, 7e-6 of C at a depth of 7168 and past 2e-5 at 32768.  The epilogues add
 // the parts in registers, rounding to nearest.  (A bf16 C's own rounding is 250 times larger.)
-constexpr int kPartBlocks = 16;
+constexpr int kPartBlocks = 8;
 
 enum Kind { kForward, kInputGrad, kWeightGrad };
 
@@ -61,9 +61,9 @@ inline bool encode_matrix(CUtensorMap* m, const void* base, int cols, int64_t ro
 struct SplitPlan {
   int tokens, splits;  // rows of a tile, CTAs that share its depth; splits = 0: not for these sizes
 };
-SplitPlan plan_split(int T, int columns, int half, int depth);
+SplitPlan plan_split(int T, int columns, int half, int depth, bool f32);
 cudaError_t launch_split(Kind kind, const LinearDims& d, SplitPlan plan, const void* x, const void* w,
-                         const float* bias, const void* residual, void* out, void* z, int32_t* status,
-                         cudaStream_t st);
+                         const float* bias, const void* residual, void* out, void* z, int add,
+                         int32_t* status, cudaStream_t st);
 
 }  // namespace moonep

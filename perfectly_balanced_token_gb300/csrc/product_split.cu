@@ -2,6 +2,7 @@
 //
 // The operands change sides: 128 columns of w are the M of the instruction and up to 256 rows of x,
 // any multiple of 16, its N, so that one token costs a 16-wide instruction and not a 128-row tile.
+// (Weight gradient: d_z takes the place of w and x^T that of x, the depth is the number of tokens.)
 // A cluster of 1, 2, 4 or 8 CTAs shares the depth of one tile: each runs its part through a ring of
 // TMA-fed stages into TMEM, then sends its partial sums of a token to the CTA that owns the token
 // (stores to the shared memory of the cluster, into the stages that are done), which adds them in
@@ -24,8 +25,8 @@ constexpr int kSplitSmem = kSplitRing + 1024 + (2 * kSplitStages + 2) * 8 + 16;
 static_assert(kSplitSmem <= 232448, "shared memory of a CTA");
 
 struct SplitArgs {
-  int T, columns, depth;  // rows of x, columns of w (or rows, input gradient), depth
-  int half, act, f32;
+  int T, columns, depth;  // rows and columns of the result, depth
+  int half, act, f32, add;
   int tokens, splits, stages, parts;
   const float* bias;
   const uint16_t* residual;
@@ -46,22 +47,12 @@ __device__ __forceinline__ float4 add_parts(const float4* at, int stride, int sp
   return v;
 }
 
-// act of the two columns' four tokens
-__device__ __forceinline__ void act_pairs(int act, float (&v)[2][4]) {
-  auto each = [&](auto f) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i >> 2][i & 3] = f(v[i >> 2][i & 3]);
-  };
-  if (act == kActRelu) each([](float z) { return act_value(kActRelu, z); });
-  else if (act == kActGelu) each([](float z) { return act_value(kActGelu, z); });
-  else if (act == kActSilu) each([](float z) { return act_value(kActSilu, z); });
-}
-
 template <int KIND>
 __global__ void __launch_bounds__(kSplitThreads, 1)
 k_product_split(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                 const __grid_constant__ SplitArgs a) {
-  constexpr bool AMN = KIND == kForward;  // w runs along its columns, w^T along the depth
+  constexpr bool AMN = KIND != kInputGrad;  // w runs along its columns, w^T along the depth
+  constexpr bool BMN = KIND == kWeightGrad;  // x runs along the depth, x^T does not
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint64_t* bars = (uint64_t*)(smem + kSplitRing);
@@ -81,7 +72,8 @@ k_product_split(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
   const int c0 = (tile % CT) * step, t0 = (tile / CT) * a.tokens;
   const int KB = (a.depth + kDepth - 1) / kDepth;
   const int kb0 = (int)((int64_t)KB * rank / S), kb1 = (int)((int64_t)KB * (rank + 1) / S);
-  const uint32_t stage_bytes = 2 * kPanelBytes + a.tokens * 128;
+  const int panels = (a.tokens + 63) / 64;  // of x^T
+  const uint32_t stage_bytes = 2 * kPanelBytes + (BMN ? panels * kPanelBytes : a.tokens * 128);
   const int stages = a.stages;
   const uint32_t span = a.tokens <= 32 ? 32 : (a.tokens <= 64 ? 64 : (a.tokens <= 128 ? 128 : 256));
   const uint32_t tmem_cols = span * a.parts;  // a.parts is a power of two
@@ -124,7 +116,12 @@ k_product_split(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
         } else {
           tma_load_2d(sa, &tm_w, full(stage), k0, c0);
         }
-        tma_load_2d(sa + 2 * kPanelBytes, &tm_x, full(stage), k0, t0);
+        if (BMN) {
+          for (int j = 0; j < panels; ++j)
+            tma_load_2d(sa + (2 + j) * kPanelBytes, &tm_x, full(stage), t0 + 64 * j, k0);
+        } else {
+          tma_load_2d(sa + 2 * kPanelBytes, &tm_x, full(stage), k0, t0);
+        }
         if (++stage == stages) { stage = 0; phase ^= 1u; }
       }
       if (!ok) {
@@ -138,7 +135,7 @@ k_product_split(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
     }
   } else if (warp == 1) {
     if (elect_one()) {
-      const uint32_t idesc = product_idesc(128, a.tokens, AMN, false);
+      const uint32_t idesc = product_idesc(128, a.tokens, AMN, BMN);
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -153,7 +150,7 @@ k_product_split(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
         const uint32_t sb = sa + 2 * kPanelBytes;
 #pragma unroll
         for (int k = 0; k < kDepth / 16; ++k)
-          umma_bf16(acc, stage_desc(sa, k, AMN), stage_desc(sb, k, false), idesc, left != 0 || k != 0);
+          umma_bf16(acc, stage_desc(sa, k, AMN), stage_desc(sb, k, BMN), idesc, left != 0 || k != 0);
         if (++left == of_part) left = 0;
         umma_commit(empty(stage));
         if (++stage == stages) { stage = 0; phase ^= 1u; }
@@ -268,13 +265,11 @@ k_product_split(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
             float u[2][4];
             get(u, 64, bias_up);
             if (a.z != nullptr) put(a.z + at_z + a.half, a.columns, u);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              float& z = v[i >> 2][i & 3];
-              z = z * sigmoid_f(z) * u[i >> 2][i & 3];
-            }
+            swiglu_each(v[0], u[0]);
+            swiglu_each(v[1], u[1]);
           } else if (a.act != kActNone) {
-            act_pairs(a.act, v);
+            act_each(a.act, v[0]);
+            act_each(a.act, v[1]);
           }
           if (a.residual != nullptr) {
 #pragma unroll
@@ -288,7 +283,14 @@ k_product_split(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
           float* o = (float*)a.out + at;
 #pragma unroll
           for (int j = 0; j < 4; ++j, o += ncols)
-            if (j < left) *reinterpret_cast<float2*>(o) = make_float2(v[0][j], v[1][j]);
+            if (j < left) {
+              float2 f = make_float2(v[0][j], v[1][j]);
+              if (KIND == kWeightGrad && a.add) {
+                const float2 was = *reinterpret_cast<const float2*>(o);
+                f.x += was.x, f.y += was.y;
+              }
+              *reinterpret_cast<float2*>(o) = f;
+            }
         } else {
           put((uint16_t*)a.out + at, ncols, v);
         }
@@ -306,82 +308,134 @@ k_product_split(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
 }
 
 // -- host side ------------------------------------------------------------------
-// How the rows are cut and the depth is split, or splits = 0 where the pair kernel's tiles are the
-// better choice.  Times in microseconds of the two kernels on one box: a block of 64 of the depth
-// costs the larger of its loads and its instructions.
-SplitPlan plan_split(int T, int columns, int half, int depth) {
+static int span_of(int tokens) {  // columns of TMEM that one accumulator takes
+  return tokens <= 32 ? 32 : (tokens <= 64 ? 64 : (tokens <= 128 ? 128 : 256));
+}
+
+template <int KIND>
+static cudaError_t opt_in() {
   static PerDevice kept;
-  int sms = 0;
-  if (kept(&sms, [](int* n) { return *n = sm_count_gemm(), cudaSuccess; }) != cudaSuccess) sms = 152;
+  int set = 0;
+  return kept(&set, [&](int* done) {
+    *done = 1;
+    return cudaFuncSetAttribute(k_product_split<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kSplitSmem);
+  });
+}
+
+// CTAs that run at once in clusters of `splits` (1, 2, 4, 8): the GPU's processing clusters do not
+// all have a multiple of eight multiprocessors.
+static int at_once(int splits) {
+  static PerDevice kept[4];
+  const int which = splits == 1 ? 0 : (splits == 2 ? 1 : (splits == 4 ? 2 : 3));
+  int n = 0;
+  const cudaError_t e = kept[which](&n, [&](int* found) {
+    if (splits == 1) return *found = sm_count_gemm(), cudaSuccess;
+    const cudaError_t e = opt_in<kForward>();
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute cluster;
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim.x = splits;
+    cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(splits * 64);
+    cfg.blockDim = dim3(kSplitThreads);
+    cfg.dynamicSmemBytes = kSplitSmem;
+    cfg.attrs = &cluster;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    const cudaError_t e2 = cudaOccupancyMaxActiveClusters(&clusters, (void*)k_product_split<kForward>, &cfg);
+    *found = std::max(1, clusters) * splits;
+    return e2;
+  });
+  return e == cudaSuccess ? n : 0;
+}
+
+// How the rows are cut and the depth is split, or splits = 0 where the pair kernel's tiles are the
+// better choice.  The two kernels' times in microseconds, fitted to 25 shapes of 1 to 8192 rows (each
+// with up to 15 choices; on the average off by 11 %, and the choice 1 % from the best one):
+// a block of 64 of the depth costs an instruction's least time or grows with its tokens, 0.16 to 0.33;
+// a round of CTAs begins and ends in 3 + 0.02 a token, a cluster's exchange adds 0.9 + 0.005 a token.
+// The pair kernel takes 0.27 for a block of a tile and 8.2 for its first round.
+SplitPlan plan_split(int T, int columns, int half, int depth, bool f32) {
   const int64_t CT = half ? (half + 63) / 64 : (columns + 127) / 128;
   const int KB = (depth + kDepth - 1) / kDepth;
-  const int64_t pairs = std::max(1, sms / 2);
+  const int64_t pairs = std::max(1, at_once(1) / 2);
   const int64_t pair_tiles =
       ((T + 255) / 256) * (int64_t)(half ? (half + 127) / 128 : (columns + 255) / 256);
+  const double rounds = (double)((pair_tiles + pairs - 1) / pairs);
   SplitPlan best{0, 0};
-  double cost = (double)((pair_tiles + pairs - 1) / pairs) * (KB * 0.36 + 1.0) + 6.0;
-  for (int S = 1; S <= 8 && (S == 1 || KB >= 2 * S); S *= 2)
+  double cost = rounds * (0.2685 * KB + 2.0) + 4.25;
+  for (int S = 1; S <= 8 && (S == 1 || KB >= 2 * S); S *= 2) {
+    const int room = at_once(S);
+    if (room == 0) continue;
+    const int blocks = (KB + S - 1) / S;
     for (int waves = 0; waves <= 3; ++waves) {  // 0: as few cuts as there can be
       const int64_t fewest = (T + 255) / 256;
-      const int64_t cuts = waves ? waves * sms / (CT * S) : fewest;
+      const int64_t cuts = waves ? waves * room / (CT * S) : fewest;
       if (cuts < fewest) continue;
       const int tokens = (int)(((T + cuts - 1) / cuts + 15) / 16 * 16);
+      // fp32 sums in parts: each has its columns of TMEM
+      if (f32 && blocks > 512 / span_of(tokens) * kPartBlocks) continue;
       const int64_t ctas = (T + tokens - 1) / tokens * CT * S;
-      const double block = std::max(0.10, 0.06 + tokens * 0.0014);
-      const double c = (double)((ctas + sms - 1) / sms) *
-                           ((KB + S - 1) / S * block + 1.5 + tokens * 0.01) + 5.0 + 0.3 * (S > 1);
+      const double c = (double)((ctas + room - 1) / room) *
+                       (blocks * std::max(0.1585, 0.073 + 0.001 * tokens) + 3.02 + 0.0207 * tokens +
+                        (S > 1 ? 0.914 + 0.0047 * tokens : 0.0));
       if (c < cost) cost = c, best = {tokens, S};
     }
+  }
   return best;
 }
 
 template <int KIND>
 static cudaError_t launch_kind(const CUtensorMap& w, const CUtensorMap& x, const SplitArgs& a,
                                int64_t ctas, cudaStream_t st) {
-  auto* kernel = k_product_split<KIND>;
-  static PerDevice kept;
-  int set = 0;
-  const cudaError_t e = kept(&set, [&](int* done) {
-    *done = 1;
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSplitSmem);
-  });
+  const cudaError_t e = opt_in<KIND>();
   if (e != cudaSuccess) return e;
-  return launch_after(kernel, (unsigned)ctas, kSplitThreads, kSplitSmem, st, a.splits, w, x, a);
+  return launch_after(k_product_split<KIND>, (unsigned)ctas, kSplitThreads, kSplitSmem, st, a.splits, w,
+                      x, a);
 }
 
+// x and w: the operands as the kernel has them (see there), `out` [T][C]
 cudaError_t launch_split(Kind kind, const LinearDims& d, SplitPlan plan, const void* x, const void* w,
-                         const float* bias, const void* residual, void* out, void* z, int32_t* status,
-                         cudaStream_t st) {
+                         const float* bias, const void* residual, void* out, void* z, int add,
+                         int32_t* status, cudaStream_t st) {
   SplitArgs a = {};
-  a.T = d.T;
+  a.T = kind == kWeightGrad ? d.K : d.T;
   a.tokens = plan.tokens;
   a.splits = plan.splits;
-  a.stages = std::min(kSplitStages, kSplitRing / (2 * kPanelBytes + plan.tokens * 128));
+  const int rows_bytes = kind == kWeightGrad ? (plan.tokens + 63) / 64 * kPanelBytes : plan.tokens * 128;
+  a.stages = std::min(kSplitStages, kSplitRing / (2 * kPanelBytes + rows_bytes));
   a.out = out;
   a.status = status;
   CUtensorMap tw, tx;
+  bool ok;
   if (kind == kForward) {
     a.columns = d.N, a.depth = d.K;
     a.half = d.half, a.act = d.act, a.f32 = d.f32;
     a.bias = bias;
     a.residual = (const uint16_t*)residual;
     a.z = (uint16_t*)z;
-    if (!encode_matrix(&tw, w, d.N, d.K, d.N, 64)) return cudaErrorInvalidValue;
-  } else {
+    ok = encode_matrix(&tw, w, d.N, d.K, d.N, 64) && encode_matrix(&tx, x, d.K, d.T, d.K, plan.tokens);
+  } else if (kind == kInputGrad) {
     a.columns = d.K, a.depth = d.N;
-    if (!encode_matrix(&tw, w, d.N, d.K, d.N, 128)) return cudaErrorInvalidValue;
+    ok = encode_matrix(&tw, w, d.N, d.K, d.N, 128) && encode_matrix(&tx, x, d.N, d.T, d.N, plan.tokens);
+  } else {
+    a.columns = d.N, a.depth = d.T;
+    a.f32 = 1, a.add = add;
+    ok = encode_matrix(&tw, w, d.N, d.T, d.N, 64) && encode_matrix(&tx, x, d.K, d.T, d.K, 64);
   }
-  if (!encode_matrix(&tx, x, a.depth, d.T, a.depth, plan.tokens)) return cudaErrorInvalidValue;
+  if (!ok) return cudaErrorInvalidValue;
   const int64_t CT = a.half ? (a.half + 63) / 64 : (a.columns + 127) / 128;
-  const int64_t ctas = ((d.T + plan.tokens - 1) / plan.tokens) * CT * plan.splits;
+  const int64_t ctas = ((a.T + plan.tokens - 1) / plan.tokens) * CT * plan.splits;
   a.parts = 1;
   if (a.f32) {
     const int blocks = ((a.depth + kDepth - 1) / kDepth + plan.splits - 1) / plan.splits;
-    const int span = plan.tokens <= 32 ? 32 : (plan.tokens <= 64 ? 64 : (plan.tokens <= 128 ? 128 : 256));
-    while (a.parts * kPartBlocks < blocks && a.parts * span < 512) a.parts *= 2;
+    while (a.parts * kPartBlocks < blocks && a.parts * span_of(plan.tokens) < 512) a.parts *= 2;
   }
-  return kind == kForward ? launch_kind<kForward>(tw, tx, a, ctas, st)
-                          : launch_kind<kInputGrad>(tw, tx, a, ctas, st);
+  if (kind == kForward) return launch_kind<kForward>(tw, tx, a, ctas, st);
+  if (kind == kInputGrad) return launch_kind<kInputGrad>(tw, tx, a, ctas, st);
+  return launch_kind<kWeightGrad>(tw, tx, a, ctas, st);
 }
 
 }  // namespace moonep

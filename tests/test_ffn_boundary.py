@@ -123,7 +123,7 @@ def test_act_backward_is_checked(lib):
     assert act(lib, rows=0, z=None, d_out=None, d_z=None) == _lib.OK
     assert act(lib, rows=0, d_bias=OK_PTR, acc=1) == _lib.OK
     assert mx.moonep_act_backward_workspace_bytes(0, 64) == 64 * 4
-    assert mx.moonep_act_backward_workspace_bytes(129, 64) == 2 * 64 * 4
+    assert mx.moonep_act_backward_workspace_bytes(129, 64) == 3 * 64 * 4
     assert lib.moonep_act_backward_workspace_bytes(4, 64, None) == _lib.ERR_ARG
     assert lib.moonep_grouped_act_backward_workspace_bytes(ctypes.byref(d), None) == _lib.ERR_ARG
     # a tile of the plan's list and one of a column of sums each
@@ -203,7 +203,7 @@ int main(void) {
   size_t n = 0;
   int32_t status = 0;
   uint16_t b[8];
-  if (moonep_act_backward_workspace_bytes(300, 64, &n) != MOONEP_OK || n != 3 * 64 * 4) return 1;
+  if (moonep_act_backward_workspace_bytes(300, 64, &n) != MOONEP_OK || n != 5 * 64 * 4) return 1;
   if (moonep_linear(&d, NULL, b, NULL, NULL, b, NULL, &status, NULL) != MOONEP_ERR_ARG) return 2;
   d.K = 65;
   if (moonep_linear_dx(&d, b, b, b, &status, NULL) != MOONEP_ERR_SHAPE) return 3;
