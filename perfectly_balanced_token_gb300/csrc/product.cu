@@ -41,6 +41,10 @@ struct ProductCfg {
   static constexpr int kNumBars = 2 * kStages + 5 + 2 * kQueue;
   static constexpr int kBarBytes = kNumBars * 8 + 16 + 4 * kQueue;
   static constexpr int kSmem = kStages * kStageBytes + kOutBytes + 1024 + kBarBytes;
+  // With z kept, a tile has two or three stores where it had one, and waiting until TMA has read the
+  // buffer that the one before the last left costs more than a stage is worth (12000 rows x 1024 x
+  // 576, gelu and z: 69 -> 5x us): the last stage's memory becomes four buffers a warp in place of two.
+  static constexpr bool kCanDeepen = PAIR && !F32;
 };
 static_assert(ProductCfg<true, false>::kSmem <= 232448 && ProductCfg<true, true>::kSmem <= 232448 &&
                   ProductCfg<false, false>::kSmem <= 232448,
@@ -52,6 +56,7 @@ struct ProductArgs {
   int act;         // Act
   int half;        // swiglu: N / 2, otherwise 0
   int add;         // fp32 C: added into
+  int bn;          // columns of a tile: 256, 192 or 128 (swiglu: half of them gates)
   const float* bias;  // [N], grouped [E][N]; or null
   const uint16_t* residual;  // [M][out columns] or null
   uint16_t *out, *z;         // for rows stored one by one; z null if not asked for
@@ -81,9 +86,9 @@ struct Issue {  // the forms of one CTA and of a pair
 };
 
 // A warp's staging buffers of 32 rows x 128 bytes (128-byte swizzle) and the stores from them.
-template <int BUFFERS>
 struct OutRing {
   uint8_t* base;
+  int buffers;  // 1, 2 or 4
   int n, lane;
   static __device__ __forceinline__ uint32_t word(uint32_t v) { return v; }
   static __device__ __forceinline__ uint32_t word(float v) { return __float_as_uint(v); }
@@ -91,9 +96,13 @@ struct OutRing {
   template <typename T>
   __device__ __forceinline__ void put(const T (&v)[32], const CUtensorMap* m, int x, int y,
                                       bool add) {
-    uint8_t* buf = base + (n % BUFFERS) * 4096;
+    uint8_t* buf = base + (n & (buffers - 1)) * 4096;
     ++n;
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(BUFFERS - 1) : "memory");
+    if (lane == 0) {  // until the store that had this buffer has read it
+      if (buffers == 1) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      else if (buffers == 2) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+      else asm volatile("cp.async.bulk.wait_group.read 3;" ::: "memory");
+    }
     __syncwarp();
     uint4* row = reinterpret_cast<uint4*>(buf + lane * 128);
 #pragma unroll
@@ -208,13 +217,14 @@ k_product(const __grid_constant__ ProductMaps tm, const __grid_constant__ Produc
   static_assert(DENSE || !F32, "the grouped output is bf16");
   using Cfg = ProductCfg<PAIR, F32>;
   using Op = Issue<PAIR>;
-  constexpr int STAGES = Cfg::kStages;
+  const bool deep = Cfg::kCanDeepen && a.has_z;
+  const int STAGES = Cfg::kStages - (deep ? 1 : 0);
   constexpr bool AMN = KIND == kWeightGrad;  // A = x^T: runs along M in memory
   constexpr bool BMN = KIND != kInputGrad;   // B = w^T there: runs along the depth
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* out_stage = smem + STAGES * Cfg::kStageBytes;  // 1024-aligned
-  uint64_t* bars = (uint64_t*)(out_stage + Cfg::kOutBytes);
+  uint64_t* bars = (uint64_t*)(smem + Cfg::kStages * Cfg::kStageBytes + Cfg::kOutBytes);
   uint32_t* tmem_slot = (uint32_t*)(bars + Cfg::kNumBars);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   volatile int* dead = (volatile int*)(tmem_slot + 2 + kQueue);  // the status was set
@@ -237,7 +247,8 @@ k_product(const __grid_constant__ ProductMaps tm, const __grid_constant__ Produc
     grid_wait();
     if (p.counters[MOONEP_CNT_TILE_ROWS] != Cfg::kTileM) return;
   }
-  const int NT = a.half ? (a.half + 127) / 128 : (a.N + 255) / 256;
+  const int step = a.half ? a.bn / 2 : a.bn;  // output columns of a tile
+  const int NT = ((a.half ? a.half : a.N) + step - 1) / step;
   const int MT = DENSE ? (a.M + Cfg::kTileM - 1) / Cfg::kTileM : p.counters[MOONEP_CNT_MTILES];
   const int total = MT * NT;
   const int KB = (a.K + kDepth - 1) / kDepth;
@@ -303,7 +314,7 @@ k_product(const __grid_constant__ ProductMaps tm, const __grid_constant__ Produc
     } else {
       mt = p.mtiles[t / NT];
     }
-    n0 = (t % NT) * (a.half ? 128 : 256);
+    n0 = (t % NT) * step;
   };
 
   if (skip) {
@@ -336,13 +347,18 @@ k_product(const __grid_constant__ ProductMaps tm, const __grid_constant__ Produc
         const CUtensorMap* bmap = mt.wsel >= 0 ? &tm.b : &tm.b_slots;
         const int wrow = (mt.wsel >= 0 ? mt.wsel : (-1 - mt.wsel)) * a.wrows;
         const int row0 = mt.row0 + (int)crank * 128;
-        // this CTA's columns of B: panel j begins at col0 + 64 j, or col1 + 64 (j - 2)
-        const int col0 = PAIR ? (a.half ? (int)crank * a.half + n0 : n0 + (int)crank * 128) : n0;
-        const int col1 = a.half ? a.half + n0 : n0 + 128;  // (one CTA only)
+        // this CTA's columns of B
+        // (past the first bn / 64 of one CTA, or bn / 2 columns of one of two, there is none)
+        const int mine = PAIR ? (a.half ? (int)crank * a.half + n0 : n0 + (int)crank * (a.bn / 2)) : n0;
+        const int panels = PAIR ? (a.bn / 2 + 63) / 64 : a.bn / 64;
+        auto column = [&](int j) {
+          return !PAIR && a.half && j >= panels / 2 ? a.half + n0 + 64 * (j - panels / 2) : mine + 64 * j;
+        };
+        const uint32_t bytes = Cfg::kABytes + (BMN ? panels : Cfg::kBPanels) * kPanelBytes;
         for (int kb = 0; kb < KB; ++kb) {
           if (!mbar_wait(empty(stage), phase ^ 1u, abort_flag)) { ok = false; break; }
           const uint32_t fb = PAIR ? pair_map(full(stage), 0) : full(stage);
-          if (leader) mbar_expect_tx(full(stage), (PAIR ? 2 : 1) * Cfg::kStageBytes);
+          if (leader) mbar_expect_tx(full(stage), (PAIR ? 2 : 1) * bytes);
           const uint32_t sa = smem_u32(smem + stage * Cfg::kStageBytes);
           const uint32_t sb = sa + Cfg::kABytes;
           const int k0 = kb * kDepth;
@@ -353,15 +369,12 @@ k_product(const __grid_constant__ ProductMaps tm, const __grid_constant__ Produc
             Op::load(sa, &tm.a, fb, k0, row0);
           }
           if (BMN) {
-            Op::load(sb, bmap, fb, col0, wrow + k0);
-            Op::load(sb + kPanelBytes, bmap, fb, col0 + 64, wrow + k0);
-            if (!PAIR) {
-              Op::load(sb + 2 * kPanelBytes, bmap, fb, col1, wrow + k0);
-              Op::load(sb + 3 * kPanelBytes, bmap, fb, col1 + 64, wrow + k0);
-            }
-          } else {
-            Op::load(sb, bmap, fb, k0, wrow + col0);
-            if (!PAIR) Op::load(sb + 2 * kPanelBytes, bmap, fb, k0, wrow + col1);
+#pragma unroll
+            for (int j = 0; j < Cfg::kBPanels; ++j)
+              if (j < panels) Op::load(sb + j * kPanelBytes, bmap, fb, column(j), wrow + k0);
+          } else {  // 128 rows of w at a time
+            Op::load(sb, bmap, fb, k0, wrow + mine);
+            if (!PAIR) Op::load(sb + 2 * kPanelBytes, bmap, fb, k0, wrow + mine + 128);
           }
           ++issued;
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
@@ -387,7 +400,7 @@ k_product(const __grid_constant__ ProductMaps tm, const __grid_constant__ Produc
   } else if (warp == 1) {
     // ---------------- MMA issuer (leader only) ----------------
     if (leader && elect_one()) {
-      constexpr uint32_t idesc = product_idesc(Cfg::kTileM, 256, AMN, BMN);
+      const uint32_t idesc = product_idesc(Cfg::kTileM, a.bn, AMN, BMN);
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
@@ -432,7 +445,8 @@ k_product(const __grid_constant__ ProductMaps tm, const __grid_constant__ Produc
     // ---------------- epilogue (warps 2.., both CTAs) ----------------
     const int qw = warp & 3;         // TMEM lanes 32 qw .. are this warp's rows
     const int hs = (warp - 2) >> 2;  // fp32: which half of the columns is this warp's
-    OutRing<Cfg::kOutBuffers> ring{out_stage + (warp - 2) * Cfg::kOutBuffers * 4096, 0, lane};
+    const int buffers = Cfg::kOutBuffers * (deep ? 2 : 1);
+    OutRing ring{out_stage + (warp - 2) * buffers * 4096, buffers, 0, lane};
     const int ocols = a.half ? a.half : a.N;
     const int parts = F32 ? (KB + kPartBlocks - 1) / kPartBlocks : 1;
     int acc = 0;
@@ -490,54 +504,57 @@ k_product(const __grid_constant__ ProductMaps tm, const __grid_constant__ Produc
         if (a.half) put(pu, &tm.z_up, x, a.z + a.half, a.N, cols);
       };
       if constexpr (F32) {
-        float sum[4][32];  // of 128 columns: 64 gates and the 64 up columns of the same numbers for swiglu
+        // up to 128 columns: for swiglu 64 gates and the 64 up columns of the same numbers, otherwise
+        // half of the tile's
+        float sum[4][32];
+        const int width = a.half ? 128 : a.bn / 2;
         for (int k = 0; k < parts && ok; ++k) {
           ok = take();
           if (!ok) break;
           // (16 columns at a time: the sums leave few registers)
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const int at = a.half ? 128 * (j >> 2) + 64 * hs + 16 * (j & 3) : 128 * hs + 16 * j;
-            uint32_t v[16];
-            tmem_ld_x16(lanes_at() + at, v);
-            tmem_ld_wait();
+            if (16 * j < width) {
+              const int at = a.half ? 128 * (j >> 2) + 64 * hs + 16 * (j & 3) : width * hs + 16 * j;
+              uint32_t v[16];
+              tmem_ld_x16(lanes_at() + at, v);
+              tmem_ld_wait();
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              float& to = sum[j >> 1][16 * (j & 1) + c];
-              to = __uint_as_float(v[c]) + (k == 0 ? 0.f : to);
+              for (int c = 0; c < 16; ++c) {
+                float& to = sum[j >> 1][16 * (j & 1) + c];
+                to = __uint_as_float(v[c]) + (k == 0 ? 0.f : to);
+              }
             }
           }
           release();
         }
         if (!ok || !any) continue;
-        auto unit = [&](auto number) {  // 64 output columns
-          constexpr int U = decltype(number)::value;
-          const int x = n0 + (a.half ? 64 * hs : 128 * hs + 64 * U);
-          const int cols = min(64, ocols - x);
+        auto quarter = [&](auto number) {  // 32 output columns
+          constexpr int Q = decltype(number)::value;
+          if (32 * Q >= (a.half ? 64 : width)) return;
+          const int x = n0 + (a.half ? 64 : width) * hs + 32 * Q;
+          const int cols = min(32, ocols - x);
           if (cols <= 0) return;
-          auto half = [&](auto h) {
-            constexpr int H = decltype(h)::value;
-            const int xh = x + 32 * H, left = cols - 32 * H;
-            if (left <= 0) return;
-            if (KIND == kForward)
-              // (z in bf16 goes row by row: the sums leave no registers to collect 64 columns in)
-              forward32(a, bias, residual, xh, left, sum[2 * U + H], sum[2 + H],
-                        [&](const float(&z)[32], bool up) {
-                          if (a.has_z && valid)
-                            put_z32(z, a.z + (size_t)row * a.N + (up ? a.half : 0) + xh, left);
-                          __syncwarp();
-                        });
-            ring.put(sum[2 * U + H], &tm.out, xh, mt.row0 + first, a.add);
-          };
-          half(std::integral_constant<int, 0>());
-          half(std::integral_constant<int, 1>());
+          if (KIND == kForward)
+            // (z in bf16 goes row by row: the sums leave no registers to collect 64 columns in)
+            forward32(a, bias, residual, x, cols, sum[Q], sum[(2 + Q) & 3],
+                      [&](const float(&z)[32], bool up) {
+                        if (a.has_z && valid)
+                          put_z32(z, a.z + (size_t)row * a.N + (up ? a.half : 0) + x, cols);
+                        __syncwarp();
+                      });
+          ring.put(sum[Q], &tm.out, x, mt.row0 + first, a.add);
         };
-        unit(std::integral_constant<int, 0>());
-        if (!a.half) unit(std::integral_constant<int, 1>());
+        quarter(std::integral_constant<int, 0>());
+        quarter(std::integral_constant<int, 1>());
+        if (!a.half) {
+          quarter(std::integral_constant<int, 2>());
+          quarter(std::integral_constant<int, 3>());
+        }
       } else {
         ok = take();
         if (!ok) break;
-        const int chunks = any ? (a.half ? 2 : 4) : 0;
+        const int chunks = any ? step / 64 : 0;
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
           const int x = n0 + 64 * c;  // first output column
@@ -549,7 +566,7 @@ k_product(const __grid_constant__ ProductMaps tm, const __grid_constant__ Produc
             float v[32], u[32];
             load32(lanes_at() + 64 * c + 32 * H, v);
             if (KIND == kForward) {
-              if (a.half) load32(lanes_at() + 128 + 64 * c + 32 * H, u);
+              if (a.half) load32(lanes_at() + a.bn / 2 + 64 * c + 32 * H, u);
               forward32(a, bias, residual, x + 32 * H, cols - 32 * H, v, u,
                         [&](const float(&z)[32], bool up) { pack32<H>(up ? pu : pz, z); });
             }
@@ -612,8 +629,39 @@ static cudaError_t launch_one(const ProductMaps& tm, const ProductArgs& a, const
   return launch_after(kernel, grid, Cfg::kThreads, Cfg::kSmem, st, CG, tm, a, p);
 }
 
-static int64_t tiles_of(int64_t M, int N, int half, int rows) {
-  return ((M + rows - 1) / rows) * (half ? (half + 127) / 128 : (N + 255) / 256);
+static int64_t tiles_of(int64_t M, const ProductArgs& a, int rows) {
+  const int step = a.half ? a.bn / 2 : a.bn;
+  return ((M + rows - 1) / rows) * (((a.half ? a.half : a.N) + step - 1) / step);
+}
+
+// Columns of a tile: 256, or 192 or 128 where less of them lies past the last column.  A tile's time
+// grows with its columns plus a share that does not (that of 32 columns, roughly: the rows' loads and
+// the end of a tile).  `rounds` counts what a choice makes the fullest pair do; the plan's tiles are
+// not known here, and their number of column tiles stands for it.
+template <typename F>
+static int pick_bn(int half, bool f32, F&& rounds) {
+  int best = 256;
+  double least = 0;
+  for (int bn = 256; bn >= 128; bn -= 64) {
+    if (half && (bn == 192 || f32)) continue;  // (halves of 64 columns; fp32 sums of 128)
+    if (f32 && bn == 128) continue;
+    const double c = rounds(bn) * (bn + 32);
+    if (bn == 256 || c < least) least = c, best = bn;
+  }
+  return best;
+}
+static int pick_bn_dense(int M, int N, int half, bool f32) {
+  return pick_bn(half, f32, [&](int bn) {
+    const int step = half ? bn / 2 : bn;
+    const int64_t tiles = (int64_t)((M + 255) / 256) * (((half ? half : N) + step - 1) / step);
+    return (double)((tiles + 75) / 76);
+  });
+}
+static int pick_bn_grouped(int N, int half) {
+  return pick_bn(half, false, [&](int bn) {
+    const int step = half ? bn / 2 : bn;
+    return (double)(((half ? half : N) + step - 1) / step);
+  });
 }
 
 cudaError_t launch_linear(const LinearDims& d, const void* x, const void* w, const float* bias,
@@ -644,8 +692,9 @@ cudaError_t launch_linear(const LinearDims& d, const void* x, const void* w, con
   a.z = (uint16_t*)z;
   a.has_z = z != nullptr;
   a.status = status;
+  a.bn = pick_bn_dense(d.T, d.N, d.half, d.f32);
   *launches += 1;
-  const int64_t tiles = tiles_of(d.T, d.N, d.half, 256);
+  const int64_t tiles = tiles_of(d.T, a, 256);
   return d.f32 ? launch_one<true, kForward, true, true>(tm, a, PlanPtrs{}, tiles, st)
                : launch_one<true, kForward, true, false>(tm, a, PlanPtrs{}, tiles, st);
 }
@@ -666,8 +715,9 @@ cudaError_t launch_linear_dx(const LinearDims& d, const void* d_z, const void* w
   ProductArgs a = {};
   a.M = d.T, a.N = d.K, a.K = d.N;
   a.status = status;
+  a.bn = pick_bn_dense(d.T, d.K, 0, false);
   *launches += 1;
-  return launch_one<true, kInputGrad, true, false>(tm, a, PlanPtrs{}, tiles_of(d.T, d.K, 0, 256), st);
+  return launch_one<true, kInputGrad, true, false>(tm, a, PlanPtrs{}, tiles_of(d.T, a, 256), st);
 }
 
 cudaError_t launch_linear_dw(const LinearDims& d, const void* x, const void* d_z, float* d_w,
@@ -687,8 +737,9 @@ cudaError_t launch_linear_dw(const LinearDims& d, const void* x, const void* d_z
   a.M = d.K, a.N = d.N, a.K = d.T;
   a.add = add;
   a.status = status;
+  a.bn = pick_bn_dense(d.K, d.N, 0, true);
   *launches += 1;
-  return launch_one<true, kWeightGrad, true, true>(tm, a, PlanPtrs{}, tiles_of(d.K, d.N, 0, 256), st);
+  return launch_one<true, kWeightGrad, true, true>(tm, a, PlanPtrs{}, tiles_of(d.K, a, 256), st);
 }
 
 cudaError_t launch_grouped_gemm_act(const Dims& d, const PlanPtrs& p, int act, const void* recv,
@@ -720,7 +771,8 @@ cudaError_t launch_grouped_gemm_act(const Dims& d, const PlanPtrs& p, int act, c
   a.has_z = z != nullptr;
   a.status = p.status;
   // with the height left to the plan both are launched; the one it did not choose returns at once
-  const int64_t tiles = (int64_t)d.max_mtiles * (half ? (half + 127) / 128 : (d.Hp + 255) / 256);
+  a.bn = pick_bn_grouped(d.Hp, half);
+  const int64_t tiles = (int64_t)d.max_mtiles * tiles_of(1, a, 256);
   if (d.tile_m != 2 * kMmaM) {
     const cudaError_t e = launch_one<false, kForward, false, false>(tm, a, p, tiles, st);
     if (e != cudaSuccess) return e;
