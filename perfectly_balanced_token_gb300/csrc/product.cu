@@ -8,13 +8,13 @@
 // One kernel, C[M x N] = A[M x K] . B[K x N] on 256-row tiles of a CTA pair (cta_group::2) or
 // 128-row tiles of one CTA, 256 columns a tile:
 //  * warp 0 feeds a ring of 64-deep stages by TMA, warp 1's elected lane issues the MMAs into one of
-//    two accumulators in TMEM, warps 2..5 drain the other: bias, z, activation, residual and one
+//    two accumulators in TMEM, warps 2..9 drain the other: bias, z, activation, residual and one
 //    rounding happen in registers, so z and the activation never make a trip through memory that
 //    the caller did not ask for.
 //  * swiglu: a tile takes 128 gate columns and the 128 columns of the same numbers in the up half,
 //    so one lane holds both factors of a value.  On a pair, the first CTA brings the gates and the
 //    second the up columns of B; the MMA gives either CTA both for its rows.
-//  * outputs leave by TMA stores of 32 rows x 128 bytes, staged in shared memory; their maps clip
+//  * outputs leave by TMA stores of 32 rows x 32 columns, staged in shared memory; their maps clip
 //    what lies past the last row or column, so sizes need not divide the tile.  Rows of a group that
 //    ends inside a tile are stored one by one, as the next group's rows follow.
 //  * dense tiles are walked with a fixed stride, the plan's tiles claimed in order (tcgen05.cuh).
@@ -26,24 +26,24 @@
 
 namespace moonep {
 
+constexpr int kEpilogueWarps = 8;  // two for each 32 lanes of TMEM, half of a tile's columns each
+constexpr int kProductThreads = 64 + 32 * kEpilogueWarps;
+
 template <bool PAIR, bool F32>
 struct ProductCfg {
-  // fp32 sums of 128 columns a thread take eight epilogue warps
-  static constexpr int kEpilogueWarps = F32 ? 8 : 4;
-  static constexpr int kThreads = 64 + 32 * kEpilogueWarps;
   static constexpr int kStages = PAIR ? 6 : 4;
   static constexpr int kTileM = PAIR ? 256 : 128;
   static constexpr int kABytes = 128 * kDepth * 2;
   static constexpr int kBPanels = PAIR ? 2 : 4;  // of 64 columns, in one CTA
   static constexpr int kStageBytes = kABytes + kBPanels * kPanelBytes;
-  static constexpr int kOutBuffers = F32 ? 1 : 2;  // of 32 rows x 128 bytes, a warp
-  static constexpr int kOutBytes = kEpilogueWarps * kOutBuffers * 4096;
+  static constexpr int kOutWarpBytes = 4096;  // staging of a warp's stores
+  static constexpr int kOutBytes = kEpilogueWarps * kOutWarpBytes;
   static constexpr int kNumBars = 2 * kStages + 5 + 2 * kQueue;
   static constexpr int kBarBytes = kNumBars * 8 + 16 + 4 * kQueue;
   static constexpr int kSmem = kStages * kStageBytes + kOutBytes + 1024 + kBarBytes;
-  // With z kept, a tile has two or three stores where it had one, and waiting until TMA has read the
-  // buffer that the one before the last left costs more than a stage is worth (12000 rows x 1024 x
-  // 576, gelu and z: 69 -> 5x us): the last stage's memory becomes four buffers a warp in place of two.
+  // With z kept, 32 columns have two or three stores where they had one, and waiting until TMA has
+  // read the buffer of the one before the last costs more than a stage is worth: the last stage's
+  // memory becomes two more buffers a warp (12000 rows x 1024 x 576, gelu and z: 69 -> 61 us).
   static constexpr bool kCanDeepen = PAIR && !F32;
 };
 static_assert(ProductCfg<true, false>::kSmem <= 232448 && ProductCfg<true, true>::kSmem <= 232448 &&
@@ -85,18 +85,15 @@ struct Issue {  // the forms of one CTA and of a pair
   }
 };
 
-// A warp's staging buffers of 32 rows x 128 bytes (128-byte swizzle) and the stores from them.
+// A warp's staging buffers and the stores from them: boxes of 32 rows x 32 columns, bf16 (2 KB, 64-byte
+// swizzle; two or four buffers) or fp32 (4 KB, 128-byte swizzle; one).
 struct OutRing {
   uint8_t* base;
-  int buffers;  // 1, 2 or 4
+  int buffers;
   int n, lane;
-  static __device__ __forceinline__ uint32_t word(uint32_t v) { return v; }
-  static __device__ __forceinline__ uint32_t word(float v) { return __float_as_uint(v); }
-  // writes this lane's row (32 words) and stores the box at column x, row y
-  template <typename T>
-  __device__ __forceinline__ void put(const T (&v)[32], const CUtensorMap* m, int x, int y,
-                                      bool add) {
-    uint8_t* buf = base + (n & (buffers - 1)) * 4096;
+
+  __device__ __forceinline__ uint8_t* begin(int bytes) {
+    uint8_t* buf = base + (n & (buffers - 1)) * bytes;
     ++n;
     if (lane == 0) {  // until the store that had this buffer has read it
       if (buffers == 1) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
@@ -104,11 +101,9 @@ struct OutRing {
       else asm volatile("cp.async.bulk.wait_group.read 3;" ::: "memory");
     }
     __syncwarp();
-    uint4* row = reinterpret_cast<uint4*>(buf + lane * 128);
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      row[j ^ (lane & 7)] =
-          make_uint4(word(v[4 * j]), word(v[4 * j + 1]), word(v[4 * j + 2]), word(v[4 * j + 3]));
+    return buf;
+  }
+  __device__ __forceinline__ void end(const uint8_t* buf, const CUtensorMap* m, int x, int y, bool add) {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
     if (lane == 0) {
@@ -125,23 +120,30 @@ struct OutRing {
       asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
   }
+  __device__ __forceinline__ void put(const uint32_t (&v)[16], const CUtensorMap* m, int x, int y) {
+    uint8_t* buf = begin(2048);
+    uint4* row = reinterpret_cast<uint4*>(buf + lane * 64);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      row[j ^ ((lane >> 1) & 3)] = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    end(buf, m, x, y, false);
+  }
+  __device__ __forceinline__ void put(const float (&v)[32], const CUtensorMap* m, int x, int y, bool add) {
+    uint8_t* buf = begin(4096);
+    float4* row = reinterpret_cast<float4*>(buf + lane * 128);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      row[j ^ (lane & 7)] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    end(buf, m, x, y, add);
+  }
 };
 
-// The first `cols` (a multiple of 8) of a row's 64 bf16 values.
-__device__ __forceinline__ void put_row(const uint32_t (&v)[32], uint16_t* at, int cols) {
+// The first `cols` (a multiple of 8) of a row's 32 bf16 values.
+__device__ __forceinline__ void put_row(const uint32_t (&v)[16], uint16_t* at, int cols) {
   uint4* p = reinterpret_cast<uint4*>(at);
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (8 * j < cols) p[j] = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-}
-
-// The same of 32 values, rounded.
-__device__ __forceinline__ void put_z32(const float (&v)[32], uint16_t* at, int cols) {
-  uint4* p = reinterpret_cast<uint4*>(at);
-  auto two = [&](int i) { return pack_bf16x2(__float_as_uint(v[i]), __float_as_uint(v[i + 1])); };
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    if (8 * j < cols) p[j] = make_uint4(two(8 * j), two(8 * j + 2), two(8 * j + 4), two(8 * j + 6));
+    if (8 * j < cols) p[j] = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
 }
 
 // v += bias[0 .. 31], of which the first `cols` (a multiple of 8) are there; every lane has the same
@@ -175,12 +177,10 @@ __device__ __forceinline__ void add_residual(float (&v)[32], const uint16_t* at,
   }
 }
 
-// bf16 of v into the h-th half of p
-template <int H>
-__device__ __forceinline__ void pack32(uint32_t (&p)[32], const float (&v)[32]) {
+__device__ __forceinline__ void pack32(uint32_t (&p)[16], const float (&v)[32]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i)
-    p[16 * H + i] = pack_bf16x2(__float_as_uint(v[2 * i]), __float_as_uint(v[2 * i + 1]));
+    p[i] = pack_bf16x2(__float_as_uint(v[2 * i]), __float_as_uint(v[2 * i + 1]));
 }
 
 __device__ __forceinline__ void load32(uint32_t taddr, float (&v)[32]) {
@@ -211,7 +211,7 @@ __device__ __forceinline__ void forward32(const ProductArgs& a, const float* bia
 }
 
 template <bool PAIR, int KIND, bool DENSE, bool F32>
-__global__ void __launch_bounds__(ProductCfg<PAIR, F32>::kThreads, 1)
+__global__ void __launch_bounds__(kProductThreads, 1)
 k_product(const __grid_constant__ ProductMaps tm, const __grid_constant__ ProductArgs a,
           const __grid_constant__ PlanPtrs p) {
   static_assert(DENSE || !F32, "the grouped output is bf16");
@@ -261,10 +261,11 @@ k_product(const __grid_constant__ ProductMaps tm, const __grid_constant__ Produc
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull(b), 1);
-      mbar_init(tempty(b), (PAIR ? 2 : 1) * Cfg::kEpilogueWarps);
+      mbar_init(tempty(b), (PAIR ? 2 : 1) * kEpilogueWarps);
     }
     mbar_init(drain, 1);
-    if (!DENSE) queue_init(q, PAIR ? kQueueConsumers : kQueueConsumersSolo);
+    // who takes a tile: the issuer and the epilogue's warps, in a pair also the other CTA's feeder
+    if (!DENSE) queue_init(q, (PAIR ? 2 : 1) * (1 + kEpilogueWarps));
     *abort_flag = 0;
     fence_barrier_init();
     if (DENSE) grid_wait();
@@ -444,9 +445,12 @@ k_product(const __grid_constant__ ProductMaps tm, const __grid_constant__ Produc
   } else {
     // ---------------- epilogue (warps 2.., both CTAs) ----------------
     const int qw = warp & 3;         // TMEM lanes 32 qw .. are this warp's rows
-    const int hs = (warp - 2) >> 2;  // fp32: which half of the columns is this warp's
-    const int buffers = Cfg::kOutBuffers * (deep ? 2 : 1);
-    OutRing ring{out_stage + (warp - 2) * buffers * 4096, buffers, 0, lane};
+    const int hs = (warp - 2) >> 2;  // which half of the columns is this warp's
+    OutRing ring{out_stage + (warp - 2) * Cfg::kOutWarpBytes * (deep ? 2 : 1),
+                 F32 ? 1 : (deep ? 4 : 2), 0, lane};
+    // its columns of a tile: `own` from the accumulator's column hs own on (swiglu: gates, with the up
+    // columns of the same numbers bn / 2 further)
+    const int own = step / 2;
     const int ocols = a.half ? a.half : a.N;
     const int parts = F32 ? (KB + kPartBlocks - 1) / kPartBlocks : 1;
     int acc = 0;
@@ -492,22 +496,19 @@ k_product(const __grid_constant__ ProductMaps tm, const __grid_constant__ Produc
       const uint16_t* residual =
           a.residual != nullptr ? a.residual + (size_t)min(row, a.M - 1) * ocols : nullptr;
       const bool any = first < mt.rows;  // otherwise none of this warp's rows is stored
-      auto put = [&](const uint32_t (&v)[32], const CUtensorMap* m, int x, uint16_t* plain, int pitch,
+      auto put = [&](const float (&v)[32], const CUtensorMap* m, int x, uint16_t* plain, int pitch,
                      int cols) {
-        if (whole) ring.put(v, m, x, mt.row0 + first, false);
-        else if (valid) put_row(v, plain + (size_t)row * pitch + x, cols);
+        uint32_t packed[16];
+        pack32(packed, v);
+        if (whole) ring.put(packed, m, x, mt.row0 + first);
+        else if (valid) put_row(packed, plain + (size_t)row * pitch + x, cols);
         __syncwarp();
-      };
-      auto put_z = [&](const uint32_t (&pz)[32], const uint32_t (&pu)[32], int x, int cols) {
-        if (KIND != kForward || !a.has_z) return;
-        put(pz, &tm.z, x, a.z, a.N, cols);
-        if (a.half) put(pu, &tm.z_up, x, a.z + a.half, a.N, cols);
       };
       if constexpr (F32) {
         // up to 128 columns: for swiglu 64 gates and the 64 up columns of the same numbers, otherwise
         // half of the tile's
         float sum[4][32];
-        const int width = a.half ? 128 : a.bn / 2;
+        const int width = a.bn / 2;
         for (int k = 0; k < parts && ok; ++k) {
           ok = take();
           if (!ok) break;
@@ -531,16 +532,17 @@ k_product(const __grid_constant__ ProductMaps tm, const __grid_constant__ Produc
         if (!ok || !any) continue;
         auto quarter = [&](auto number) {  // 32 output columns
           constexpr int Q = decltype(number)::value;
-          if (32 * Q >= (a.half ? 64 : width)) return;
-          const int x = n0 + (a.half ? 64 : width) * hs + 32 * Q;
+          const int x = n0 + own * hs + 32 * Q;
           const int cols = min(32, ocols - x);
-          if (cols <= 0) return;
+          if (32 * Q >= own || cols <= 0) return;
           if (KIND == kForward)
-            // (z in bf16 goes row by row: the sums leave no registers to collect 64 columns in)
             forward32(a, bias, residual, x, cols, sum[Q], sum[(2 + Q) & 3],
                       [&](const float(&z)[32], bool up) {
+                        // (bf16, and no buffer of its own: row by row)
+                        uint32_t packed[16];
+                        pack32(packed, z);
                         if (a.has_z && valid)
-                          put_z32(z, a.z + (size_t)row * a.N + (up ? a.half : 0) + x, cols);
+                          put_row(packed, a.z + (size_t)row * a.N + (up ? a.half : 0) + x, cols);
                         __syncwarp();
                       });
           ring.put(sum[Q], &tm.out, x, mt.row0 + first, a.add);
@@ -554,28 +556,22 @@ k_product(const __grid_constant__ ProductMaps tm, const __grid_constant__ Produc
       } else {
         ok = take();
         if (!ok) break;
-        const int chunks = any ? step / 64 : 0;
 #pragma unroll 1
-        for (int c = 0; c < chunks; ++c) {
-          const int x = n0 + 64 * c;  // first output column
-          const int cols = min(64, ocols - x);
+        for (int c = own * hs; any && c < own * (hs + 1); c += 32) {
+          const int x = n0 + c;  // first output column
+          const int cols = min(32, ocols - x);
           if (cols <= 0) break;
-          uint32_t pz[32], pu[32], po[32];
-          auto half = [&](auto h) {
-            constexpr int H = decltype(h)::value;
-            float v[32], u[32];
-            load32(lanes_at() + 64 * c + 32 * H, v);
-            if (KIND == kForward) {
-              if (a.half) load32(lanes_at() + a.bn / 2 + 64 * c + 32 * H, u);
-              forward32(a, bias, residual, x + 32 * H, cols - 32 * H, v, u,
-                        [&](const float(&z)[32], bool up) { pack32<H>(up ? pu : pz, z); });
-            }
-            pack32<H>(po, v);
-          };
-          half(std::integral_constant<int, 0>());
-          half(std::integral_constant<int, 1>());
-          put(po, &tm.out, x, a.out, ocols, cols);
-          put_z(pz, pu, x, cols);
+          float v[32], u[32];
+          load32(lanes_at() + c, v);
+          if (KIND == kForward) {
+            if (a.half) load32(lanes_at() + a.bn / 2 + c, u);
+            forward32(a, bias, residual, x, cols, v, u, [&](const float(&z)[32], bool up) {
+              if (!a.has_z) return;
+              if (up) put(z, &tm.z_up, x, a.z + a.half, a.N, cols);
+              else put(z, &tm.z, x, a.z, a.N, cols);
+            });
+          }
+          put(v, &tm.out, x, a.out, ocols, cols);
         }
         release();
       }
@@ -615,7 +611,7 @@ static cudaError_t launch_one(const ProductMaps& tm, const ProductArgs& a, const
     cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * std::max(1, sm_count_gemm() / 2));
-    cfg.blockDim = dim3(Cfg::kThreads);
+    cfg.blockDim = dim3(kProductThreads);
     cfg.dynamicSmemBytes = Cfg::kSmem;
     cfg.attrs = &cluster;
     cfg.numAttrs = 1;
@@ -626,7 +622,7 @@ static cudaError_t launch_one(const ProductMaps& tm, const ProductArgs& a, const
   });
   if (e != cudaSuccess) return e;
   const unsigned grid = CG * (unsigned)std::max<int64_t>(1, std::min<int64_t>(most, tiles));
-  return launch_after(kernel, grid, Cfg::kThreads, Cfg::kSmem, st, CG, tm, a, p);
+  return launch_after(kernel, grid, kProductThreads, Cfg::kSmem, st, CG, tm, a, p);
 }
 
 static int64_t tiles_of(int64_t M, const ProductArgs& a, int rows) {
@@ -675,13 +671,13 @@ cudaError_t launch_linear(const LinearDims& d, const void* x, const void* w, con
   ProductMaps tm;
   const int ocols = d.half ? d.half : d.N;
   if (!encode_matrix(&tm.a, x, d.K, d.T, d.K, 128) || !encode_matrix(&tm.b, w, d.N, d.K, d.N, 64) ||
-      !encode_matrix(&tm.out, out, ocols, d.T, ocols, 32, d.f32))
+      !encode_out(&tm.out, out, ocols, d.T, ocols, d.f32))
     return cudaErrorInvalidValue;
   tm.b_slots = tm.b;
   tm.z = tm.z_up = tm.out;
   if (z != nullptr) {  // the halves have maps of their own, so that either is clipped at its end
-    if (!encode_matrix(&tm.z, z, ocols, d.T, d.N, 32)) return cudaErrorInvalidValue;
-    if (d.half && !encode_matrix(&tm.z_up, (uint16_t*)z + d.half, ocols, d.T, d.N, 32))
+    if (!encode_out(&tm.z, z, ocols, d.T, d.N)) return cudaErrorInvalidValue;
+    if (d.half && !encode_out(&tm.z_up, (uint16_t*)z + d.half, ocols, d.T, d.N))
       return cudaErrorInvalidValue;
   }
   ProductArgs a = {};
@@ -708,7 +704,7 @@ cudaError_t launch_linear_dx(const LinearDims& d, const void* d_z, const void* w
   }
   ProductMaps tm;
   if (!encode_matrix(&tm.a, d_z, d.N, d.T, d.N, 128) || !encode_matrix(&tm.b, w, d.N, d.K, d.N, 128) ||
-      !encode_matrix(&tm.out, d_x, d.K, d.T, d.K, 32))
+      !encode_out(&tm.out, d_x, d.K, d.T, d.K))
     return cudaErrorInvalidValue;
   tm.b_slots = tm.b;
   tm.z = tm.z_up = tm.out;
@@ -729,7 +725,7 @@ cudaError_t launch_linear_dw(const LinearDims& d, const void* x, const void* d_z
   }
   ProductMaps tm;
   if (!encode_matrix(&tm.a, x, d.K, d.T, d.K, 64) || !encode_matrix(&tm.b, d_z, d.N, d.T, d.N, 64) ||
-      !encode_matrix(&tm.out, d_w, d.N, d.K, d.N, 32, true))
+      !encode_out(&tm.out, d_w, d.N, d.K, d.N, true))
     return cudaErrorInvalidValue;
   tm.b_slots = tm.b;
   tm.z = tm.z_up = tm.out;
@@ -751,15 +747,15 @@ cudaError_t launch_grouped_gemm_act(const Dims& d, const PlanPtrs& p, int act, c
   const bool slots = w_slot != nullptr && d.B > 0;
   if (!encode_matrix(&tm.a, recv, d.H, d.N, d.H, 128) ||
       !encode_matrix(&tm.b, w_home, d.Hp, (int64_t)d.E * d.H, d.Hp, 64) ||
-      !encode_matrix(&tm.out, y, ocols, d.N, ocols, 32))
+      !encode_out(&tm.out, y, ocols, d.N, ocols))
     return cudaErrorInvalidValue;
   tm.b_slots = tm.b;
   if (slots && !encode_matrix(&tm.b_slots, w_slot, d.Hp, (int64_t)d.R * d.B * d.H, d.Hp, 64))
     return cudaErrorInvalidValue;
   tm.z = tm.z_up = tm.out;
   if (z != nullptr) {
-    if (!encode_matrix(&tm.z, z, ocols, d.N, d.Hp, 32)) return cudaErrorInvalidValue;
-    if (half && !encode_matrix(&tm.z_up, (uint16_t*)z + half, ocols, d.N, d.Hp, 32))
+    if (!encode_out(&tm.z, z, ocols, d.N, d.Hp)) return cudaErrorInvalidValue;
+    if (half && !encode_out(&tm.z_up, (uint16_t*)z + half, ocols, d.N, d.Hp))
       return cudaErrorInvalidValue;
   }
   ProductArgs a = {};

@@ -40,21 +40,30 @@ __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr));
 }
 
-// A row-major matrix [rows][cols] with `pitch` elements a row; boxes of 128 bytes x `box` rows,
-// 128-byte swizzle.
-inline bool encode_matrix(CUtensorMap* m, const void* base, int cols, int64_t rows, int64_t pitch,
-                          int box, bool f32 = false) {
+// A row-major matrix [rows][cols] with `pitch` elements a row.
+inline bool encode_boxes(CUtensorMap* m, const void* base, int cols, int64_t rows, int64_t pitch,
+                         int box_cols, int box_rows, bool f32) {
   EncodeTiledFn enc = get_encode();
   if (!enc) return false;
   const int size = f32 ? 4 : 2;
   cuuint64_t dim[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
   cuuint64_t stride[1] = {(cuuint64_t)(pitch * size)};
-  cuuint32_t b[2] = {(cuuint32_t)(128 / size), (cuuint32_t)box};
+  cuuint32_t b[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
   cuuint32_t one[2] = {1, 1};
   return enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
              const_cast<void*>(base), dim, stride, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+             box_cols * size == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// An operand: boxes of 64 bf16 (128 bytes, 128-byte swizzle) x `box` rows.
+inline bool encode_matrix(CUtensorMap* m, const void* base, int cols, int64_t rows, int64_t pitch,
+                          int box) {
+  return encode_boxes(m, base, cols, rows, pitch, 64, box, false);
+}
+// An output: boxes of 32 columns x 32 rows.
+inline bool encode_out(CUtensorMap* m, const void* base, int cols, int64_t rows, int64_t pitch,
+                       bool f32 = false) {
+  return encode_boxes(m, base, cols, rows, pitch, 32, 32, f32);
 }
 
 // product_split.cu: products of few tiles, split along the depth.
