@@ -62,31 +62,29 @@ __device__ __forceinline__ F2 sigmoid2(F2 z) {
 }
 
 // P(N(0,1) <= z), and the density.
-// For a = |z| the tail is e G(a), e = exp(-a^2 / 2), G(a) = erfcx(a / sqrt 2) / 2, and (1 + a / 2) G(a)
-// is smooth in t = (a - 4) / (a + 4) over all of [0, inf) (the substitution of Shepherd and
-// Laframboise, "Chebyshev approximation of (1 + 2x) exp(x^2) erfc x in 0 <= x < inf", 1981): a
-// polynomial of degree 8, fitted to the smallest relative error (2.2e-8), one reciprocal for both
-// quotients, and no branch; 1 + erf would cancel there.  Roundings of a^2 and of the exponent make
-// it 2^-24 a^2 of the tail.  (erfcf, with a branch for each range, made the gelu epilogue of a
+// For a = |z| the tail is e G(a), e = exp(-a^2 / 2), G(a) = erfcx(a / sqrt 2) / 2, and (a + k) G(a) is
+// smooth in t = (a - k) / (a + k) = 1 - 2k / (a + k) over all of [0, inf) (the substitution of Shepherd
+// and Laframboise, "Chebyshev approximation of (1 + 2x) exp(x^2) erfc x in 0 <= x < inf", 1981):
+// with k = 4.25 a polynomial of degree 7, fitted to the smallest relative error (1.2e-7), one
+// reciprocal and no branch, where 1 + erf would cancel.  Roundings of a^2 and of the exponent make
+// it 2^-24 a^2 of the tail more.  (erfcf, with a branch for each range, made the gelu epilogue of a
 // tile take several times as long as its product.)  From a = 16 on e is 0.
 __device__ __forceinline__ F2 normal_cdf2(F2 z, F2* density = nullptr) {
   float x, y;
   z.get(x, y);
   const F2 a(fminf(fabsf(x), 16.f), fminf(fabsf(y), 16.f));
   const F2 e = exp2_2(a * a * F2(-0.72134752044448170f));
-  const F2 u = a + F2(4.f), v = fma2(a, F2(0.5f), F2(1.f));
-  const F2 r = recip2(u * v);
-  const F2 t = (a + F2(-4.f)) * v * r;
-  F2 p(2.554573875386e-04f);
-  p = fma2(p, t, F2(1.216406453750e-04f));
-  p = fma2(p, t, F2(-2.259995089844e-03f));
-  p = fma2(p, t, F2(4.738154821098e-03f));
-  p = fma2(p, t, F2(-6.626949179176e-04f));
-  p = fma2(p, t, F2(-2.155544050038e-02f));
-  p = fma2(p, t, F2(6.918913871050e-02f));
-  p = fma2(p, t, F2(-1.335505396128e-01f));
-  p = fma2(p, t, F2(2.832319140434e-01f));
-  const F2 tail = e * p * (u * r);
+  const F2 r = recip2(a + F2(4.25f));
+  const F2 t = fma2(r, F2(-8.5f), F2(1.f));
+  F2 p(2.106905449182e-03f);
+  p = fma2(p, t, F2(-1.038260525092e-03f));
+  p = fma2(p, t, F2(-1.938312128186e-02f));
+  p = fma2(p, t, F2(8.534678816795e-02f));
+  p = fma2(p, t, F2(-2.205096930265e-01f));
+  p = fma2(p, t, F2(4.182209968567e-01f));
+  p = fma2(p, t, F2(-6.251299977303e-01f));
+  p = fma2(p, t, F2(7.595543265343e-01f));
+  const F2 tail = e * r * p;
   if (density != nullptr) *density = e * F2(0.3989422804f);
   float tx, ty, cx, cy;
   tail.get(tx, ty);

@@ -15,7 +15,7 @@ constexpr int kPanelBytes = 64 * 128;  // 64 rows of 64 bf16
 // fp32 sums do not hold, always towards zero, so a long sum drifts: against 64 bits, with the whole
 // depth in one accumulator, 7e-6 of C at a depth of 7168 and past 2e-5 at 32768.  The epilogues add
 // the parts in registers, rounding to nearest.  (A bf16 C's own rounding is 250 times larger.)
-constexpr int kPartBlocks = 8;
+constexpr int kPartBlocks = 12;
 
 enum Kind { kForward, kInputGrad, kWeightGrad };
 
