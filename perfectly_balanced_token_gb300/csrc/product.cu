@@ -46,6 +46,7 @@ struct ProductCfg {
   // memory becomes two more buffers a warp (12000 rows x 1024 x 576, gelu and z: 69 -> 61 us).
   static constexpr bool kCanDeepen = PAIR && !F32;
 };
+static_assert(kTmapSlots > ProductCfg<true, false>::kStages, "a map's copy outlives the loads in flight");
 static_assert(ProductCfg<true, false>::kSmem <= 232448 && ProductCfg<true, true>::kSmem <= 232448 &&
                   ProductCfg<false, false>::kSmem <= 232448,
               "shared memory of a CTA");
@@ -328,6 +329,17 @@ k_product(const __grid_constant__ ProductMaps tm, const __grid_constant__ Produc
       bool ok = true;
       int next = 0;
       if (!DENSE && leader) next = atomicAdd(sched, 1);
+      // Rows past a group's end are loaded as zeros, through copies of A's map that end there: they
+      // are never stored, but products of zeros take less of the power that limits long products.
+      // A copy is rewritten eight such tiles later, when the loads through it are over.
+      constexpr bool kCut = PAIR && !DENSE;
+      uint4* maps = kCut ? reinterpret_cast<uint4*>(p.tmaps) + (size_t)blockIdx.x * kTmapSlots * 16 : nullptr;
+      int slot = 0;
+      if (kCut) {
+        const uint4* from = reinterpret_cast<const uint4*>(&tm.a);
+        for (int i = 0; i < kTmapSlots; ++i)
+          for (int j = 0; j < 8; ++j) maps[i * 16 + j] = from[j];
+      }
       for (int i = 0; ok; ++i) {
         int t;
         if (DENSE) {
@@ -347,7 +359,19 @@ k_product(const __grid_constant__ ProductMaps tm, const __grid_constant__ Produc
         tile(t, mt, n0);
         const CUtensorMap* bmap = mt.wsel >= 0 ? &tm.b : &tm.b_slots;
         const int wrow = (mt.wsel >= 0 ? mt.wsel : (-1 - mt.wsel)) * a.wrows;
-        const int row0 = mt.row0 + (int)crank * 128;
+        int row0 = mt.row0 + (int)crank * 128;
+        const CUtensorMap* amap = &tm.a;
+        if (kCut && mt.rows < ((int)crank + 1) * 128) {
+          if (mt.rows <= (int)crank * 128) {
+            row0 = a.M;  // no row of this CTA's: a box past the last one, all zeros
+          } else {
+            uint4* m = maps + slot * 16;
+            tmap_set_dim1(m, mt.row0 + mt.rows);
+            tmap_publish(m);
+            amap = reinterpret_cast<const CUtensorMap*>(m);
+            if (++slot == kTmapSlots) slot = 0;
+          }
+        }
         // this CTA's columns of B
         // (past the first bn / 64 of one CTA, or bn / 2 columns of one of two, there is none)
         const int mine = PAIR ? (a.half ? (int)crank * a.half + n0 : n0 + (int)crank * (a.bn / 2)) : n0;
@@ -367,7 +391,7 @@ k_product(const __grid_constant__ ProductMaps tm, const __grid_constant__ Produc
             Op::load(sa, &tm.a, fb, row0, k0);
             Op::load(sa + kPanelBytes, &tm.a, fb, row0 + 64, k0);
           } else {
-            Op::load(sa, &tm.a, fb, k0, row0);
+            Op::load(sa, amap, fb, k0, row0);
           }
           if (BMN) {
 #pragma unroll
@@ -622,6 +646,7 @@ static cudaError_t launch_one(const ProductMaps& tm, const ProductArgs& a, const
   });
   if (e != cudaSuccess) return e;
   const unsigned grid = CG * (unsigned)std::max<int64_t>(1, std::min<int64_t>(most, tiles));
+  if (!DENSE && grid > (unsigned)kMaxGemmCtas) return cudaErrorInvalidConfiguration;  // maps' copies
   return launch_after(kernel, grid, kProductThreads, Cfg::kSmem, st, CG, tm, a, p);
 }
 
