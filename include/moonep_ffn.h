@@ -81,8 +81,8 @@ int moonep_act_backward_workspace_bytes(int64_t rows, int32_t cols, size_t* byte
  * accumulate = 1).  z bf16 [rows][cols], d_out bf16 [rows][cols, or cols / 2 for
  * swiglu], d_z bf16 [rows][cols]; d_bias fp32 [cols] or NULL, and scratch (overwritten)
  * with it.  With MOONEP_ACT_NONE z is not read and may be NULL, and so may d_z if
- * d_bias is not.  cols a multiple of 8 (16 for swiglu), 0 <= rows < 2^40
- * (MOONEP_ERR_SHAPE). */
+ * d_bias is not.  cols a multiple of 8 (16 for swiglu) below 2^31 - 512, 0 <= rows <
+ * 2^40 (MOONEP_ERR_SHAPE). */
 int moonep_act_backward(int64_t rows, int32_t cols, int32_t act, const uint16_t* z,
                         const uint16_t* d_out, uint16_t* d_z, float* d_bias, int32_t accumulate,
                         void* scratch, void* stream);
@@ -102,7 +102,7 @@ int moonep_grouped_act_backward_workspace_bytes(const moonep_dims* dims, size_t*
 /* moonep_act_backward on rows as moonep_grouped_gemm_act makes them: z, d_z bf16
  * [R][C][Hp], d_y bf16 [R][C][Hp, or Hp / 2]; d_bias fp32 [E][Hp] or NULL: every
  * expert's sum over all its rows, home or slot (0 for an expert without rows).  d_z
- * then goes to moonep_grouped_gemm_dx and _dw. */
+ * then goes to moonep_grouped_gemm_dx and _dw.  Hp below 2^26 (MOONEP_ERR_SHAPE). */
 int moonep_grouped_act_backward(const moonep_dims* dims, void* plan_ws, int32_t act,
                                 const uint16_t* z, const uint16_t* d_y, uint16_t* d_z, float* d_bias,
                                 int32_t accumulate, void* scratch, void* stream);

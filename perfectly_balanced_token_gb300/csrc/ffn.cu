@@ -44,7 +44,7 @@ static int check_act_rows(int64_t rows, int32_t cols, int act) {
   if (rows < 0 || cols <= 0) return MOONEP_ERR_ARG;
   const int rc = check_act(act, cols);
   if (rc != MOONEP_OK) return rc;
-  return rows >= (int64_t(1) << 40) ? MOONEP_ERR_SHAPE : MOONEP_OK;
+  return rows >= (int64_t(1) << 40) || cols >= kMostRows ? MOONEP_ERR_SHAPE : MOONEP_OK;
 }
 
 // the arguments that the activation's two gradients share
@@ -195,6 +195,7 @@ int moonep_grouped_act_backward(const moonep_dims* dims, void* plan_ws, int32_t 
   MOONEP_CHECK(check_act(act, d.Hp));
   if (accumulate != 0 && accumulate != 1) return MOONEP_ERR_ARG;
   MOONEP_CHECK(check_act_buffers(act, z, d_y, d_z, d_bias, scratch));
+  if (d.Hp >= 1 << 26) return MOONEP_ERR_SHAPE;  // 1024 columns of d_bias a block
   int n = 0;
   const cudaError_t e = launch_grouped_act_backward(d, P, act, z, d_y, d_z, d_bias, accumulate,
                                                     (float*)scratch, (cudaStream_t)stream, &n);

@@ -107,6 +107,8 @@ def test_act_backward_is_checked(lib):
     assert act(lib, cols=12) == _lib.ERR_SHAPE
     assert act(lib, cols=24, act=4) == _lib.ERR_SHAPE
     assert act(lib, rows=1 << 40) == _lib.ERR_SHAPE
+    assert act(lib, cols=(1 << 31) - 256) == _lib.ERR_SHAPE
+    assert grouped_act(lib, mx.dims(1, 2, 0, 1, 1, 64, 1 << 26, 1)) == _lib.ERR_SHAPE
     for call in (act, lambda lib, **kw: grouped_act(lib, d, **kw)):
         for bad in (-1, 5):
             assert call(lib, act=bad) == _lib.ERR_ARG
