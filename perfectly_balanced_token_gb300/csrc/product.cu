@@ -655,20 +655,18 @@ static int64_t tiles_of(int64_t M, const ProductArgs& a, int rows) {
   return ((M + rows - 1) / rows) * (((a.half ? a.half : a.N) + step - 1) / step);
 }
 
-// Columns of a tile: 256, or 192 or 128 where less of them lies past the last column.  A tile's time
-// grows with its columns plus a share that does not (that of 32 columns, roughly: the rows' loads and
-// the end of a tile).  `rounds` counts what a choice makes the fullest pair do; the plan's tiles are
-// not known here, and their number of column tiles stands for it.
+// Columns of a tile: 256, or 192 or 128 where that makes up for what a narrower tile loses.  It does
+// not take that much less time, as its rows are loaded all the same and L2's feed is what bounds the
+// wide tile already: 0.88 and 0.75 of a wide one's (8192 x 7168 x 384: 39.5 us with 256, 35.2 with 192;
+// 4096 x 7168 x 4096 of swiglu: 204 us with 128, 1xx with 256).  `rounds` counts what a choice makes the
+// fullest pair do; the plan's tiles are not known here, and their number of column tiles stands for it.
 template <typename F>
 static int pick_bn(int half, bool f32, F&& rounds) {
   int best = 256;
-  double least = 0;
-  for (int bn = 256; bn >= 128; bn -= 64) {
-    if (half && (bn == 192 || f32)) continue;  // (halves of 64 columns; fp32 sums of 128)
-    if (f32 && bn == 128) continue;
-    const double c = rounds(bn) * (bn + 32);
-    if (bn == 256 || c < least) least = c, best = bn;
-  }
+  double least = rounds(256);
+  // (halves of 64 columns; fp32 sums of 192 or 256)
+  if (!half && 0.88 * rounds(192) < least) least = 0.88 * rounds(192), best = 192;
+  if (!f32 && 0.75 * rounds(128) < least) best = 128;
   return best;
 }
 static int pick_bn_dense(int M, int N, int half, bool f32) {
