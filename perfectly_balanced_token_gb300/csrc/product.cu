@@ -307,16 +307,29 @@ k_product(const __grid_constant__ ProductMaps tm, const __grid_constant__ Produc
     *abort_flag = 1;
     set_error(a.status, MOONEP_ERR_TIMEOUT);
   };
-  // tile t's rows (first, number, weight and rank as the plan lists them) and first column
+  // Tile t's rows (first, number, weight and rank as the plan lists them) and first column.  The tiles
+  // that run together are to be near a square of rows and columns, which needs the fewest panels: strips
+  // of 8 column tiles, in a strip one row tile after the other (65536 x 7168 x 4096: 2309 us with rows
+  // across all 16 columns, 2231 so); of the plan's tiles, whose weights differ from group to group,
+  // blocks of 18 row tiles are taken strip by strip (131072 rows: 5117 and 5078 us).
+  constexpr int kStrip = 8, kBlockRows = 18;
   auto tile = [&](int t, MTile& mt, int& n0) {
+    const int rows = DENSE ? MT : kBlockRows;
+    const int block = DENSE ? 0 : t / (rows * NT);
+    t -= block * rows * NT;
+    const int here = DENSE ? MT : min(rows, MT - block * rows);
+    const int strip = t / (here * kStrip);
+    t -= strip * here * kStrip;
+    const int wide = min(kStrip, NT - strip * kStrip);
+    const int r = t / wide;
+    n0 = (strip * kStrip + t - r * wide) * step;
     if (DENSE) {
-      mt.row0 = (t / NT) * Cfg::kTileM;
+      mt.row0 = r * Cfg::kTileM;
       mt.rows = min(Cfg::kTileM, a.M - mt.row0);
       mt.wsel = 0;
     } else {
-      mt = p.mtiles[t / NT];
+      mt = p.mtiles[block * rows + r];
     }
-    n0 = (t % NT) * step;
   };
 
   if (skip) {
@@ -380,13 +393,17 @@ k_product(const __grid_constant__ ProductMaps tm, const __grid_constant__ Produc
           return !PAIR && a.half && j >= panels / 2 ? a.half + n0 + 64 * (j - panels / 2) : mine + 64 * j;
         };
         const uint32_t bytes = Cfg::kABytes + (BMN ? panels : Cfg::kBPanels) * kPanelBytes;
+        // Input gradient: row tiles begin at other blocks of the depth, so that the pairs that read one
+        // panel of w, whose rows lie 2 N bytes apart, do not do so at the same moment (8192 x 7168 x
+        // 4096: 284 -> 262 us).  The products along N-major panels are faster in step (271 and 280).
+        const int turn = KIND == kInputGrad ? (int)((unsigned)(mt.row0 / Cfg::kTileM) * 7u % (unsigned)KB) : 0;
         for (int kb = 0; kb < KB; ++kb) {
           if (!mbar_wait(empty(stage), phase ^ 1u, abort_flag)) { ok = false; break; }
           const uint32_t fb = PAIR ? pair_map(full(stage), 0) : full(stage);
           if (leader) mbar_expect_tx(full(stage), (PAIR ? 2 : 1) * bytes);
           const uint32_t sa = smem_u32(smem + stage * Cfg::kStageBytes);
           const uint32_t sb = sa + Cfg::kABytes;
-          const int k0 = kb * kDepth;
+          const int k0 = (kb + turn < KB ? kb + turn : kb + turn - KB) * kDepth;
           if (AMN) {
             Op::load(sa, &tm.a, fb, row0, k0);
             Op::load(sa + kPanelBytes, &tm.a, fb, row0 + 64, k0);
@@ -658,7 +675,7 @@ static int64_t tiles_of(int64_t M, const ProductArgs& a, int rows) {
 // Columns of a tile: 256, or 192 or 128 where that makes up for what a narrower tile loses.  It does
 // not take that much less time, as its rows are loaded all the same and L2's feed is what bounds the
 // wide tile already: 0.88 and 0.75 of a wide one's (8192 x 7168 x 384: 39.5 us with 256, 35.2 with 192;
-// 4096 x 7168 x 4096 of swiglu: 204 us with 128, 1xx with 256).  `rounds` counts what a choice makes the
+// 4096 x 7168 x 4096 of swiglu: 204 us with 128, 150 with 256).  `rounds` counts what a choice makes the
 // fullest pair do; the plan's tiles are not known here, and their number of column tiles stands for it.
 template <typename F>
 static int pick_bn(int half, bool f32, F&& rounds) {
