@@ -21,7 +21,7 @@ namespace moonep {
 // ---------------------------------------------------------------------------
 constexpr int kActThreads = 256;
 constexpr int kActWarps = kActThreads / 32;
-constexpr int kActBlocks = 3;       // a multiprocessor
+constexpr int act_blocks(int act) { return act == kActSwiglu ? 3 : 4; }  // a multiprocessor
 constexpr int kActMostChunks = 512;  // dense: rows of scratch
 
 struct ActArgs {
@@ -132,7 +132,7 @@ __device__ __forceinline__ void act_chunk(const ActArgs& a, float (*part)[kActWa
 
 // plan: 0 = none, 1 = chunks are its work tiles, 2 = only its status counts
 template <int ACT>
-__global__ void __launch_bounds__(kActThreads, kActBlocks)
+__global__ void __launch_bounds__(kActThreads, act_blocks(ACT))
 k_act_backward(ActArgs a, PlanPtrs p, int plan) {
   __shared__ float part[ACT == kActSwiglu ? 2 : 1][kActWarps][256];
   grid_wait();
@@ -246,8 +246,8 @@ static cudaError_t launch_act(int act, const ActArgs& a, const PlanPtrs& p, int 
 }
 
 // Dense chunks: two rounds of blocks (one leaves the slowest multiprocessor alone at the end).
-static int64_t cut_rows(ActArgs* a) {
-  const int64_t blocks = (int64_t)sm_count_gemm() * kActBlocks * 2;
+static int64_t cut_rows(ActArgs* a, int act) {
+  const int64_t blocks = (int64_t)sm_count_gemm() * act_blocks(act) * 2;
   const int64_t most = std::max<int64_t>(1, std::min<int64_t>(act_chunks(a->rows), blocks / a->strips));
   a->chunk = (a->rows + most - 1) / most;
   return (a->rows + a->chunk - 1) / a->chunk;
@@ -259,7 +259,7 @@ cudaError_t launch_act_backward(int64_t rows, int cols, int act, const void* z, 
   ActArgs a{rows, 0, cols, 0, 0, (const uint16_t*)z, (const uint16_t*)d_out, (uint16_t*)d_z,
             d_bias ? scratch : nullptr};
   cut_columns(&a, act, 32);
-  const int64_t chunks = cut_rows(&a);
+  const int64_t chunks = cut_rows(&a, act);
   cudaError_t e = launch_act(act, a, PlanPtrs{}, 0, chunks, st);
   *launches += 1;
   if (e != cudaSuccess || d_bias == nullptr) return e;
@@ -276,7 +276,7 @@ cudaError_t launch_grouped_act_backward(const Dims& d, const PlanPtrs& p, int ac
   // (rows of one expert matter to the sums alone; work tiles are few, so narrower strips of them even
   // out the multiprocessors' shares)
   cut_columns(&a, act, d_bias ? 16 : 32);
-  const int64_t chunks = d_bias ? d.max_mtiles : cut_rows(&a);
+  const int64_t chunks = d_bias ? d.max_mtiles : cut_rows(&a, act);
   const cudaError_t e = launch_act(act, a, p, d_bias ? 1 : 2, chunks, st);
   *launches += 1;
   if (e != cudaSuccess || d_bias == nullptr) return e;
