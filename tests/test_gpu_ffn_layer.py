@@ -241,6 +241,16 @@ def test_stream_argument():
     assert torch.equal(out, want)
 
 
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    from perfectly_balanced_token_gb300 import _ffn
+    x, w, out, st = bf(4, 64), bf(64, 64), bf(4, 64), word()
+    monkeypatch.setattr(_ffn, "_device", lambda: 1)  # as if another device were the current one
+    before = mx.moonep_launch_count()
+    with pytest.raises(ValueError, match="x is on device 0, the current one is 1"):
+        mx.moonep_linear(mx.linear_dims(4, 64, 64), x, w, out, st)
+    assert mx.moonep_launch_count() == before
+
+
 @pytest.mark.parametrize("T,K,N", [(1, 2048, 2048), (40, 7168, 384), (1000, 1032, 520), (6000, 512, 1032)])
 def test_products_repeat_launch_after_launch(T, K, N):
     # launches overlap the end of the one before: each writes what one alone does
