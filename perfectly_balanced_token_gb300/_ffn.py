@@ -25,6 +25,9 @@ _device = _lib._raw_device or torch.cuda.current_device
 
 
 def _ptr(t, dtype, numel, name, allow_none=False):
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.is_cuda and t.get_device() == _device()
+            and t.is_contiguous() and (numel is None or t.numel() == numel)):
+        return t.data_ptr()
     p = _lib._ptr(t, dtype, numel, name, allow_none)
     if t is not None and t.get_device() != _device():
         raise ValueError(f"{name} is on device {t.get_device()}, the current one is {_device()}")
@@ -119,11 +122,17 @@ def moonep_linear_dw(ld, x, d_z, d_w, status, accumulate=False, stream=None):
         _ptr(status, torch.int32, 1, "status"), _stream(stream)), "moonep_linear_dw")
 
 
+_act_scratch: dict = {}  # scratch bytes of (rows, cols) already asked for
+
+
 def moonep_act_backward_workspace_bytes(rows: int, cols: int) -> int:
-    n = ctypes.c_size_t(0)
-    _check(library().moonep_act_backward_workspace_bytes(rows, cols, ctypes.byref(n)),
-           "moonep_act_backward_workspace_bytes")
-    return n.value
+    size = _act_scratch.get((rows, cols))
+    if size is None:
+        n = ctypes.c_size_t(0)
+        _check(library().moonep_act_backward_workspace_bytes(rows, cols, ctypes.byref(n)),
+               "moonep_act_backward_workspace_bytes")
+        size = _keep(_act_scratch, (rows, cols), n.value)
+    return size
 
 
 def _scratch(t, need):
