@@ -10,7 +10,7 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import _check, _keep, _stream, _ws, moonep_dims
+from ._lib import _check, _keep, _stream, moonep_dims
 
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3, "swiglu": 4}
 OUT_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
@@ -25,6 +25,8 @@ _device = _lib._raw_device or torch.cuda.current_device
 
 
 def _ptr(t, dtype, numel, name, allow_none=False):
+    if t is None and allow_none:
+        return None
     if (type(t) is torch.Tensor and t.dtype is dtype and t.is_cuda and t.get_device() == _device()
             and t.is_contiguous() and (numel is None or t.numel() == numel)):
         return t.data_ptr()
@@ -159,17 +161,31 @@ def moonep_act_backward(z, d_out, d_z, act="none", d_bias=None, scratch=None, ac
         int(bool(accumulate)), _scratch(scratch, need), _stream(stream)), "moonep_act_backward")
 
 
+_plans: dict = {}  # of plan dims already seen, by their fields
+
+
+def _plan_sizes(d):
+    """(workspace bytes, N, N*H, N*Hp, E*H*Hp, R*B*H*Hp, E*Hp, R*S*Hp), kept as _linear_sizes keeps its."""
+    key = bytes(d)
+    got = _plans.get(key)
+    if got is None:
+        hh = d.H * d.Hp
+        got = _keep(_plans, key, (_lib.moonep_plan_workspace_bytes(d), d.N, d.N * d.H, d.N * d.Hp, d.E * hh,
+                                  d.R * d.B * hh, d.E * d.Hp, d.R * d.S * d.Hp))
+    return got
+
+
 def moonep_grouped_gemm_act(d, plan_ws, recv, w_home, w_slot, y, act="none", bias=None, z=None,
                             stream=None):
     """moonep_grouped_gemm with bias float32 [E, Hp] and an activation; z [R, C, Hp] if given."""
-    code, hh = _act(act), d.H * d.Hp
-    cols = d.Hp // 2 if act == "swiglu" else d.Hp
+    code = _act(act)
+    need, _, NH, NP, home, slots, EP, _ = _plan_sizes(d)
     _check(library().moonep_grouped_gemm_act(
-        ctypes.byref(d), _ws(d, plan_ws), code, _ptr(recv, BF16, d.N * d.H, "recv"),
-        _ptr(w_home, BF16, d.E * hh, "w_home"),
-        _ptr(w_slot, BF16, d.R * d.B * hh, "w_slot", allow_none=d.B == 0),
-        _ptr(bias, torch.float32, d.E * d.Hp, "bias", True), _ptr(y, BF16, d.N * cols, "y"),
-        _ptr(z, BF16, d.N * d.Hp, "z", True), _stream(stream)), "moonep_grouped_gemm_act")
+        ctypes.byref(d), _ptr(plan_ws, torch.uint8, need, "plan_ws"), code, _ptr(recv, BF16, NH, "recv"),
+        _ptr(w_home, BF16, home, "w_home"), _ptr(w_slot, BF16, slots, "w_slot", allow_none=slots == 0),
+        _ptr(bias, torch.float32, EP, "bias", True),
+        _ptr(y, BF16, NP // 2 if act == "swiglu" else NP, "y"), _ptr(z, BF16, NP, "z", True),
+        _stream(stream)), "moonep_grouped_gemm_act")
 
 
 _grouped_act: dict = {}  # scratch bytes of dims already asked for, by their fields
@@ -191,32 +207,33 @@ def moonep_grouped_act_backward(d, plan_ws, z, d_y, d_z, act="none", d_bias=None
                                 accumulate=False, stream=None):
     """moonep_act_backward on the plan's rows; d_bias float32 [E, Hp] with scratch (uint8,
     moonep_grouped_act_backward_workspace_bytes)."""
-    code, n = _act(act), d.N * d.Hp
-    need = moonep_grouped_act_backward_workspace_bytes(d) if d_bias is not None else 0
+    code = _act(act)
+    need, _, _, n, _, _, EP, _ = _plan_sizes(d)
+    sums = moonep_grouped_act_backward_workspace_bytes(d) if d_bias is not None else 0
     _check(library().moonep_grouped_act_backward(
-        ctypes.byref(d), _ws(d, plan_ws), code, _ptr(z, BF16, n, "z", code == 0),
-        _ptr(d_y, BF16, n // 2 if act == "swiglu" else n, "d_y"),
-        _ptr(d_z, BF16, n, "d_z", code == 0),
-        _ptr(d_bias, torch.float32, d.E * d.Hp, "d_bias", True), int(bool(accumulate)),
-        _scratch(scratch, need), _stream(stream)), "moonep_grouped_act_backward")
+        ctypes.byref(d), _ptr(plan_ws, torch.uint8, need, "plan_ws"), code,
+        _ptr(z, BF16, n, "z", code == 0), _ptr(d_y, BF16, n // 2 if act == "swiglu" else n, "d_y"),
+        _ptr(d_z, BF16, n, "d_z", code == 0), _ptr(d_bias, torch.float32, EP, "d_bias", True),
+        int(bool(accumulate)), _scratch(scratch, sums), _stream(stream)), "moonep_grouped_act_backward")
 
 
 def moonep_combine_dropout(d, plan_ws, y, gates, out, residual=None, p=0.0, rng=None, stream=None):
     """moonep_combine with dropout of probability p (rng: int64 CUDA tensor {seed, offset}), added to
     the residual."""
-    n = d.R * d.S * d.Hp
+    need, N, _, NP, _, _, _, n = _plan_sizes(d)
     _check(library().moonep_combine_dropout(
-        ctypes.byref(d), _ws(d, plan_ws), _ptr(y, BF16, d.N * d.Hp, "y"),
-        _ptr(gates, torch.float32, d.N, "gates"), _ptr(residual, BF16, n, "residual", True),
-        _ptr(out, BF16, n, "out"), float(p), _ptr(rng, torch.int64, 2, "rng", True),
-        _stream(stream)), "moonep_combine_dropout")
+        ctypes.byref(d), _ptr(plan_ws, torch.uint8, need, "plan_ws"), _ptr(y, BF16, NP, "y"),
+        _ptr(gates, torch.float32, N, "gates"), _ptr(residual, BF16, n, "residual", True),
+        _ptr(out, BF16, n, "out"), p, _ptr(rng, torch.int64, 2, "rng", True), _stream(stream)),
+        "moonep_combine_dropout")
 
 
 def moonep_combine_dropout_backward(d, plan_ws, y, gates, d_out, d_y, d_gates, p=0.0, rng=None,
                                     stream=None):
     """The gradient, with the p and rng of the forward pass."""
+    need, N, _, NP, _, _, _, n = _plan_sizes(d)
     _check(library().moonep_combine_dropout_backward(
-        ctypes.byref(d), _ws(d, plan_ws), _ptr(y, BF16, d.N * d.Hp, "y"),
-        _ptr(gates, torch.float32, d.N, "gates"), _ptr(d_out, BF16, d.R * d.S * d.Hp, "d_out"),
-        _ptr(d_y, BF16, d.N * d.Hp, "d_y"), _ptr(d_gates, torch.float32, d.N, "d_gates"), float(p),
-        _ptr(rng, torch.int64, 2, "rng", True), _stream(stream)), "moonep_combine_dropout_backward")
+        ctypes.byref(d), _ptr(plan_ws, torch.uint8, need, "plan_ws"), _ptr(y, BF16, NP, "y"),
+        _ptr(gates, torch.float32, N, "gates"), _ptr(d_out, BF16, n, "d_out"), _ptr(d_y, BF16, NP, "d_y"),
+        _ptr(d_gates, torch.float32, N, "d_gates"), p, _ptr(rng, torch.int64, 2, "rng", True),
+        _stream(stream)), "moonep_combine_dropout_backward")

@@ -64,6 +64,7 @@ struct ProductArgs {
   const uint16_t* residual;  // [M][out columns] or null
   uint16_t *out, *z;         // for rows stored one by one; z null if not asked for
   int has_z;
+  int all;  // grouped, one CTA: takes the plan's tiles whatever height it chose
   int32_t* status;
 };
 
@@ -248,7 +249,7 @@ k_product(const __grid_constant__ ProductMaps tm, const __grid_constant__ Produc
   const int work = PAIR ? blockIdx.x >> 1 : blockIdx.x;  // this one
   if (!DENSE) {
     grid_wait();
-    if (p.counters[MOONEP_CNT_TILE_ROWS] != Cfg::kTileM) return;
+    if (p.counters[MOONEP_CNT_TILE_ROWS] != Cfg::kTileM && (PAIR || !a.all)) return;
   }
   const int step = a.half ? a.bn / 2 : a.bn;  // output columns of a tile
   const int NT = ((a.half ? a.half : a.N) + step - 1) / step;
@@ -805,15 +806,19 @@ cudaError_t launch_grouped_gemm_act(const Dims& d, const PlanPtrs& p, int act, c
   a.z = (uint16_t*)z;
   a.has_z = z != nullptr;
   a.status = p.status;
-  // with the height left to the plan both are launched; the one it did not choose returns at once
+  // With the height left to the plan both are launched; the one it did not choose returns at once.  Where
+  // no rank has more than 128 rows, no tile has, and one CTA takes them all.
+  const bool pair = d.tile_m != kMmaM && d.C > kMmaM;
+  const bool solo = d.tile_m != 2 * kMmaM || !pair;
+  a.all = !pair;
   a.bn = pick_bn_grouped(d.Hp, half);
   const int64_t tiles = (int64_t)d.max_mtiles * tiles_of(1, a, 256);
-  if (d.tile_m != 2 * kMmaM) {
+  if (solo) {
     const cudaError_t e = launch_one<false, kForward, false, false>(tm, a, p, tiles, st);
     if (e != cudaSuccess) return e;
     *launches += 1;
   }
-  if (d.tile_m != kMmaM) {
+  if (pair) {
     const cudaError_t e = launch_one<true, kForward, false, false>(tm, a, p, tiles, st);
     if (e != cudaSuccess) return e;
     *launches += 1;
