@@ -781,8 +781,13 @@ cudaError_t launch_linear_dw(const LinearDims& d, const void* x, const void* d_z
 cudaError_t launch_grouped_gemm_act(const Dims& d, const PlanPtrs& p, int act, const void* recv,
                                     const void* w_home, const void* w_slot, const float* bias, void* y,
                                     void* z, cudaStream_t st, int* launches) {
-  ProductMaps tm;
   const int half = act == kActSwiglu ? d.Hp / 2 : 0;
+  const SplitPlan split = plan_split_grouped(d, half);
+  if (split.splits) {
+    *launches += 1;
+    return launch_split_grouped(d, p, split, act, half, recv, w_home, w_slot, bias, y, z, st);
+  }
+  ProductMaps tm;
   const int ocols = half ? half : d.Hp;
   const bool slots = w_slot != nullptr && d.B > 0;
   if (!encode_matrix(&tm.a, recv, d.H, d.N, d.H, 128) ||

@@ -75,4 +75,9 @@ cudaError_t launch_split(Kind kind, const LinearDims& d, SplitPlan plan, const v
                          const float* bias, const void* residual, void* out, void* z, int add,
                          int32_t* status, cudaStream_t st);
 
+SplitPlan plan_split_grouped(const Dims& d, int half);
+cudaError_t launch_split_grouped(const Dims& d, const PlanPtrs& p, SplitPlan plan, int act, int half,
+                                 const void* recv, const void* w_home, const void* w_slot,
+                                 const float* bias, void* y, void* z, cudaStream_t st);
+
 }  // namespace moonep

@@ -7,12 +7,14 @@
 // TMA-fed stages into TMEM, then sends its partial sums of a token to the CTA that owns the token
 // (stores to the shared memory of the cluster, into the stages that are done), which adds them in
 // rank order in fp32, applies bias, activation and residual and stores the rows.  No scratch memory,
-// no atomics, one launch.
+// no atomics, one launch.  The plan's tiles run the same way where they are few (1 token x 2 of 14 experts,
+// 4864 x 1664 of swiglu: 33 us with tiles of one CTA, 9.7 so).
 // What bounds it: at few rows reading w once (all of it is in flight over the multiprocessors'
 // rings at any time), towards 256 rows a tile the rate at which L2 feeds the rings.  Measured: 1 x 7168
 // x 4096 of swiglu 13.1 us (58.7 MB: 8.8 us at the copy's rate), 256 rows 18.9, 1024 x 7168 x 2048 27
 // (pair tiles: 37), 100 x 512 x 4096 4.9; and between the smallest kernels of a chain 2.9 us.
 #include <algorithm>
+#include <cmath>
 
 #include "product.cuh"
 
@@ -49,10 +51,13 @@ __device__ __forceinline__ float4 add_parts(const float4* at, int stride, int sp
   return v;
 }
 
-template <int KIND>
+// GROUPED: a tile is one of the plan's work tiles (all of them within `tokens` rows) instead of rows of x;
+// the grid has room for as many as there can be, and clusters without one end at once.
+template <int KIND, bool GROUPED>
 __global__ void __launch_bounds__(kSplitThreads, 1)
-k_product_split(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
-                const __grid_constant__ SplitArgs a) {
+k_product_split(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_slots,
+                const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ SplitArgs a,
+                const __grid_constant__ PlanPtrs p) {
   constexpr bool AMN = KIND != kInputGrad;  // w runs along its columns, w^T along the depth
   constexpr bool BMN = KIND == kWeightGrad;  // x runs along the depth, x^T does not
   extern __shared__ uint8_t smem_raw[];
@@ -71,7 +76,19 @@ k_product_split(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
   const int ncols = a.half ? a.half : a.columns;
   const int CT = (ncols + step - 1) / step;
   const int tile = (int)blockIdx.x / S;
-  const int c0 = (tile % CT) * step, t0 = (tile / CT) * a.tokens;
+  const int c0 = (tile % CT) * step;
+  int t0 = (tile / CT) * a.tokens, rows = min(a.tokens, a.T - t0), wrow = 0, expert = 0;
+  const CUtensorMap* wmap = &tm_w;
+  if (GROUPED) {
+    grid_wait();
+    if (tile / CT >= p.counters[MOONEP_CNT_MTILES]) return;  // (the same for a whole cluster)
+    const MTile mt = p.mtiles[tile / CT];
+    t0 = mt.row0;
+    rows = max(1, min(mt.rows, a.tokens));  // (a failed plan may hold anything; nothing is stored then)
+    if (mt.wsel < 0) wmap = &tm_slots;
+    expert = mt.wsel;
+    wrow = (mt.wsel >= 0 ? mt.wsel : -1 - mt.wsel) * a.depth;
+  }
   const int KB = (a.depth + kDepth - 1) / kDepth;
   const int kb0 = (int)((int64_t)KB * rank / S), kb1 = (int)((int64_t)KB * (rank + 1) / S);
   const int panels = (a.tokens + 63) / 64;  // of x^T
@@ -99,7 +116,7 @@ k_product_split(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  grid_wait();  // (what is above runs while the kernel before this one ends)
+  if (!GROUPED) grid_wait();  // (what is above runs while the kernel before this one ends)
 
   if (warp == 0) {
     if (elect_one()) {
@@ -113,8 +130,8 @@ k_product_split(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
         const uint32_t sa = smem_u32(smem) + stage * stage_bytes;
         const int k0 = kb * kDepth;
         if (AMN) {
-          tma_load_2d(sa, &tm_w, full(stage), c0, k0);
-          tma_load_2d(sa + kPanelBytes, &tm_w, full(stage), a.half ? a.half + c0 : c0 + 64, k0);
+          tma_load_2d(sa, wmap, full(stage), c0, wrow + k0);
+          tma_load_2d(sa + kPanelBytes, wmap, full(stage), a.half ? a.half + c0 : c0 + 64, wrow + k0);
         } else {
           tma_load_2d(sa, &tm_w, full(stage), k0, c0);
         }
@@ -177,7 +194,7 @@ k_product_split(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
   tc_fence_after();
   if (S > 1) pair_sync();
 
-  const int valid = min(a.tokens, a.T - t0);   // rows of this tile
+  const int valid = rows;                      // of this tile
   const int fours = (valid + 3) / 4;           // in groups of four
   const int per = (fours + S - 1) / S;         // groups that a CTA owns
   const uint32_t red = smem_u32(smem);         // [splits][per][128 columns][4 tokens] partial sums
@@ -229,8 +246,10 @@ k_product_split(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
       const bool biased = KIND == kForward && a.bias != nullptr;
       float2 bias = make_float2(0.f, 0.f), bias_up = bias;
       if (biased) {
-        bias = __ldg(reinterpret_cast<const float2*>(a.bias + x));
-        if (a.half) bias_up = __ldg(reinterpret_cast<const float2*>(a.bias + a.half + x));
+        const float* from = a.bias + x;
+        if (GROUPED) from += (size_t)(expert >= 0 ? expert : p.slot_expert[-1 - expert]) * a.columns;
+        bias = __ldg(reinterpret_cast<const float2*>(from));
+        if (a.half) bias_up = __ldg(reinterpret_cast<const float2*>(from + a.half));
       }
       auto get = [&](float (&to)[2][4], int at, float2 b) {
         const float4 p = add_parts(sums + at, stride, S), q = add_parts(sums + at + 1, stride, S);
@@ -314,13 +333,13 @@ static int span_of(int tokens) {  // columns of TMEM that one accumulator takes
   return tokens <= 32 ? 32 : (tokens <= 64 ? 64 : (tokens <= 128 ? 128 : 256));
 }
 
-template <int KIND>
+template <int KIND, bool GROUPED>
 static cudaError_t opt_in() {
   static PerDevice kept;
   int set = 0;
   return kept(&set, [&](int* done) {
     *done = 1;
-    return cudaFuncSetAttribute(k_product_split<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(k_product_split<KIND, GROUPED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 kSplitSmem);
   });
 }
@@ -333,7 +352,7 @@ static int at_once(int splits) {
   int n = 0;
   const cudaError_t e = kept[which](&n, [&](int* found) {
     if (splits == 1) return *found = sm_count_gemm(), cudaSuccess;
-    const cudaError_t e = opt_in<kForward>();
+    const cudaError_t e = opt_in<kForward, false>();
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute cluster;
     cluster.id = cudaLaunchAttributeClusterDimension;
@@ -346,7 +365,7 @@ static int at_once(int splits) {
     cfg.attrs = &cluster;
     cfg.numAttrs = 1;
     int clusters = 0;
-    const cudaError_t e2 = cudaOccupancyMaxActiveClusters(&clusters, (void*)k_product_split<kForward>, &cfg);
+    const cudaError_t e2 = cudaOccupancyMaxActiveClusters(&clusters, (void*)k_product_split<kForward, false>, &cfg);
     *found = std::max(1, clusters) * splits;
     return e2;
   });
@@ -389,13 +408,41 @@ SplitPlan plan_split(int T, int columns, int half, int depth, bool f32) {
   return best;
 }
 
-template <int KIND>
-static cudaError_t launch_kind(const CUtensorMap& w, const CUtensorMap& x, const SplitArgs& a,
-                               int64_t ctas, cudaStream_t st) {
-  const cudaError_t e = opt_in<KIND>();
+// The same for the plan's tiles, where no rank has more than 128 rows: the tiles that so many copies of
+// evenly chosen experts make, against the product on tiles of one CTA (0.37 us for a block of 64 by 256
+// columns).  The second is the better one as soon as its tiles fill the GPU, and where reading the
+// weights takes longer than either.
+SplitPlan plan_split_grouped(const Dims& d, int half) {
+  SplitPlan best{0, 0};
+  if (d.C > kMmaM) return best;
+  const int KB = d.H / kDepth;
+  const double met = d.E * (1 - std::pow(1 - 1.0 / d.E, (double)d.N));
+  const int64_t tiles = (int64_t)std::ceil(met);
+  const int64_t CT = half ? (half + 63) / 64 : (d.Hp + 127) / 128;
+  const int64_t wide = half ? (half + 127) / 128 : (d.Hp + 255) / 256;
+  const int64_t sms = std::max(1, at_once(1));
+  const int tokens = (std::min(d.C, 128) + 15) / 16 * 16;
+  const double read = met * d.H * d.Hp * 2 / 6.5e6;  // us
+  double cost = 0.9 * std::max(read, (double)((tiles * wide + sms - 1) / sms) * (0.37 * KB + 1.0) + 4.0);
+  for (int S = 1; S <= 8 && (S == 1 || KB >= 2 * S); S *= 2) {
+    const int room = at_once(S);
+    if (room == 0) continue;
+    const double c = std::max(read, (double)((tiles * CT * S + room - 1) / room) *
+                         ((KB + S - 1) / S * std::max(0.1585, 0.073 + 0.001 * tokens) + 3.02 +
+                          0.0207 * tokens + (S > 1 ? 0.914 + 0.0047 * tokens : 0.0)) +
+                     1.0);
+    if (c < cost) cost = c, best = {tokens, S};
+  }
+  return best;
+}
+
+template <int KIND, bool GROUPED>
+static cudaError_t launch_kind(const CUtensorMap& w, const CUtensorMap& slots, const CUtensorMap& x,
+                               const SplitArgs& a, const PlanPtrs& p, int64_t ctas, cudaStream_t st) {
+  const cudaError_t e = opt_in<KIND, GROUPED>();
   if (e != cudaSuccess) return e;
-  return launch_after(k_product_split<KIND>, (unsigned)ctas, kSplitThreads, kSplitSmem, st, a.splits, w,
-                      x, a);
+  return launch_after(k_product_split<KIND, GROUPED>, (unsigned)ctas, kSplitThreads, kSplitSmem, st,
+                      a.splits, w, slots, x, a, p);
 }
 
 // x and w: the operands as the kernel has them (see there), `out` [T][C]
@@ -435,9 +482,39 @@ cudaError_t launch_split(Kind kind, const LinearDims& d, SplitPlan plan, const v
     const int blocks = ((a.depth + kDepth - 1) / kDepth + plan.splits - 1) / plan.splits;
     while (a.parts * kPartBlocks < blocks && a.parts * span_of(plan.tokens) < 512) a.parts *= 2;
   }
-  if (kind == kForward) return launch_kind<kForward>(tw, tx, a, ctas, st);
-  if (kind == kInputGrad) return launch_kind<kInputGrad>(tw, tx, a, ctas, st);
-  return launch_kind<kWeightGrad>(tw, tx, a, ctas, st);
+  const PlanPtrs none{};
+  if (kind == kForward) return launch_kind<kForward, false>(tw, tw, tx, a, none, ctas, st);
+  if (kind == kInputGrad) return launch_kind<kInputGrad, false>(tw, tw, tx, a, none, ctas, st);
+  return launch_kind<kWeightGrad, false>(tw, tw, tx, a, none, ctas, st);
+}
+
+cudaError_t launch_split_grouped(const Dims& d, const PlanPtrs& p, SplitPlan plan, int act, int half,
+                                 const void* recv, const void* w_home, const void* w_slot,
+                                 const float* bias, void* y, void* z, cudaStream_t st) {
+  SplitArgs a = {};
+  a.T = d.N, a.columns = d.Hp, a.depth = d.H;
+  a.half = half, a.act = act;
+  a.tokens = plan.tokens;
+  a.splits = plan.splits;
+  a.stages = std::min(kSplitStages, kSplitRing / (2 * kPanelBytes + plan.tokens * 128));
+  a.parts = 1;
+  a.bias = bias;
+  a.out = y;
+  a.z = (uint16_t*)z;
+  a.status = p.status;
+  CUtensorMap tw, ts, tx;
+  if (!encode_matrix(&tw, w_home, d.Hp, (int64_t)d.E * d.H, d.Hp, 64) ||
+      !encode_matrix(&tx, recv, d.H, d.N, d.H, plan.tokens))
+    return cudaErrorInvalidValue;
+  ts = tw;
+  if (w_slot != nullptr && d.B > 0 &&
+      !encode_matrix(&ts, w_slot, d.Hp, (int64_t)d.R * d.B * d.H, d.Hp, 64))
+    return cudaErrorInvalidValue;
+  const int64_t CT = half ? (half + 63) / 64 : (d.Hp + 127) / 128;
+  // work tiles: at most one a copy, and one a group
+  const int64_t ctas = std::min<int64_t>(d.max_mtiles, std::min<int64_t>(d.N, d.max_groups)) * CT * plan.splits;
+  if (ctas >= int64_t(1) << 31) return cudaErrorInvalidConfiguration;
+  return launch_kind<kForward, true>(tw, ts, tx, a, p, ctas, st);
 }
 
 }  // namespace moonep

@@ -267,7 +267,15 @@ PLANS = [dict(R=1, E=8, B=0, K=2, S=64, H=64, Hp=128, mode=1), dict(R=2, E=8, B=
          dict(R=2, E=4, B=2, K=4, S=700, H=64, Hp=1024)]
 
 
-@pytest.mark.parametrize("sizes", PLANS, ids=lambda s: "-".join(str(v) for v in s.values()))
+# few rows a rank: the depth is split over clusters where that makes few tiles
+FEW = [dict(R=1, E=14, B=0, K=2, S=1, H=2432, Hp=416 * 2, mode=1), dict(R=1, E=16, B=0, K=7, S=1, H=256, Hp=384, mode=1),
+       dict(R=2, E=8, B=4, K=3, S=5, H=1024, Hp=1152), dict(R=4, E=16, B=4, K=2, S=17, H=512, Hp=640),
+       dict(R=1, E=5, B=0, K=3, S=16, H=1024, Hp=3200, mode=1), dict(R=1, E=4, B=0, K=1, S=128, H=192, Hp=128, mode=1),
+       dict(R=2, E=4, B=2, K=4, S=32, H=4096, Hp=256), dict(R=1, E=2, B=0, K=2, S=40, H=7168, Hp=128, mode=1),
+       dict(R=8, E=64, B=8, K=8, S=1, H=4096, Hp=1024)]
+
+
+@pytest.mark.parametrize("sizes", PLANS + FEW, ids=lambda s: "-".join(str(v) for v in s.values()))
 @pytest.mark.parametrize("rows", [128, 256, 0])
 @pytest.mark.parametrize("act,bias,z", [("swiglu", True, True), ("none", False, False), ("gelu", True, True),
                                         ("silu", False, True), ("swiglu", False, False), ("relu", True, False)])
@@ -293,7 +301,9 @@ def test_grouped_gemm_act(sizes, rows, act, bias, z):
     if z:
         assert_within(zz.t, want_z, err + BF16_STEP * (np.abs(want_z) + err), "z")
         zz.check()
-    if act == "none" and not bias:  # bit for bit the call that it stands beside
+    if act == "none" and not bias and d.C > 128:
+        # bit for bit the call that it stands beside (with fewer rows a rank the depth may be split, and
+        # sums in another order are as good as the bound above says)
         plain = torch.empty_like(y.t)
         mx.moonep_grouped_gemm(d, p.ws.buf, recv.cuda(), home, slot, plain)
         assert torch.equal(plain, y.t)
