@@ -377,7 +377,7 @@ static int at_once(int splits) {
 // with up to 15 choices; on the average off by 11 %, and the choice 1 % from the best one):
 // a block of 64 of the depth costs an instruction's least time or grows with its tokens, 0.16 to 0.33;
 // a round of CTAs begins and ends in 3 + 0.02 a token, a cluster's exchange adds 0.9 + 0.005 a token.
-// The pair kernel takes 0.27 for a block of a tile and 8.2 for its first round.
+// The pair kernel takes 0.27 for a block of a tile, 2 more for a round of tiles and 4.25 once.
 SplitPlan plan_split(int T, int columns, int half, int depth, bool f32) {
   const int64_t CT = half ? (half + 63) / 64 : (columns + 127) / 128;
   const int KB = (depth + kDepth - 1) / kDepth;
@@ -409,9 +409,12 @@ SplitPlan plan_split(int T, int columns, int half, int depth, bool f32) {
 }
 
 // The same for the plan's tiles, where no rank has more than 128 rows: the tiles that so many copies of
-// evenly chosen experts make, against the product on tiles of one CTA (0.37 us for a block of 64 by 256
-// columns).  The second is the better one as soon as its tiles fill the GPU, and where reading the
-// weights takes longer than either.
+// evenly chosen experts make, against the product on tiles of one CTA (0.5 us for a block of 64 by 256
+// columns that memory has to bring).  Where reading the weights takes longer than either, the wide tiles
+// read them faster as soon as they fill the GPU twice, by 2 to 12 % (16 tokens x 8 of 64 experts, 4096 x
+// 2048: 123 us against 138), and slower below that, by 3 to 38 % (1 x 8 of 64, 7168 x 4096: 96 against 72;
+// 4 x 8 of 64, 4096 x 2048: 73 against 64), but for many tokens, whose rows the narrow tiles load twice as
+// often (128 x 1 of 16, 4096 x 4096: 84 against 95).
 SplitPlan plan_split_grouped(const Dims& d, int half) {
   SplitPlan best{0, 0};
   if (d.C > kMmaM) return best;
@@ -423,11 +426,12 @@ SplitPlan plan_split_grouped(const Dims& d, int half) {
   const int64_t sms = std::max(1, at_once(1));
   const int tokens = (std::min(d.C, 128) + 15) / 16 * 16;
   const double read = met * d.H * d.Hp * 2 / 6.5e6;  // us
-  double cost = 0.9 * std::max(read, (double)((tiles * wide + sms - 1) / sms) * (0.37 * KB + 1.0) + 4.0);
+  double cost = (tiles * wide >= 2 * sms ? 0.9 : 1.05) *
+                std::max(read, (double)((tiles * wide + sms - 1) / sms) * (0.5 * KB + 1.0) + 4.0);
   for (int S = 1; S <= 8 && (S == 1 || KB >= 2 * S); S *= 2) {
     const int room = at_once(S);
     if (room == 0) continue;
-    const double c = std::max(read, (double)((tiles * CT * S + room - 1) / room) *
+    const double c = std::max(read * (1 + tokens / 1280.0), (double)((tiles * CT * S + room - 1) / room) *
                          ((KB + S - 1) / S * std::max(0.1585, 0.073 + 0.001 * tokens) + 3.02 +
                           0.0207 * tokens + (S > 1 ? 0.914 + 0.0047 * tokens : 0.0)) +
                      1.0);
