@@ -102,7 +102,8 @@ int moonep_grouped_act_backward_workspace_bytes(const moonep_dims* dims, size_t*
 /* moonep_act_backward on rows as moonep_grouped_gemm_act makes them: z, d_z bf16
  * [R][C][Hp], d_y bf16 [R][C][Hp, or Hp / 2]; d_bias fp32 [E][Hp] or NULL: every
  * expert's sum over all its rows, home or slot (0 for an expert without rows).  d_z
- * then goes to moonep_grouped_gemm_dx and _dw.  Hp below 2^26 (MOONEP_ERR_SHAPE). */
+ * then goes to moonep_grouped_gemm_dx and _dw.  Hp up to 65535 x 1024
+ * (MOONEP_ERR_SHAPE). */
 int moonep_grouped_act_backward(const moonep_dims* dims, void* plan_ws, int32_t act,
                                 const uint16_t* z, const uint16_t* d_y, uint16_t* d_z, float* d_bias,
                                 int32_t accumulate, void* scratch, void* stream);

@@ -195,7 +195,7 @@ int moonep_grouped_act_backward(const moonep_dims* dims, void* plan_ws, int32_t 
   MOONEP_CHECK(check_act(act, d.Hp));
   if (accumulate != 0 && accumulate != 1) return MOONEP_ERR_ARG;
   MOONEP_CHECK(check_act_buffers(act, z, d_y, d_z, d_bias, scratch));
-  if (d.Hp >= 1 << 26) return MOONEP_ERR_SHAPE;  // 1024 columns of d_bias a block
+  if (d.Hp > 65535 * 1024) return MOONEP_ERR_SHAPE;  // 1024 columns of d_bias a block, blocks in y
   int n = 0;
   const cudaError_t e = launch_grouped_act_backward(d, P, act, z, d_y, d_z, d_bias, accumulate,
                                                     (float*)scratch, (cudaStream_t)stream, &n);

@@ -1,0 +1,40 @@
+"""What the feed-forward operators' launchers choose by size, on the host, against a CUDA runtime that
+launches nothing (fake_runtime_choice.cpp)."""
+import os
+import shutil
+import subprocess
+
+import pytest
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+
+
+@pytest.fixture(scope="module")
+def fake(tmp_path_factory):
+    from perfectly_balanced_token_gb300 import build as b
+    cxx = shutil.which("g++")
+    if cxx is None:
+        pytest.skip("no C++ compiler")
+    b.build()
+    headers = os.path.join(os.path.dirname(os.path.dirname(b._nvcc())), "include")
+    exe = str(tmp_path_factory.mktemp("fake") / "fake")
+    objects = [os.path.join(b.OUT_DIR, s.replace(".cu", ".o")) for s in b.SOURCES]
+    r = subprocess.run([cxx, "-std=c++17", "-O1", "-I", headers, "-o", exe,
+                        os.path.join(HERE, "fake_runtime_choice.cpp"), *objects, "-lpthread"],
+                       capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+
+    def run(device, *args):
+        r = subprocess.run([exe, str(device), *map(str, args)], capture_output=True, text=True, timeout=60)
+        assert r.returncode == 0, r.stdout + r.stderr
+        return r.stdout.splitlines()
+    return run
+
+
+def test_widest_bias_sums_of_experts(fake):
+    # 65535 blocks of 1024 columns are launched, more are refused before anything is
+    lines = fake(0, "act_bias", 2, 65535 * 1024)
+    assert len(lines) == 3 and lines[1].split()[1:3] == ["2", "65535"], lines
+    assert lines[2] == "returned 0 refused 0", lines
+    for Hp in (65535 * 1024 + 64, (1 << 26) - 64, 1 << 26):
+        assert fake(0, "act_bias", 2, Hp) == ["returned 4 refused 0"], Hp
