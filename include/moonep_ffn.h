@@ -125,8 +125,9 @@ int moonep_combine_dropout(const moonep_dims* dims, void* plan_ws, const uint16_
                            const int64_t* rng, void* stream);
 
 /* moonep_combine_backward behind it: with d = m d_out, d_y[dst[r][s][k]] =
- * bf16(gates[r][s][k] d[r][s]) and d_gates[r][s][k] = <y[dst[r][s][k]], d[r][s]>.  (The
- * residual's gradient is d_out itself.)  K <= 128, Hp <= 8192 (MOONEP_ERR_SHAPE). */
+ * bf16(gates[r][s][k] d[r][s]) and d_gates[r][s][k] = <y[dst[r][s][k]], d[r][s]>, where
+ * a dropped element counts as 0 whatever y, the gate and d_out are.  (The residual's
+ * gradient is d_out itself.)  K <= 128, Hp <= 8192 (MOONEP_ERR_SHAPE). */
 int moonep_combine_dropout_backward(const moonep_dims* dims, void* plan_ws, const uint16_t* y,
                                     const float* gates, const uint16_t* d_out, uint16_t* d_y,
                                     float* d_gates, double p, const int64_t* rng, void* stream);

@@ -97,7 +97,10 @@ def combine_dropout(y, dst, gates, residual, factor):
 
 
 def combine_dropout_backward(y, dst, gates, d_out, factor):
-    d = np.where(factor != 0, d_out * factor, 0.0)
-    d_y = np.zeros_like(y)
-    d_y[dst] = gates[..., None] * d[:, None]
-    return d_y, (y[dst] * d[:, None]).sum(-1)
+    """What was dropped counts as 0 whatever y, the gate and d_out are."""
+    kept = (factor != 0)[:, None]
+    with np.errstate(invalid="ignore"):
+        d = (d_out * factor)[:, None]
+        d_y = np.zeros_like(y)
+        d_y[dst] = np.where(kept, gates[..., None] * d, 0.0)
+        return d_y, np.where(kept, y[dst] * d, 0.0).sum(-1)

@@ -111,6 +111,33 @@ k_combine_dropout(Dims d, PlanPtrs p, const uint4* __restrict__ y, const float* 
 // come KC at a time, the first of them on their way while the random numbers are drawn.
 constexpr int kDropMaxK = 128;
 
+// A thread's part of a copy's dot product and of its d_y, where an element that was dropped counts as 0
+// whatever y and the gate are.
+template <int TEAM>
+__device__ __forceinline__ float drop_alone(const uint4* y, const uint4* dout, uint4* dy, float g, int hv,
+                                            uint64_t group0, const Dropout& drop) {
+  float dot = 0.f;
+#pragma unroll 1
+  for (int a = threadIdx.x % TEAM; a < hv; a += TEAM) {
+    float f[8], o[8], w[8], kept[8];
+    unpack8(f, __ldcs(y + a));
+    unpack8(o, __ldcs(dout + a));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) kept[j] = 1.f;
+    uint32_t random[4];
+    Philox(drop.rng).numbers(group0 + a, random);
+    Philox::apply(random, drop.cut, 1.f, kept);
+    Philox::apply(random, drop.cut, drop.scale, o);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      dot = fmaf(kept[j] != 0.f ? f[j] : 0.f, o[j], dot);
+      w[j] = kept[j] != 0.f ? g * o[j] : 0.f;
+    }
+    __stcs(dy + a, pack8(w));
+  }
+  return dot;
+}
+
 template <int TEAM, int VPT, int KC, bool DROP>
 __global__ void __launch_bounds__(kRowThreads)
 k_combine_dropout_bwd(Dims d, PlanPtrs p, const uint4* __restrict__ y,
@@ -164,6 +191,7 @@ k_combine_dropout_bwd(Dims d, PlanPtrs p, const uint4* __restrict__ y,
         Philox::apply(random, drop.cut, drop.scale, o[i]);
       }
     }
+    float probe = 0.f;  // 0, or a NaN: a gate or a dot product is not finite (alike in all lanes of a warp)
     for (int k0 = 0; k0 < d.K; k0 += KC) {
       if (k0 > 0) load(k0);
       float dot[KC];
@@ -191,10 +219,27 @@ k_combine_dropout_bwd(Dims d, PlanPtrs p, const uint4* __restrict__ y,
       for (int off = 16; off > 0; off >>= 1)
 #pragma unroll
         for (int k = 0; k < KC; ++k) dot[k] += __shfl_xor_sync(0xffffffffu, dot[k], off);
+      if (DROP) {
+#pragma unroll
+        for (int k = 0; k < KC; ++k) probe = fmaf(g[k], 0.f, fmaf(dot[k], 0.f, probe));
+      }
       if (lane == 0) {
 #pragma unroll
         for (int k = 0; k < KC; ++k)
           if (k0 + k < d.K) (TEAM == 32 ? dgates[(size_t)t * d.K + k0 + k] : part[warp][k0 + k]) = dot[k];
+      }
+    }
+    if (DROP && probe != 0.f) {
+      // 0 times what is not finite is a NaN, where the element was dropped as well: the token once more,
+      // element by element (finite ones pay two instructions a copy for it)
+#pragma unroll 1
+      for (int k = 0; k < d.K; ++k) {
+        const size_t at = (size_t)__ldg(dt + k) * hv;
+        float sum = drop_alone<TEAM>(y + at, dout + (size_t)t * hv, dy + at, __ldg(gt + k), hv, (uint64_t)t * hv,
+                                     drop);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        if (lane == 0) (TEAM == 32 ? dgates[(size_t)t * d.K + k] : part[warp][k]) = sum;
       }
     }
     if (TEAM == 32) continue;
