@@ -74,12 +74,19 @@ def _act(act):
     return code
 
 
+def _int32(value, name):
+    """A size for an int32 argument, whose higher bits ctypes would drop without a word."""
+    if not -(1 << 31) <= value < 1 << 31:
+        raise ValueError(f"{name} is {value}, past 32 bits")
+    return value
+
+
 def linear_dims(T, K, N, act="none", out_dtype=torch.bfloat16) -> moonep_linear_dims:
     """x [T, K] times w [K, N]; act: "none", "relu", "gelu", "silu" or "swiglu" (whose output has
     N / 2 columns); out_dtype: that of moonep_linear's out, bfloat16 or float32."""
     if out_dtype not in OUT_DTYPES:
         raise ValueError(f"out_dtype must be bfloat16 or float32, got {out_dtype}")
-    return moonep_linear_dims(T, K, N, _act(act), OUT_DTYPES[out_dtype])
+    return moonep_linear_dims(_int32(T, "T"), _int32(K, "K"), _int32(N, "N"), _act(act), OUT_DTYPES[out_dtype])
 
 
 _linear: dict = {}  # of linear dims already seen, by their fields
@@ -131,7 +138,7 @@ def moonep_act_backward_workspace_bytes(rows: int, cols: int) -> int:
     size = _act_scratch.get((rows, cols))
     if size is None:
         n = ctypes.c_size_t(0)
-        _check(library().moonep_act_backward_workspace_bytes(rows, cols, ctypes.byref(n)),
+        _check(library().moonep_act_backward_workspace_bytes(rows, _int32(cols, "cols"), ctypes.byref(n)),
                "moonep_act_backward_workspace_bytes")
         size = _keep(_act_scratch, (rows, cols), n.value)
     return size
@@ -156,7 +163,7 @@ def moonep_act_backward(z, d_out, d_z, act="none", d_bias=None, scratch=None, ac
     n = rows * cols
     need = moonep_act_backward_workspace_bytes(rows, cols) if d_bias is not None else 0
     _check(library().moonep_act_backward(
-        rows, cols, code, _ptr(z, BF16, n, "z", code == 0), _ptr(d_out, BF16, None, "d_out"),
+        rows, _int32(cols, "cols"), code, _ptr(z, BF16, n, "z", code == 0), _ptr(d_out, BF16, None, "d_out"),
         _ptr(d_z, BF16, n, "d_z", code == 0), _ptr(d_bias, torch.float32, cols, "d_bias", True),
         int(bool(accumulate)), _scratch(scratch, need), _stream(stream)), "moonep_act_backward")
 
