@@ -60,6 +60,7 @@ struct ProductArgs {
   int half;        // swiglu: N / 2, otherwise 0
   int add;         // fp32 C: added into
   int bn;          // columns of a tile: 256, 192 or 128 (swiglu: half of them gates)
+                   // (the eighth word: the host tests read it in a launch's arguments)
   const float* bias;  // [N], grouped [E][N]; or null
   const uint16_t* residual;  // [M][out columns] or null
   uint16_t *out, *z;         // for rows stored one by one; z null if not asked for
@@ -687,10 +688,11 @@ static int pick_bn(int half, bool f32, F&& rounds) {
   return best;
 }
 static int pick_bn_dense(int M, int N, int half, bool f32) {
+  const int64_t pairs = std::max(1, at_once(2) / 2);
   return pick_bn(half, f32, [&](int bn) {
     const int step = half ? bn / 2 : bn;
     const int64_t tiles = (int64_t)((M + 255) / 256) * (((half ? half : N) + step - 1) / step);
-    return (double)((tiles + 75) / 76);
+    return (double)((tiles + pairs - 1) / pairs);
   });
 }
 static int pick_bn_grouped(int N, int half) {

@@ -70,6 +70,9 @@ inline bool encode_out(CUtensorMap* m, const void* base, int cols, int64_t rows,
 struct SplitPlan {
   int tokens, splits;  // rows of a tile, CTAs that share its depth; splits = 0: not for these sizes
 };
+// CTAs, one a multiprocessor, that run at once in clusters of `splits` (1, 2, 4 or 8); 0 if the runtime
+// will not say.
+int at_once(int splits);
 SplitPlan plan_split(int T, int columns, int half, int depth, bool f32);
 cudaError_t launch_split(Kind kind, const LinearDims& d, SplitPlan plan, const void* x, const void* w,
                          const float* bias, const void* residual, void* out, void* z, int add,

@@ -344,9 +344,8 @@ static cudaError_t opt_in() {
   });
 }
 
-// CTAs that run at once in clusters of `splits` (1, 2, 4, 8): the GPU's processing clusters do not
-// all have a multiple of eight multiprocessors.
-static int at_once(int splits) {
+// The GPU's processing clusters do not all have a multiple of eight multiprocessors.
+int at_once(int splits) {
   static PerDevice kept[4];
   const int which = splits == 1 ? 0 : (splits == 2 ? 1 : (splits == 4 ? 2 : 3));
   int n = 0;

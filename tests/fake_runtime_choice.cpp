@@ -2,7 +2,7 @@
 // and 15 on the first device, half of it on the second), for what the launchers choose by size.
 //
 //   fake_runtime_choice DEVICE CALL SIZES...   linear T K N ACT F32, dx T K N, dw T K N:
-//                                              the kernel and its grid
+//                                              the kernel, its grid and the columns of its tiles
 //                                              act_bias E Hp: the gradient with the experts' bias sums
 #include <cuda_runtime.h>
 
@@ -24,14 +24,17 @@ cudaError_t cudaOccupancyMaxActiveClusters(int* n, const void*, const cudaLaunch
   *n = (x == 2 ? 76 : (x == 4 ? 36 : 15)) / (device + 1);
   return cudaSuccess;
 }
-cudaError_t cudaLaunchKernelExC(const cudaLaunchConfig_t* c, const void* f, void**) {
+cudaError_t cudaLaunchKernelExC(const cudaLaunchConfig_t* c, const void* f, void** args) {
   if (c->gridDim.y > 65535 || c->gridDim.z > 65535) {
     ++refused;
     std::printf("refused grid %u %u %u\n", c->gridDim.x, c->gridDim.y, c->gridDim.z);
     return cudaErrorInvalidConfiguration;
   }
   const std::string& name = names[f];
-  std::printf("%s %u %u\n", name.c_str(), c->gridDim.x, c->gridDim.y);
+  int columns = 0;  // (the tiles' columns: an argument of k_product, where product.cu says)
+  if (name.find("k_product_split") == std::string::npos && name.find("k_product") != std::string::npos)
+    columns = static_cast<const int*>(args[1])[7];
+  std::printf("%s %u %u %d\n", name.c_str(), c->gridDim.x, c->gridDim.y, columns);
   return cudaSuccess;
 }
 }

@@ -38,3 +38,18 @@ def test_widest_bias_sums_of_experts(fake):
     assert lines[2] == "returned 0 refused 0", lines
     for Hp in (65535 * 1024 + 64, (1 << 26) - 64, 1 << 26):
         assert fake(0, "act_bias", 2, Hp) == ["returned 4 refused 0"], Hp
+
+
+def first(lines):
+    """Kernel, grid and tile columns of the first launch."""
+    name, x, _, columns = lines[0].split()
+    return name, int(x), int(columns)
+
+
+@pytest.mark.parametrize("sizes,columns", [((5000, 2048, 1024), (192, 256)), ((9984, 2048, 1288), (192, 256)),
+                                           ((8192, 2048, 4096), (256, 256))])
+def test_tile_width_goes_by_the_devices_pairs(fake, sizes, columns):
+    # 76 pairs, and 38: 80 wide tiles are 2 rounds and 3, 120 of 192 columns 2 and 4 (0.88 of the time each)
+    for device in (0, 1):
+        name, _, got = first(fake(device, "linear", *sizes, 0, 0))
+        assert "k_product" in name and got == columns[device], (device, name, got)
