@@ -3,6 +3,7 @@
 //
 //   fake_runtime_choice DEVICE CALL SIZES...   linear T K N ACT F32, dx T K N, dw T K N:
 //                                              the kernel, its grid and the columns of its tiles
+//                                              experts R E B K S H Hp ACT: the same of the plan's product
 //                                              act_bias E Hp: the gradient with the experts' bias sums
 #include <cuda_runtime.h>
 
@@ -43,12 +44,14 @@ int main(int argc, char** argv) {
   if (argc < 4) return 2;
   device = std::atoi(argv[1]);
   const std::string what = argv[2];
-  int v[5] = {};
-  for (int i = 3; i < argc && i < 8; ++i) v[i - 3] = std::atoi(argv[i]);
+  int v[8] = {};
+  for (int i = 3; i < argc && i < 11; ++i) v[i - 3] = std::atoi(argv[i]);
   auto* a = (uint16_t*)at(0x100000);
   auto* f = (float*)at(0x300000);
   auto* s = (int32_t*)at(0x400000);
   moonep_linear_dims d = {v[0], v[1], v[2], 0, 0};
+  moonep_dims m;
+  std::memset(&m, 0, sizeof m);
   int rc = -1;
   if (what == "linear") {
     d.act = v[3], d.out_f32 = v[4];
@@ -57,9 +60,10 @@ int main(int argc, char** argv) {
     rc = moonep_linear_dx(&d, a, a, a, s, nullptr);
   } else if (what == "dw") {
     rc = moonep_linear_dw(&d, a, a, f, 0, s, nullptr);
+  } else if (what == "experts") {
+    m.R = v[0], m.E = v[1], m.B = v[2], m.K = v[3], m.S = v[4], m.H = v[5], m.Hp = v[6], m.mode = m.B == 0;
+    rc = moonep_grouped_gemm_act(&m, at(0x10000000), v[7], a, a, a, f, a, a, nullptr);
   } else if (what == "act_bias") {
-    moonep_dims m;
-    std::memset(&m, 0, sizeof m);
     m.R = 1, m.E = v[0], m.K = 1, m.S = 1, m.H = 64, m.Hp = v[1], m.mode = 1;
     rc = moonep_grouped_act_backward(&m, at(0x10000000), MOONEP_ACT_RELU, a, a, a, f, 0, f, nullptr);
   }

@@ -53,3 +53,19 @@ def test_tile_width_goes_by_the_devices_pairs(fake, sizes, columns):
     for device in (0, 1):
         name, _, got = first(fake(device, "linear", *sizes, 0, 0))
         assert "k_product" in name and got == columns[device], (device, name, got)
+
+
+def test_the_pair_kernels_tests_reach_it(fake):
+    from tests import test_gpu_ffn_pair as t
+    acts = ["none", "relu", "gelu", "silu", "swiglu"]
+    calls = [(("linear", T, K, N, acts.index(act), f32), width)
+             for f32, table in ((0, t.FORWARD), (1, t.FORWARD_F32)) for T, K, N, width, of in table for act in of]
+    calls += [((what, T, K, N), width) for what, table in (("dx", t.INPUT), ("dw", t.WEIGHT))
+              for T, K, N, width in table]
+    calls += [(("experts", *s.values(), act), 128) for s in t.EXPERTS for act in (0, 4)]
+    for call, width in calls:
+        lines = fake(0, *call)
+        launches = [ln.split() for ln in lines[:-1]]
+        assert len(launches) == (2 if call[0] == "experts" else 1) and lines[-1].startswith("returned 0"), (call, lines)
+        for name, _, _, columns in launches:
+            assert "k_product_split" not in name and "k_product" in name and int(columns) == width, (call, name, columns)
