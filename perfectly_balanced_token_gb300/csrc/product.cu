@@ -220,6 +220,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 k_product(const __grid_constant__ ProductMaps tm, const __grid_constant__ ProductArgs a,
           const __grid_constant__ PlanPtrs p) {
   static_assert(DENSE || !F32, "the grouped output is bf16");
+  static_assert(PAIR || KIND == kForward, "one CTA has no loads of w^T or x^T");
+  static_assert(DENSE || KIND == kForward, "the plan's gradients are moonep.h's");
   using Cfg = ProductCfg<PAIR, F32>;
   using Op = Issue<PAIR>;
   const bool deep = Cfg::kCanDeepen && a.has_z;
@@ -415,9 +417,8 @@ k_product(const __grid_constant__ ProductMaps tm, const __grid_constant__ Produc
 #pragma unroll
             for (int j = 0; j < Cfg::kBPanels; ++j)
               if (j < panels) Op::load(sb + j * kPanelBytes, bmap, fb, column(j), wrow + k0);
-          } else {  // 128 rows of w at a time
-            Op::load(sb, bmap, fb, k0, wrow + mine);
-            if (!PAIR) Op::load(sb + 2 * kPanelBytes, bmap, fb, k0, wrow + mine + 128);
+          } else {  // 128 rows of w, of which the tile's width is used
+            Op::load(sb, bmap, fb, k0, mine);
           }
           ++issued;
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
