@@ -1,4 +1,8 @@
 """Calls of the feed-forward operators that their documentation allows and that lie at its edges."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -48,3 +52,100 @@ def test_dropped_values_reach_no_gradient(K, Hp):
     assert odd.any() and np.array_equal(np.isnan(got), np.isnan(want_y))
     assert np.array_equal(got[odd], want_y[odd], equal_nan=True)
     assert_within(got[~odd], want_y[~odd], (2.0 ** -8 + 2.0 ** -22) * np.abs(want_y[~odd]), "d_y")
+
+
+def test_graph_with_branches_copies_and_fills():
+    # captured launches behind a fill, a copy, another stream's kernel, and a join of two branches
+    T, K, N = 2049, 72, 2056  # pair tiles forward and back, and a split weight gradient
+    x, w = syn.normal_bf16((T, K), 1.0, 1).cuda(), syn.normal_bf16((K, N), 0.1, 2).cuda()
+    new, held = x.clone(), torch.empty_like(x)
+    ld, st = mx.linear_dims(T, K, N, act="gelu"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    none = torch.empty(0, K, dtype=BF16, device="cuda"), torch.empty(0, N, dtype=BF16, device="cuda")
+    out, z, d_z = (torch.empty(T, N, dtype=BF16, device="cuda") for _ in range(3))
+    d_x, d_w, zero = torch.empty_like(x), torch.empty(K, N, device="cuda"), torch.ones(K, N, device="cuda")
+    d_b, scratch = torch.empty(N, device="cuda"), torch.empty(mx.moonep_act_backward_workspace_bytes(T, N),
+                                                              dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+
+    def run():
+        held.copy_(new)
+        mx.moonep_linear(ld, held, w, out, st, z=z)
+        mx.moonep_linear_dw(mx.linear_dims(0, K, N), *none, zero, st)  # a fill
+        mx.moonep_act_backward(z, out, d_z, act="gelu", d_bias=d_b, scratch=scratch)
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            mx.moonep_linear_dx(ld, d_z, w, d_x, st)
+        d_w.copy_(zero)
+        mx.moonep_linear_dw(ld, held, d_z, d_w, st, accumulate=True)
+        main.wait_stream(side)
+        mx.moonep_linear(mx.linear_dims(T, K, N), d_x, w, out, st)
+
+    def result():
+        torch.cuda.synchronize()
+        return [t.clone() for t in (out, z, d_z, d_b, d_x, d_w)]
+
+    run()
+    result()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for seed in (1, 5, 6):
+        new.copy_(syn.normal_bf16((T, K), 1.0, seed))
+        for t in (out, z, d_z, d_b, d_x, d_w, held):
+            t.fill_(float("nan"))
+        zero.fill_(1.0)
+        for _ in range(3):
+            graph.replay()
+        got = result()
+        run()
+        for a, b in zip(got, result()):
+            assert torch.equal(a, b)
+    assert int(st) == 0
+
+
+FIRST_CALL = """
+import sys, torch
+import perfectly_balanced_token_gb300 as mx
+T, K, N = 2049, 72, 2056
+bf = dict(dtype=torch.bfloat16, device="cuda")
+x, w, st = torch.randn(T, K, **bf), torch.randn(K, N, **bf), torch.zeros(1, dtype=torch.int32, device="cuda")
+out, few, d_w = torch.zeros(T, N, **bf), torch.zeros(3, N, **bf), torch.zeros(K, N, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    mx.moonep_linear(mx.linear_dims(T, K, N), x, w, out, st)
+    mx.moonep_linear(mx.linear_dims(3, K, N), x[:3], w, few, st)
+    mx.moonep_linear_dw(mx.linear_dims(T, K, N), x, out, d_w, st)
+g.replay()
+torch.cuda.synchronize()
+want = x.double() @ w.double()
+assert bool(((out.double() - want).abs() <= 2.0 ** -8 * want.abs() + 1e-3).all())
+assert bool(((few.double() - want[:3]).abs() <= 2.0 ** -8 * want[:3].abs() + 1e-3).all())
+want = x.double().t() @ out.double()
+assert bool(((d_w.double() - want).abs() <= T * 2.0 ** -23 * (x.double().abs().t() @ out.double().abs())).all())
+assert int(st) == 0
+print("captured")
+"""
+
+
+def test_first_calls_of_a_process_are_captured():
+    # what a launcher sets up once for a device is allowed while a stream is captured.  (z at K = 72 of
+    # normal values is off by 72 2^-23 sum |x w|, below 1e-3.)
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout == "captured\n", r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("T,N,f32", [(4, 64, True), (4, 64, False), (130, 16, True), (300, 2056, True)])
+def test_deep_products(T, N, f32):
+    # fp32 sums of more parts than the split product has columns of TMEM for
+    K = 200008
+    x, w = syn.normal_bf16((T, K), 1.0, 1).cuda(), syn.normal_bf16((K, N), K ** -0.5, 2).cuda()
+    out, st = torch.empty(T, N, dtype=F32 if f32 else BF16, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    mx.moonep_linear(mx.linear_dims(T, K, N, out_dtype=out.dtype), x, w, out, st)
+    want, size = x.double() @ w.double(), x.double().abs() @ w.double().abs()
+    # (parts of 768 and their joining, or the whole depth in one accumulator of a CTA)
+    e = (768 * 2.0 ** -23 + K / 768 * 2.0 ** -24) * size if f32 else K * 2.0 ** -23 * size
+    bound = e if f32 else e + 2.0 ** -8 * (want.abs() + e)
+    assert bool(((out.double() - want).abs() <= bound).all()) and int(st) == 0
