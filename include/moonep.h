@@ -31,6 +31,10 @@
  *  - stream is a cudaStream_t (NULL = legacy default stream).  All work is
  *    enqueued on it; shapes and launch configurations depend only on the dims,
  *    never on routing, so a sequence of calls can be captured in a CUDA graph.
+ *  - The grouped products of one plan, forward and backward, share scratch in its
+ *    workspace: two of them must not run at the same time (on two streams, or in
+ *    two branches of a graph).  Other calls may read the plan meanwhile, and
+ *    different plans have nothing in common.
  *  - Return value: a host-detected status (0 = MOONEP_OK), returned before
  *    anything is enqueued.  Conditions only the device can see (bad routing,
  *    a device wait that ran out) are OR-ed into a status word inside the plan

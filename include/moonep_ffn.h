@@ -21,7 +21,8 @@
  * 16-byte aligned device pointers unless stated, arrays are dense and row-major,
  * nothing allocates or synchronises, host-detected errors come back before anything
  * is enqueued, and calls that take a plan workspace write nothing if the plan
- * failed.  Buffers of one call do not overlap.
+ * failed.  Buffers of one call do not overlap.  moonep_grouped_gemm_act is one of the
+ * grouped products that must not run at the same time on one plan.
  */
 #ifndef MOONEP_FFN_H
 #define MOONEP_FFN_H
@@ -39,7 +40,8 @@ enum moonep_activation {
   MOONEP_ACT_NONE = 0,
   MOONEP_ACT_RELU = 1,
   MOONEP_ACT_GELU = 2,   /* z P(N(0,1) <= z)                                        */
-  MOONEP_ACT_SILU = 3,   /* z / (1 + e^-z)                                          */
+  MOONEP_ACT_SILU = 3,   /* z / (1 + e^-z); 0 below z = -87.33, where it is under
+                            1.1e-36 (swiglu and the gradients likewise)             */
   MOONEP_ACT_SWIGLU = 4  /* silu(z_j) z_(F+j), j < F: the first half of a row's
                             columns are gates, 2F columns of z give F of the output */
 };
@@ -69,7 +71,8 @@ int moonep_linear(const moonep_linear_dims* dims, const uint16_t* x, const uint1
 int moonep_linear_dx(const moonep_linear_dims* dims, const uint16_t* d_z, const uint16_t* w,
                      uint16_t* d_x, int32_t* status, void* stream);
 
-/* d_w fp32 [K][N] = x^T d_z, or with accumulate = 1 d_w += x^T d_z. */
+/* d_w fp32 [K][N] = x^T d_z, or with accumulate = 1 d_w += x^T d_z.  (T = 0 and
+ * accumulate = 0: d_w is zeroed and status neither read nor needed.) */
 int moonep_linear_dw(const moonep_linear_dims* dims, const uint16_t* x, const uint16_t* d_z,
                      float* d_w, int32_t accumulate, int32_t* status, void* stream);
 

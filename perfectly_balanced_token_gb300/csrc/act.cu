@@ -15,8 +15,8 @@ namespace moonep {
 //
 // A block takes a chunk of rows by a strip of 8 to 256 columns: 1 to 32 lanes of a warp, eight columns
 // each, cover the strip, the other lanes and warps further rows.  Dense chunks are cut so that the
-// strips' blocks are all there at once (a chunk of 64 rows a block, with its sums and barriers, took 152 us
-// for 32768 x 4096 of swiglu where a block for each share of the rows took 107); with a plan and sums
+// strips' blocks make two rounds of what the GPU holds at once (a chunk of 64 rows a block, with its sums and
+// barriers, took 152 us for 32768 x 4096 of swiglu where long chunks took 107); with a plan and sums
 // a chunk is a work tile, whose rows are of one expert.  A chunk's sums go to scratch, one row a
 // chunk, and a second kernel adds them in ascending order: the same bits in every run.
 // ---------------------------------------------------------------------------

@@ -19,8 +19,9 @@
 //    ends inside a tile are stored one by one, as the next group's rows follow.
 //  * dense tiles are walked with a fixed stride, the plan's tiles claimed in order (tcgen05.cuh).
 // What bounds it: L2's feed of the stages (32 KB a CTA for 64 of the depth, 15 TB/s over the GPU) while the
-// clock is high, power in long products.  Measured: 65536 x 7168 x 4096 of swiglu with bias and z 2231 us
-// (1.72 PFLOP/s), 8192 rows 272 us (1.76), its gradients at 32768 rows 2348 us together.
+// clock is high, power in long products.  Measured: 65536 x 7168 x 4096 of swiglu with bias and z 2231 to
+// 2314 us (1.72 to 1.66 PFLOP/s), 8192 rows 257 us with pauses between the calls and 292 without (1.87 and
+// 1.65), the gradients at 32768 rows 2282 to 2348 us together.
 #include <algorithm>
 #include <type_traits>
 
@@ -398,7 +399,7 @@ k_product(const __grid_constant__ ProductMaps tm, const __grid_constant__ Produc
         const uint32_t bytes = Cfg::kABytes + (BMN ? panels : Cfg::kBPanels) * kPanelBytes;
         // Input gradient: row tiles begin at other blocks of the depth, so that the pairs that read one
         // panel of w, whose rows lie 2 N bytes apart, do not do so at the same moment (8192 x 7168 x
-        // 4096: 284 -> 262 us).  The products along N-major panels are faster in step (271 and 280).
+        // 4096: 284 -> 270 us).  The products along N-major panels are faster in step (271 and 280).
         const int turn = KIND == kInputGrad ? (int)((unsigned)(mt.row0 / Cfg::kTileM) * 7u % (unsigned)KB) : 0;
         for (int kb = 0; kb < KB; ++kb) {
           if (!mbar_wait(empty(stage), phase ^ 1u, abort_flag)) { ok = false; break; }

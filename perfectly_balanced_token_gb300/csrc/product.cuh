@@ -14,7 +14,9 @@ constexpr int kPanelBytes = 64 * 128;  // 64 rows of 64 bf16
 // Blocks of the depth that one accumulator sums where C is fp32.  The instruction cuts off what its
 // fp32 sums do not hold, always towards zero, so a long sum drifts: against 64 bits, with the whole
 // depth in one accumulator, 7e-6 of C at a depth of 7168 and past 2e-5 at 32768.  The epilogues add
-// the parts in registers, rounding to nearest.  (A bf16 C's own rounding is 250 times larger.)
+// the parts in registers, rounding to nearest.  (A bf16 C's own rounding is 250 times larger, and it keeps one
+// accumulator: at a depth of 7168 0.44 % of its values are the neighbour of the one nearest to the 64-bit
+// sum, 0.06 % with sums rounded to nearest, and its distance from 64 bits is 0.165854 % and 0.165852 %.)
 constexpr int kPartBlocks = 12;
 
 enum Kind { kForward, kInputGrad, kWeightGrad };

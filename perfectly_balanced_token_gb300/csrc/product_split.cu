@@ -11,7 +11,7 @@
 // 4864 x 1664 of swiglu: 33 us with tiles of one CTA, 9.7 so).
 // What bounds it: at few rows reading w once (all of it is in flight over the multiprocessors'
 // rings at any time), towards 256 rows a tile the rate at which L2 feeds the rings.  Measured: 1 x 7168
-// x 4096 of swiglu 13.1 us (58.7 MB: 8.8 us at the copy's rate), 256 rows 18.9, 1024 x 7168 x 2048 27
+// x 4096 of swiglu 13.4 us (58.7 MB: 8.8 us at the copy's rate), 256 rows 18.9, 1024 x 7168 x 2048 27
 // (pair tiles: 37), 100 x 512 x 4096 4.9; and between the smallest kernels of a chain 2.9 us.
 #include <algorithm>
 #include <cmath>
