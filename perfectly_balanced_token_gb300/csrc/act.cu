@@ -167,7 +167,7 @@ k_act_backward(ActArgs a, PlanPtrs p, int plan) {
 }
 
 // d_bias[c] (+)= sum over chunks of sums[chunk][c]: 32 columns a block, 32 threads a column
-__global__ void __launch_bounds__(1024) k_sum_chunks(const float* __restrict__ sums, int64_t chunks,
+__global__ void __launch_bounds__(1024) k_sum_chunks(const float* sums, int64_t chunks,
                                                      int cols, float* __restrict__ d_bias, int add) {
   __shared__ float part[32][33];
   grid_wait();
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(1024) k_sum_chunks(const float* __restrict__ s
 // expert's tiles out of the plan's list, 1024 at a time and in order, and adds their rows of sums.
 constexpr int kPickThreads = 1024;
 __global__ void __launch_bounds__(kPickThreads)
-k_sum_tiles(PlanPtrs p, const float* __restrict__ sums, int cols, float* __restrict__ d_bias, int add) {
+k_sum_tiles(PlanPtrs p, const float* sums, int cols, float* __restrict__ d_bias, int add) {
   __shared__ int picked[kPickThreads];
   __shared__ int count[kPickThreads / 32];
   grid_wait();

@@ -18,8 +18,8 @@ namespace moonep {
 struct Philox {
   uint32_t k0, k1, o0, o1;
   __device__ __forceinline__ explicit Philox(const int64_t* rng) {
-    const uint64_t seed = (uint64_t)__ldg(reinterpret_cast<const long long*>(rng));
-    const uint64_t offset = (uint64_t)__ldg(reinterpret_cast<const long long*>(rng) + 1);
+    const uint64_t seed = (uint64_t)rng[0];
+    const uint64_t offset = (uint64_t)rng[1];
     k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
     o0 = (uint32_t)offset, o1 = (uint32_t)(offset >> 32);
   }
@@ -52,10 +52,14 @@ constexpr int kRowThreads = 128;
 
 // out[t] = bf16( residual[t] + dropout( sum over k ascending of gates[t][k] y[dst[t][k]] ) )
 // `lanes` threads (a power of two) take a token, so that short rows leave none of a block without work.
-template <int KC, bool DROP, bool RES>
-__global__ void __launch_bounds__(kRowThreads)
-k_combine_dropout(Dims d, PlanPtrs p, const uint4* __restrict__ y, const float* __restrict__ gates,
-                  const uint4* __restrict__ residual, uint4* __restrict__ out, Dropout drop, int lanes) {
+// Four copies are in flight in a thread, eight blocks a multiprocessor: with eight copies fewer blocks fit
+// (32768 x 8 x 7168 with residual: 732 us and 700 with four, without dropout 715 and 693).
+constexpr int kCopies = 4;
+
+template <bool DROP, bool RES>
+__global__ void __launch_bounds__(kRowThreads, 8)
+k_combine_dropout(Dims d, PlanPtrs p, const uint4* y, const float* gates,
+                  const uint4* residual, uint4* __restrict__ out, Dropout drop, int lanes) {
   grid_wait();
   grid_trigger();
   if (plan_failed(p.status)) return;
@@ -72,20 +76,20 @@ k_combine_dropout(Dims d, PlanPtrs p, const uint4* __restrict__ y, const float* 
 #pragma unroll
       for (int i = 0; i < 8; ++i) acc[i] = 0.f;
       uint32_t random[4];
-      for (int k0 = 0; k0 < d.K; k0 += KC) {
-        uint4 v[KC];
-        float g[KC];
+      for (int k0 = 0; k0 < d.K; k0 += kCopies) {
+        uint4 v[kCopies];
+        float g[kCopies];
 #pragma unroll
-        for (int k = 0; k < KC; ++k) {
+        for (int k = 0; k < kCopies; ++k) {
           if (k0 + k < d.K) {
-            v[k] = __ldcs(y + (size_t)__ldg(dt + k0 + k) * hv + a);
-            g[k] = __ldg(gt + k0 + k);
+            v[k] = __ldcs(y + (size_t)dt[k0 + k] * hv + a);
+            g[k] = gt[k0 + k];
           }
         }
         // (drawn while the first copies are on their way)
         if (DROP && k0 == 0) Philox(drop.rng).numbers((uint64_t)t * hv + a, random);
 #pragma unroll
-        for (int k = 0; k < KC; ++k)
+        for (int k = 0; k < kCopies; ++k)
           if (k0 + k < d.K) {
             float f[8];
             unpack8(f, v[k]);
@@ -138,10 +142,19 @@ __device__ __forceinline__ float drop_alone(const uint4* y, const uint4* dout, u
   return dot;
 }
 
+// Blocks a multiprocessor: as many as the vectors in flight leave registers for.  (Left to itself the
+// compiler takes 96 registers and spills where 128 threads share a token of four vectors each: 32768 x 8 x
+// 4096 718 us and 667 with four blocks; and 128 without dropout where a warp does: 8192 x 2 x 1024 10.5 and 9.5.)
+constexpr int back_blocks(int team, int vpt, int kc, bool drop) {
+  if (vpt * kc == 4) return 8;
+  if (vpt == 4) return team == 32 && !drop ? 5 : 4;
+  return vpt == 2 ? 5 : 4;
+}
+
 template <int TEAM, int VPT, int KC, bool DROP>
-__global__ void __launch_bounds__(kRowThreads)
-k_combine_dropout_bwd(Dims d, PlanPtrs p, const uint4* __restrict__ y,
-                      const float* __restrict__ gates, const uint4* __restrict__ dout,
+__global__ void __launch_bounds__(kRowThreads, back_blocks(TEAM, VPT, KC, DROP))
+k_combine_dropout_bwd(Dims d, PlanPtrs p, const uint4* y,
+                      const float* gates, const uint4* dout,
                       uint4* __restrict__ dy, float* __restrict__ dgates, Dropout drop) {
   static_assert(TEAM == 32 || TEAM == kRowThreads, "threads of a token");
   __shared__ float part[TEAM / 32][TEAM == 32 ? 1 : kDropMaxK];
@@ -161,8 +174,8 @@ k_combine_dropout_bwd(Dims d, PlanPtrs p, const uint4* __restrict__ y,
     auto load = [&](int k0) {  // copies k0 .. of the token
 #pragma unroll
       for (int k = 0; k < KC; ++k) {
-        row[k] = k0 + k < d.K ? (size_t)__ldg(dt + k0 + k) : 0;
-        g[k] = k0 + k < d.K ? __ldg(gt + k0 + k) : 0.f;
+        row[k] = k0 + k < d.K ? (size_t)dt[k0 + k] : 0;
+        g[k] = k0 + k < d.K ? gt[k0 + k] : 0.f;
       }
 #pragma unroll
       for (int k = 0; k < KC; ++k)
@@ -234,8 +247,8 @@ k_combine_dropout_bwd(Dims d, PlanPtrs p, const uint4* __restrict__ y,
       // element by element (finite ones pay two instructions a copy for it)
 #pragma unroll 1
       for (int k = 0; k < d.K; ++k) {
-        const size_t at = (size_t)__ldg(dt + k) * hv;
-        float sum = drop_alone<TEAM>(y + at, dout + (size_t)t * hv, dy + at, __ldg(gt + k), hv, (uint64_t)t * hv,
+        const size_t at = (size_t)dt[k] * hv;
+        float sum = drop_alone<TEAM>(y + at, dout + (size_t)t * hv, dy + at, gt[k], hv, (uint64_t)t * hv,
                                      drop);
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
@@ -271,11 +284,8 @@ cudaError_t launch_combine_dropout(const Dims& d, const PlanPtrs& p, const void*
                      (const uint4*)residual, (uint4*)out, drop, lanes);
   };
   const bool r = residual != nullptr;
-  // Copies in flight in a thread: eight, but four beside the random numbers, whose registers would
-  // otherwise cost blocks (32768 x 8 x 7168 with residual: 732 us with eight and 696 with four).
-  if (drop.cut) r ? go(k_combine_dropout<4, true, true>) : go(k_combine_dropout<4, true, false>);
-  else if (d.K >= 8) r ? go(k_combine_dropout<8, false, true>) : go(k_combine_dropout<8, false, false>);
-  else r ? go(k_combine_dropout<4, false, true>) : go(k_combine_dropout<4, false, false>);
+  if (drop.cut) r ? go(k_combine_dropout<true, true>) : go(k_combine_dropout<true, false>);
+  else r ? go(k_combine_dropout<false, true>) : go(k_combine_dropout<false, false>);
   *launches += 1;
   return e;
 }

@@ -3,7 +3,9 @@
 // their writes are there; grid_trigger() lets the next kernel begin in the same way.  Measured between
 // dependent kernels of a CUDA graph: 1.6 us less for each.
 // Every thread of a kernel launched with launch_after() calls grid_wait() before it touches global
-// memory.  (Without that, the kernel after it could run before the one in front of it has ended.)
+// memory.  (Without that, the kernel after it could run before the one in front of it has ended.)  What it
+// then reads may have been written since it began, so it is read by ordinary loads, never by non-coherent
+// ones (__ldg, or a parameter that is const and __restrict__).
 #pragma once
 
 #include <cuda_runtime.h>

@@ -158,7 +158,7 @@ __device__ __forceinline__ void add_bias(float (&v)[32], const float* bias, int 
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     if (4 * j < cols) {
-      const float4 f = __ldg(b + j);
+      const float4 f = b[j];
       v[4 * j] += f.x;
       v[4 * j + 1] += f.y;
       v[4 * j + 2] += f.z;
@@ -172,7 +172,7 @@ __device__ __forceinline__ void add_residual(float (&v)[32], const uint16_t* at,
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     if (8 * j < cols) {
-      const uint4 r = __ldg(p + j);
+      const uint4 r = p[j];
       const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {

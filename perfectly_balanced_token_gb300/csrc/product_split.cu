@@ -248,8 +248,8 @@ k_product_split(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
       if (biased) {
         const float* from = a.bias + x;
         if (GROUPED) from += (size_t)(expert >= 0 ? expert : p.slot_expert[-1 - expert]) * a.columns;
-        bias = __ldg(reinterpret_cast<const float2*>(from));
-        if (a.half) bias_up = __ldg(reinterpret_cast<const float2*>(from + a.half));
+        bias = *reinterpret_cast<const float2*>(from);
+        if (a.half) bias_up = *reinterpret_cast<const float2*>(from + a.half);
       }
       auto get = [&](float (&to)[2][4], int at, float2 b) {
         const float4 p = add_parts(sums + at, stride, S), q = add_parts(sums + at + 1, stride, S);
@@ -279,7 +279,7 @@ k_product_split(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
             const uint16_t* r = a.residual + at;
 #pragma unroll
             for (int j = 0; j < 4; ++j, r += ncols)
-              if (j < left) res[j] = __ldg(reinterpret_cast<const uint32_t*>(r));
+              if (j < left) res[j] = *reinterpret_cast<const uint32_t*>(r);
           }
           if (a.z != nullptr) put(a.z + at_z, a.columns, v);
           if (a.half) {

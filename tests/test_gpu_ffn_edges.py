@@ -149,3 +149,67 @@ def test_deep_products(T, N, f32):
     e = (768 * 2.0 ** -23 + K / 768 * 2.0 ** -24) * size if f32 else K * 2.0 ** -23 * size
     bound = e if f32 else e + 2.0 ** -8 * (want.abs() + e)
     assert bool(((out.double() - want).abs() <= bound).all()) and int(st) == 0
+
+
+@pytest.mark.parametrize("T,N", [(300, 512), (2049, 2056)])
+@pytest.mark.parametrize("graph", [False, True])
+def test_what_the_launch_before_wrote_is_read(T, N, graph):
+    # Every call reads, by ordinary loads, a buffer that the launch right before it wrote (bias sums from
+    # scratch, a bias, a residual, gates, y), and that held other values one step earlier.
+    K, E = 72, 8
+    w, wg = syn.normal_bf16((K, N), 0.1, 2).cuda(), syn.normal_bf16((K, E), 0.1, 3).cuda()
+    xs = [syn.normal_bf16((T, K), 1.0, 10 + i).cuda() for i in range(2)]
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ld, lg = mx.linear_dims(T, K, N), mx.linear_dims(T, K, E, out_dtype=F32)
+    z, res, d_z = (torch.empty(T, N, dtype=BF16, device="cuda") for _ in range(3))
+    bias, gates = torch.empty(N, device="cuda"), torch.empty(T, E, device="cuda")
+    scratch = torch.empty(mx.moonep_act_backward_workspace_bytes(T, N), dtype=torch.uint8, device="cuda")
+    Hp = 64 * (N // 64)
+    d = mx.dims(1, E, 0, E, T, 64, Hp, 1)
+    ws = mx.PlanWorkspace(d)
+    mx.moonep_plan(d, torch.arange(E, device="cuda", dtype=torch.int32).repeat(T), ws.buf)
+    y, l_y = torch.empty(T * E, Hp, dtype=BF16, device="cuda"), mx.linear_dims(T * E, K, Hp)
+    ys = [syn.normal_bf16((T * E, K), 1.0, 20 + i).cuda() for i in range(2)]
+    wy = syn.normal_bf16((K, Hp), 0.1, 4).cuda()
+    rng = torch.tensor([1, 2], device="cuda")
+
+    def outputs():
+        return (torch.empty(T, N, dtype=BF16, device="cuda"), torch.empty(N, device="cuda"),
+                torch.empty(T, N, dtype=BF16, device="cuda"), torch.empty(T, Hp, dtype=BF16, device="cuda"),
+                torch.empty(T * E, Hp, dtype=BF16, device="cuda"), torch.empty(T, E, device="cuda"))
+
+    def step(i, o, wait=lambda: None):
+        x = xs[i % 2]
+        for call in (lambda: mx.moonep_linear(ld, x, w, z, st),
+                     lambda: mx.moonep_act_backward(z, z, d_z, act="silu", d_bias=bias, scratch=scratch),
+                     lambda: mx.moonep_linear(ld, x, w, res, st, bias=bias),
+                     lambda: mx.moonep_linear(ld, x, w, o[0], st, residual=res),
+                     lambda: mx.moonep_act_backward(o[0], res, o[2], act="gelu", d_bias=o[1], scratch=scratch),
+                     lambda: mx.moonep_linear(l_y, ys[i % 2], wy, y, st),
+                     lambda: mx.moonep_linear(lg, x, wg, gates, st),
+                     lambda: mx.moonep_combine_dropout(d, ws.buf, y, gates, o[3], residual=y[:T], p=0.25, rng=rng),
+                     lambda: mx.moonep_combine_dropout_backward(d, ws.buf, y, gates, o[3], o[4], o[5], p=0.25,
+                                                                rng=rng)):
+            call()
+            wait()
+
+    alone = [outputs() for _ in range(2)]
+    for i in range(2):
+        step(i, alone[i], torch.cuda.synchronize)
+    got = [outputs() for _ in range(10)]
+    run = lambda: [step(i, o) for i, o in enumerate(got)]  # noqa: E731
+    if graph:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run()
+        run = g.replay
+    for _ in range(5):
+        for o in got:
+            for t in o:
+                t.fill_(float("nan"))
+        run()
+        torch.cuda.synchronize()
+        for i, o in enumerate(got):
+            for a, b in zip(o, alone[i % 2]):
+                assert torch.equal(a, b), i
+    assert int(st) == 0 and not torch.equal(alone[0][1], alone[1][1])
